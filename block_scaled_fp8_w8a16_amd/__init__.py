@@ -10,6 +10,10 @@ library has not been built, every call raises -- there is no fallback.
 A is BF16 [m, k] (any row pitch that is a multiple of 8), W is FP8 E4M3
 [n, k] (torch.float8_e4m3fn or its uint8 bytes), S is float32
 [ceil(n/128), k/128], C is BF16 [m, n] (any row pitch >= n).
+
+Beside it: FP8 activations and the W8A8 GEMM, the W4A4 MX GEMV, and what a
+decoder layer does between its projections (rotary positions, a paged FP8
+cache and attention over it: see ``attention.py``).
 """
 
 from __future__ import annotations
@@ -17,6 +21,10 @@ from __future__ import annotations
 import ctypes
 import os
 from typing import Optional
+
+from . import attention as _attention
+from .attention import (KV_BLOCK, KV_KERNEL_ROWS, KVCache, KVPlan, kv_append, kv_attention, kv_cache,
+                        plan_kv_attention, rope, rope_table)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libw8a16.so")
@@ -32,6 +40,7 @@ ERR_BAD_PLAN = 7
 ERR_HIP = 8
 ERR_WORKSPACE = 9
 ERR_ENV = 10
+ERR_SHAPE = 11
 
 KERNEL_STREAM = 1
 KERNEL_TILE = 2
@@ -49,7 +58,9 @@ EXPORTS = ("w8a16_check_args", "w8a16_plan", "w8a16_plan_finalize", "w8a16_gemm"
            "w8a16_gemm_planned", "w8a16_gemm_noalloc", "w8a16_plan_batched", "w8a16_gemm_batched",
            "w8a16_act_quant_fp8", "w8a16_plan_w8a8", "w8a16_gemm_w8a8",
            "w8a16_gemm_w8a8_planned", "w8a16_gemm_w4a4", "w8a16_plan_w4a4",
-           "w8a16_gemm_w4a4_planned", "w8a16_status_string", "w8a16_last_error")
+           "w8a16_gemm_w4a4_planned", "w8a16_rope_table", "w8a16_rope", "w8a16_kv_append",
+           "w8a16_kv_attention", "w8a16_plan_kv_attention", "w8a16_status_string",
+           "w8a16_last_error")
 
 MAX_BATCH = 8
 
@@ -132,6 +143,7 @@ def library() -> ctypes.CDLL:
         lib.w8a16_gemm_w4a4_planned.argtypes = [vp, u32, vp, vp, vp, vp, u32, u32, u32, u32,
                                                 ctypes.POINTER(Plan), vp]
         lib.w8a16_gemm_w4a4_planned.restype = ctypes.c_int
+        _attention.declare(lib)
         lib.w8a16_status_string.argtypes = [ctypes.c_int]
         lib.w8a16_status_string.restype = ctypes.c_char_p
         lib.w8a16_last_error.argtypes = []

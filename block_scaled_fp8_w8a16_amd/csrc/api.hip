@@ -17,22 +17,13 @@
 #include <utility>
 #include <vector>
 
+#include "host.h"
 #include "kernels.h"
 #include "plan.h"
 
 namespace w8a16 {
 
 namespace {
-
-// Split-K workspace and arrival counters of one (device, stream).  The
-// counters are zeroed once at allocation; every kernel that uses them
-// leaves them at zero again.
-struct Workspace {
-    float *ws = nullptr;
-    uint64_t ws_bytes = 0;
-    uint32_t *counters = nullptr;
-    uint32_t counter_count = 0;
-};
 
 std::mutex g_ws_mutex;
 std::map<std::pair<int, hipStream_t>, Workspace> g_ws;
@@ -44,12 +35,16 @@ std::vector<void *> g_retired;
 std::mutex g_cu_mutex;
 std::map<int, uint32_t> g_cu_count;
 
+}  // namespace
+
 int hip_fail(hipError_t e, const char *what)
 {
     char buf[256];
     snprintf(buf, sizeof buf, "w8a16_gemm: %s failed: %s", what, hipGetErrorString(e));
     return fail(W8A16_ERR_HIP, buf);
 }
+
+namespace {
 
 // ---- diagnostics ---------------------------------------------------------
 // W8A16_LOG (print each distinct launch and its plan once) and
@@ -89,6 +84,10 @@ const Levers &levers()
     return l;
 }
 
+}  // namespace
+
+bool log_enabled() { return levers().log; }
+
 int check_levers(const char *entry)
 {
     const Levers &l = levers();
@@ -98,6 +97,8 @@ int check_levers(const char *entry)
     snprintf(buf, sizeof buf, "%s: %s", entry, l.msg);
     return fail(l.status, buf);
 }
+
+namespace {
 
 const char *kernel_name(uint32_t kernel)
 {
@@ -115,6 +116,8 @@ const char *kernel_name(uint32_t kernel)
 std::mutex g_log_mutex;
 std::set<std::string> g_logged;   // lines already printed (at most 4096 kept)
 
+}  // namespace
+
 void log_line(const char *line)
 {
     std::lock_guard<std::mutex> lock(g_log_mutex);
@@ -122,6 +125,8 @@ void log_line(const char *line)
         return;
     std::fputs(line, stderr);
 }
+
+namespace {
 
 // Under W8A16_LOG=1: the launch of `entry` with plan `p`; `why` is the
 // planner's reason, or null for a caller's plan.
@@ -141,6 +146,8 @@ void log_plan(const char *entry, uint32_t m, uint32_t n, uint32_t k, const w8a16
              why ? why : "caller's plan");
     log_line(line);
 }
+
+}  // namespace
 
 // Success epilogue of a call that enqueued work: clears the last error and,
 // under W8A16_DEBUG_SYNC=1, waits for the stream (unless it is being
@@ -238,6 +245,8 @@ int get_workspace(int dev, hipStream_t stream, const w8a16_plan_t &plan, Workspa
     *out = w;
     return W8A16_OK;
 }
+
+namespace {
 
 // ---- scratch of w8a16_gemm_noalloc ---------------------------------------
 // One static device array per GPU (each device holds its own copy of the

@@ -1,0 +1,102 @@
+// Kernel arguments and launch interface of the attention operators (rotary
+// positions, paged FP8 cache, attention over it).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "w8a16.h"
+
+namespace w8a16 {
+
+// Division of n < 2^31 by a constant d >= 1: with s = ceil(log2 d) and
+// mul = ceil(2^(31 + s) / d), n * mul >> (31 + s) is floor(n / d).
+struct FastDiv {
+    uint32_t d = 1, mul = 1u << 31, shift = 31;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t div) : d(div)
+    {
+        uint32_t s = 0;
+        while (s < 31 && (1u << s) < div)
+            ++s;
+        shift = 31 + s;
+        mul = (uint32_t)((((uint64_t)1 << shift) + div - 1) / div);
+    }
+    __host__ __device__ uint32_t div(uint32_t n) const
+    {
+        return (uint32_t)(((uint64_t)n * mul) >> shift);
+    }
+};
+
+// One token row of a rotation: `pair_items` items of P pairs, then
+// `pass_items` items of 2P unrotated elements.
+struct RopeRows {
+    const uint8_t *x;
+    uint8_t *y;
+    int64_t x_token, x_head, y_token, y_head;   // strides in elements
+    const float *table;
+    uint32_t table_positions, rot, dim, half;   // half: pairs are i and i + rot/2
+    uint32_t heads, pair_items, items;          // items per head
+    FastDiv by_items;                           // items per head
+    uint32_t pairs;                             // P: pairs per item (1, 4 or 8)
+};
+
+struct RopeArgs {
+    RopeRows r;
+    const int32_t *positions;
+    uint32_t total;                             // tokens * heads * items
+    FastDiv by_row;                             // heads * items
+    uint32_t inverse;
+};
+
+struct KvPool {
+    uint8_t *k, *v, *k_scale, *v_scale;
+    uint64_t k_page, v_page, ks_page, vs_page;  // page strides in bytes
+    uint32_t pages, heads, dim, blocks;         // blocks of 16 tokens per page
+    FastDiv by_blocks;
+};
+
+struct KvSeqs {
+    const int32_t *block_table, *kv_lens, *cu;
+    uint32_t bt_stride, bt_width, seqs, tokens, uniform;   // uniform: tokens per sequence without cu
+    FastDiv by_uniform;
+};
+
+struct AppendArgs {
+    KvPool pool;
+    KvSeqs seqs;
+    const uint8_t *k, *v;
+    int64_t k_token, k_head, v_token, v_head;
+    uint32_t vec;              // rows are 16-byte aligned and rotate in whole 8-element chunks
+    uint32_t seq_blocks;       // blocks a sequence's new tokens may touch
+    uint32_t kv_groups;        // workgroups of the append; the rest rotate queries
+    FastDiv by_units, by_seq_units;
+    RopeRows q;                // q.x null: no queries
+    uint32_t q_groups;         // workgroups per token of the queries
+    FastDiv by_q_groups;
+};
+
+struct AttnArgs {
+    KvPool pool;
+    KvSeqs seqs;
+    const uint8_t *q;
+    uint8_t *out;
+    float *lse, *ws;
+    int64_t q_token, q_head, out_token, out_head;
+    float scale_log2;          // scale * log2(e)
+    uint32_t group;            // query heads per KV head
+    FastDiv by_group;
+    uint32_t q_heads, causal, window;
+    uint32_t row_tiles, chunks, chunk_tiles;
+};
+
+constexpr uint32_t kKvTile = 64;                // keys per tile
+
+hipError_t launch_rope_table(const w8a16_rope_config_t &c, float *table, uint32_t positions,
+                             uint32_t rot_dim, hipStream_t stream);
+hipError_t launch_rope(const RopeArgs &a, uint32_t dtype, hipStream_t stream);
+hipError_t launch_kv_append(const AppendArgs &a, uint32_t dtype, hipStream_t stream);
+hipError_t launch_kv_rows(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t dtype,
+                          hipStream_t stream);
+
+}  // namespace w8a16

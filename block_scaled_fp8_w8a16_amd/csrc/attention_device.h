@@ -1,0 +1,147 @@
+// Device pieces shared by the attention kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "attention.h"
+#include "device_common.h"
+
+namespace w8a16 {
+namespace dev {
+
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+
+constexpr float kNegInf = -__builtin_inff();
+
+// Query types: K codes are widened to the query's type with scale 1, which
+// is exact for both (E4M3 spans 2^-9 .. 448), so the products see the query
+// unrounded; the block's scale multiplies the FP32 sums.
+template <bool HI>
+__device__ __forceinline__ uint32_t f16_pair_from_fp8(uint32_t raw, float scale)
+{
+    auto v = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(raw, scale, HI);
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+__device__ __forceinline__ u32x4_t f16_from_fp8x8(uint32_t a, uint32_t b, float scale)
+{
+    u32x4_t r;
+    r.x = f16_pair_from_fp8<false>(a, scale);
+    r.y = f16_pair_from_fp8<true>(a, scale);
+    r.z = f16_pair_from_fp8<false>(b, scale);
+    r.w = f16_pair_from_fp8<true>(b, scale);
+    return r;
+}
+
+struct QueryBf16 {
+    typedef __bf16 elem;
+    static __device__ __forceinline__ u32x4_t widen(uint32_t a, uint32_t b)
+    {
+        u32x4_t r;
+        r.x = bf16_pair_from_fp8<false>(a);
+        r.y = bf16_pair_from_fp8<true>(a);
+        r.z = bf16_pair_from_fp8<false>(b);
+        r.w = bf16_pair_from_fp8<true>(b);
+        return r;
+    }
+    static __device__ __forceinline__ f32x4_t mfma16(u32x4_t k, u32x4_t q, f32x4_t c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, k),
+                                                       __builtin_bit_cast(bf16x8_t, q), c, 0, 0, 0);
+    }
+};
+
+struct QueryF16 {
+    typedef _Float16 elem;
+    static __device__ __forceinline__ u32x4_t widen(uint32_t a, uint32_t b)
+    {
+        return f16_from_fp8x8(a, b, 1.0f);
+    }
+    static __device__ __forceinline__ f32x4_t mfma16(u32x4_t k, u32x4_t q, f32x4_t c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, k),
+                                                      __builtin_bit_cast(f16x8_t, q), c, 0, 0, 0);
+    }
+};
+
+__device__ __forceinline__ f32x4_t mfma16_f16(u32x4_t a, u32x4_t b, f32x4_t c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a),
+                                                  __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ uint32_t f16_pair(float a, float b)
+{
+    f16x2_t v = {static_cast<_Float16>(a), static_cast<_Float16>(b)};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
+// 2^x of the hardware (within 1 ulp); 2^-inf is 0.
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ float pow2_byte(uint32_t byte)     // 2^(byte - 127), bytes 1..254
+{
+    return __builtin_bit_cast(float, byte << 23);
+}
+
+// 0x80 in each byte of w whose code is NaN (0x7f or 0xff).
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w)
+{
+    return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+}
+
+// What one workgroup knows about its sequence and rows.
+struct RowTile {
+    uint32_t first, count;       // the sequence's new tokens
+    int32_t kv_len, base;        // tokens held; position of new token 0
+    uint32_t rows, row0;         // rows (token * group + head) of the sequence; first of the tile
+    int32_t lo, hi;              // keys some row of the tile may see: [lo, hi)
+    int32_t all_lo, all_hi;      // keys every row of the tile sees: [all_lo, all_hi)
+};
+
+// Sequence b's extent; false if its offsets do not lie in the token axis.
+__device__ __forceinline__ bool seq_extent(const KvSeqs &s, uint32_t b, RowTile &t)
+{
+    t.first = b * s.uniform;
+    uint32_t end = t.first + s.uniform;
+    if (s.cu) {
+        t.first = (uint32_t)s.cu[b];
+        end = (uint32_t)s.cu[b + 1];
+        if (t.first > s.tokens || end > s.tokens || end < t.first)
+            return false;
+    }
+    t.count = end - t.first;
+    t.kv_len = s.kv_lens[b];
+    t.base = t.kv_len - (int32_t)t.count;
+    return true;
+}
+
+__device__ __forceinline__ void tile_range(const AttnArgs &a, uint32_t tile_rows, RowTile &t)
+{
+    const uint32_t last = t.row0 + tile_rows < t.rows ? t.row0 + tile_rows : t.rows;
+    const int32_t p0 = t.base + (int32_t)a.by_group.div(t.row0);
+    const int32_t p1 = t.base + (int32_t)a.by_group.div(last - 1);
+    t.hi = a.causal ? (p1 + 1 < t.kv_len ? p1 + 1 : t.kv_len) : t.kv_len;
+    if (p1 < 0)
+        t.hi = 0;      // rows of no sequence see nothing
+    t.lo = 0;
+    if (a.window && p0 >= (int32_t)a.window)
+        t.lo = p0 - (int32_t)a.window + 1;
+    t.hi = t.hi > t.lo ? t.hi : t.lo;
+    t.all_lo = a.window && p1 >= (int32_t)a.window ? p1 - (int32_t)a.window + 1 : 0;
+    t.all_hi = p0 < 0 ? 0 : (a.causal && p0 + 1 < t.kv_len ? p0 + 1 : t.kv_len);
+}
+
+// Keys row `row` sees: [lo, hi).
+__device__ __forceinline__ void row_range(const AttnArgs &a, const RowTile &t, uint32_t row,
+                                          int32_t &lo, int32_t &hi)
+{
+    const int32_t p = t.base + (int32_t)a.by_group.div(row);
+    hi = row < t.rows && p >= 0 ? (a.causal && p + 1 < t.kv_len ? p + 1 : t.kv_len) : 0;
+    lo = a.window && p >= (int32_t)a.window ? p - (int32_t)a.window + 1 : 0;
+}
+
+}  // namespace dev
+}  // namespace w8a16

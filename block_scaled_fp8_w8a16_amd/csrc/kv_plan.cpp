@@ -1,0 +1,98 @@
+// Launch plans of the cache attention.  Pure host code with no HIP
+// dependency, like the GEMM planner.
+
+#include <cstdio>
+#include <cstring>
+
+#include "plan.h"
+
+namespace w8a16 {
+
+namespace {
+
+constexpr uint64_t kKeysPerTile = 64;
+
+uint64_t div_up(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+// Fills the derived fields of a plan whose kernel, row_blocks and
+// chunk_tiles are set, or refuses it.
+int kv_plan_finalize(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_heads,
+                     uint32_t kv_heads, uint32_t head_dim, uint32_t window, w8a16_kv_plan_t *p)
+{
+    if (p->kernel != W8A16_KV_ROWS || p->row_blocks < 1 || p->row_blocks > 2 || p->chunk_tiles < 1)
+        return fail(W8A16_ERR_BAD_PLAN, "w8a16_kv_attention: plan needs kernel W8A16_KV_ROWS, "
+                                        "row_blocks 1 or 2 and chunk_tiles of at least 1");
+    // the tiles a row tile can see: all of the cache, or the window's and
+    // those its rows' positions add
+    const uint64_t tile_rows = 16ull * p->row_blocks, rows = (uint64_t)max_new * (q_heads / kv_heads);
+    uint64_t keys = max_kv;
+    if (window && (uint64_t)window + max_new < keys)
+        keys = (uint64_t)window + max_new;
+    uint64_t tiles = div_up(keys, kKeysPerTile) + (window ? 1 : 0);
+    if (tiles < 1)
+        tiles = 1;
+    const uint64_t row_tiles = div_up(rows, tile_rows), chunks = div_up(tiles, p->chunk_tiles);
+    const uint64_t grid = (uint64_t)seqs * kv_heads * row_tiles * chunks;
+    if (grid >= (1ull << 31))
+        return fail(W8A16_ERR_SHAPE, "w8a16_kv_attention: too many workgroups (2^31) for one call");
+    p->row_tiles = (uint32_t)row_tiles;
+    p->chunks = (uint32_t)chunks;
+    p->grid = (uint32_t)grid;
+    p->workspace_bytes = chunks > 1 ? grid * tile_rows * (head_dim + 4) * 4 : 0;
+    return W8A16_OK;
+}
+
+int make_kv_plan(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_heads,
+                 uint32_t kv_heads, uint32_t head_dim, uint32_t window, uint32_t cu_count,
+                 w8a16_kv_plan_t *out)
+{
+    if (!out)
+        return fail(W8A16_ERR_NULL_PTR, "w8a16_plan_kv_attention: null plan");
+    if (!seqs || !max_new || !q_heads || !kv_heads || q_heads % kv_heads || head_dim < 16 ||
+        head_dim > W8A16_KV_MAX_HEAD_DIM || head_dim % 16 || max_kv > (1u << 30)) {
+        char buf[224];
+        snprintf(buf, sizeof buf,
+                 "w8a16_plan_kv_attention: seqs=%u max_new=%u max_kv=%u q_heads=%u kv_heads=%u "
+                 "head_dim=%u is not a shape the attention takes",
+                 seqs, max_new, max_kv, q_heads, kv_heads, head_dim);
+        return fail(W8A16_ERR_SHAPE, buf);
+    }
+    const uint64_t cus = cu_count ? cu_count : kDefaultCUs;
+    w8a16_kv_plan_t p;
+    std::memset(&p, 0, sizeof p);
+    p.kernel = W8A16_KV_ROWS;
+    const uint64_t rows = (uint64_t)max_new * (q_heads / kv_heads);
+    p.row_blocks = rows <= 16 ? 1 : 2;
+    // two workgroups fit a CU; cut the keys until there are four for each,
+    // but leave every wave two tiles
+    p.chunk_tiles = 1u << 30;
+    int st = kv_plan_finalize(seqs, max_new, max_kv, q_heads, kv_heads, head_dim, window, &p);
+    if (st != W8A16_OK)
+        return st;
+    uint64_t tiles = div_up(window && (uint64_t)window + max_new < max_kv
+                                ? (uint64_t)window + max_new : max_kv, kKeysPerTile) + (window ? 1 : 0);
+    if (tiles < 1)
+        tiles = 1;
+    const uint64_t want = div_up(4 * cus, p.grid);
+    uint64_t per = div_up(tiles, want);
+    if (per < 8)
+        per = 8;
+    p.chunk_tiles = (uint32_t)per;
+    st = kv_plan_finalize(seqs, max_new, max_kv, q_heads, kv_heads, head_dim, window, &p);
+    if (st != W8A16_OK)
+        return st;
+    *out = p;
+    return W8A16_OK;
+}
+
+}  // namespace w8a16
+
+extern "C" int w8a16_plan_kv_attention(uint32_t seqs, uint32_t max_new, uint32_t max_kv,
+                                       uint32_t q_heads, uint32_t kv_heads, uint32_t head_dim,
+                                       uint32_t window, uint32_t cu_count, w8a16_kv_plan_t *out)
+{
+    return w8a16::make_kv_plan(seqs, max_new, max_kv, q_heads, kv_heads, head_dim, window, cu_count,
+                               out);
+}

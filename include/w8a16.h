@@ -67,14 +67,17 @@ typedef enum w8a16_status {
     W8A16_ERR_WORKSPACE = 9,         /* the plan's split-K workspace cannot be provided:
                                         it would have to grow during stream capture,
                                         or it exceeds w8a16_gemm_noalloc's scratch */
-    W8A16_ERR_ENV = 10               /* a diagnostic environment variable holds a value
+    W8A16_ERR_ENV = 10,              /* a diagnostic environment variable holds a value
                                         other than 0 or 1 (see Diagnostics below) */
+    W8A16_ERR_SHAPE = 11             /* attention operators: a size, type, stride or
+                                        alignment the operator does not take */
 } w8a16_status;
 
 /* Diagnostics.  Two environment variables, read once per process at the
  * first call of an entry point that enqueues work (w8a16_gemm,
  * _gemm_planned, _gemm_noalloc, _gemm_batched, _act_quant_fp8,
- * _gemm_w8a8[_planned], _gemm_w4a4[_planned]); unset, empty or "0" is off,
+ * _gemm_w8a8[_planned], _gemm_w4a4[_planned], _rope_table, _rope,
+ * _kv_append, _kv_attention); unset, empty or "0" is off,
  * "1" is on, and any other value makes each of those calls return
  * W8A16_ERR_ENV, before any other check, with the variable named in
  * w8a16_last_error().  The pure planning calls ignore them.
@@ -358,6 +361,179 @@ int w8a16_gemm_w4a4_planned(const void *a, uint32_t a_row_stride, const uint8_t 
                             const void *w_fp4, const uint8_t *w_scale, void *c,
                             uint32_t c_row_stride, uint32_t m, uint32_t n, uint32_t k,
                             const w8a16_plan_t *plan, void *stream);
+
+/* ---- Attention between the projections -----------------------------------
+ * What a decoder layer does between its Q/K/V and output projections:
+ * rotary positions, a paged cache of keys and values held in FP8, and
+ * attention over that cache.  Device pointers owned by the caller; calls are
+ * asynchronous on `stream`.  Errors, in order: W8A16_ERR_ENV, then
+ * W8A16_ERR_NULL_PTR, then W8A16_ERR_SHAPE; nothing is enqueued on an error.
+ * A call with no tokens enqueues nothing and succeeds.  Strides of
+ * activations are in elements, the last axis is contiguous, and rows need
+ * only the alignment of their type (16-byte rows run fastest). */
+
+typedef enum w8a16_dtype { W8A16_BF16 = 1, W8A16_FP16 = 2, W8A16_FP32 = 3 } w8a16_dtype;
+
+/* Which elements of a head form a pair: i and i + rot_dim/2, or 2i and
+ * 2i + 1 (i < rot_dim/2).  Elements from rot_dim on are not rotated. */
+typedef enum w8a16_rope_layout {
+    W8A16_ROPE_HALF = 0,
+    W8A16_ROPE_INTERLEAVED = 1
+} w8a16_rope_layout;
+
+/* Frequencies of the rotation, f_i = base^(-2i / rot_dim), and how they are
+ * stretched for contexts longer than the `original` positions a model was
+ * trained on:
+ *   LINEAR  f_i / factor
+ *   BASE    base replaced by base * factor^(rot_dim / (rot_dim - 2))
+ *   BANDS   with turns = original * f_i / (2 pi): f_i from high_turns up,
+ *           f_i / factor up to low_turns, and between them
+ *           f_i * (w + (1 - w) / factor), w = (turns - low_turns) / (high_turns - low_turns)
+ * Cosines and sines are multiplied by `magnitude`. */
+typedef enum w8a16_rope_scaling {
+    W8A16_ROPE_PLAIN = 0,
+    W8A16_ROPE_LINEAR = 1,
+    W8A16_ROPE_BASE = 2,
+    W8A16_ROPE_BANDS = 3
+} w8a16_rope_scaling;
+
+typedef struct w8a16_rope_config {
+    double base, factor, original, low_turns, high_turns, magnitude;
+    uint32_t scaling;         /* w8a16_rope_scaling */
+} w8a16_rope_config_t;
+
+/* table: FP32 [positions, rot_dim/2, 2], (cos, sin) of position * f_i,
+ * computed in FP64 and rounded once.  rot_dim even, 2..1024 (4 and up for
+ * BASE); base > 1; factor >= 1; for BANDS original > 0 and
+ * 0 <= low_turns < high_turns. */
+int w8a16_rope_table(const w8a16_rope_config_t *config, float *table, uint32_t positions,
+                     uint32_t rot_dim, void *stream);
+
+/* y = x rotated: for pair i of a head of the token at position p, with
+ * (c, s) = table[p][i]:  y0 = x0 c - x1 s,  y1 = x1 c + x0 s, each product
+ * and sum rounded to FP32, then once to the type.  inverse != 0 rotates by
+ * -p, which is also the gradient of the forward rotation: dx from dy.
+ * x, y: [tokens, heads, head_dim] of `dtype`; y may be x with the same
+ * strides, and must not overlap it otherwise.  positions: int32 [tokens]; a
+ * position outside the table gives NaN in that token's rotated elements. */
+int w8a16_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, void *y,
+               int64_t y_token_stride, int64_t y_head_stride, uint32_t dtype, uint32_t tokens,
+               uint32_t heads, uint32_t head_dim, const float *table, uint32_t table_positions,
+               uint32_t rot_dim, const int32_t *positions, uint32_t layout, uint32_t inverse,
+               void *stream);
+
+/* The cache.  A page holds page_size tokens (a multiple of W8A16_KV_BLOCK up
+ * to 1024) of every KV head; inside a page, blocks of 16 tokens of one head
+ * share a scale.
+ *   k        E4M3 [pages, kv_heads, page_size, head_dim]
+ *   v        E4M3 [pages, kv_heads, page_size / 16, head_dim, 16]: the 16
+ *            tokens of a block are adjacent for each channel
+ *   k_scale, v_scale  E8M0 [pages, kv_heads, page_size / 16]: a code stands
+ *            for code * 2^(byte - 127).  Bytes 1..254; a visible block whose
+ *            byte is 0 or 255 (never written) gives NaN.
+ * Page strides are in bytes, so that a cache may be a slice of a larger
+ * one; everything inside a page is contiguous.  k and v 16-byte aligned,
+ * their page strides multiples of 16; head_dim a multiple of 16 up to 256.
+ * Slots past a sequence's length may hold anything. */
+#define W8A16_KV_BLOCK 16
+#define W8A16_KV_MAX_HEAD_DIM 256
+typedef struct w8a16_kv_cache {
+    void *k, *v;
+    uint8_t *k_scale, *v_scale;
+    uint64_t k_page_stride, v_page_stride, k_scale_page_stride, v_scale_page_stride;
+    uint32_t pages, page_size, kv_heads, head_dim;
+} w8a16_kv_cache_t;
+
+/* The sequences of a call.  Sequence b brings new tokens
+ * cu_seqlens[b] .. cu_seqlens[b + 1] - 1 of the flat token axis (cu_seqlens
+ * null: tokens / seqs each), n_b of them, and holds kv_lens[b] tokens in all,
+ * the new ones among them: its new token j has position kv_lens[b] - n_b + j.
+ * A token whose position is negative belongs to no sequence (an empty slot
+ * of a padded batch).  Its tokens i * page_size onwards are on page
+ * block_table[b * block_table_stride + i], i < block_table_width.
+ * max_new: at least the largest n_b.  All arrays int32. */
+typedef struct w8a16_kv_seqs {
+    const int32_t *block_table, *kv_lens, *cu_seqlens;
+    uint32_t block_table_stride, block_table_width;
+    uint32_t seqs, tokens, max_new;
+} w8a16_kv_seqs_t;
+
+/* New keys and values, and optionally queries to rotate by the same
+ * positions.  k, v: [tokens, kv_heads, head_dim]; q, q_out: [tokens,
+ * q_heads, head_dim] (q null: none; q_out may be q).  table null: no
+ * rotation (then q must be null). */
+typedef struct w8a16_kv_append_args {
+    const void *k, *v, *q;
+    void *q_out;
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+    int64_t q_token_stride, q_head_stride, q_out_token_stride, q_out_head_stride;
+    const float *table;
+    uint32_t table_positions, rot_dim, layout, dtype, q_heads;
+} w8a16_kv_append_args_t;
+
+/* Append: rotate each new key as w8a16_rope does (in FP32, not rounded to
+ * the type), and store keys and values as codes.  For a block of 16 slots
+ * that new tokens fall into, with A the largest finite magnitude among them:
+ *   byte = max(smallest b >= 1 with A <= 448 * 2^(b - 127),
+ *              the block's byte if it holds older tokens of the sequence)
+ *   code = E4M3, nearest even, of x * 2^(127 - byte), saturated to +-448
+ * NaN is stored as NaN.  If the byte grew, the older tokens' codes are
+ * stored again for it, rounded once more only where they become subnormal.
+ * Rotated queries are rounded once to the type; a query without a position
+ * comes back as zeros.  Tokens past the block table, or whose page number is
+ * outside the cache, are not stored.  Two sequences of a call must not
+ * append to the same page. */
+int w8a16_kv_append(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
+                    const w8a16_kv_append_args_t *args, void *stream);
+
+/* Launch plan of the attention. */
+typedef enum w8a16_kv_kernel {
+    /* Row kernel: a workgroup takes 16 * row_blocks (query, head) rows of
+     * one KV head and a chunk of the keys; its four waves take interleaved
+     * 64-key tiles straight from the cache into matrix operands. */
+    W8A16_KV_ROWS = 1
+} w8a16_kv_kernel;
+typedef struct w8a16_kv_plan {
+    uint32_t kernel;          /* w8a16_kv_kernel */
+    uint32_t row_blocks;      /* 16-row blocks per workgroup */
+    uint32_t row_tiles;       /* row tiles of the longest sequence (derived) */
+    uint32_t chunk_tiles;     /* 64-key tiles per chunk */
+    uint32_t chunks;          /* chunks the longest sequence is cut into (derived) */
+    uint32_t grid;            /* workgroups launched (derived) */
+    uint64_t workspace_bytes; /* partial results (derived; 0 if chunks == 1) */
+} w8a16_kv_plan_t;
+
+/* For query row i of sequence b at position p = kv_lens[b] - n_b + i and
+ * query head h, KV head h / (q_heads / kv_heads):
+ *   out = sum_j softmax_j(scale * q . k_j) v_j,  lse = ln sum_j exp(scale * q . k_j)
+ * over the visible keys j < kv_lens[b]; causal: j <= p; window > 0:
+ * j > p - window.  A row that sees nothing gives zeros and lse = -inf; what
+ * hidden places hold, NaN included, changes nothing.  q, out: [tokens,
+ * q_heads, head_dim] of `dtype` (BF16 or FP16); lse: FP32 [tokens, q_heads]
+ * contiguous, or null.  max_kv: at least the largest kv_lens (0: the block
+ * table's width); it shapes the launch only, longer sequences stay right.
+ * plan: null for the default. */
+typedef struct w8a16_kv_attention_args {
+    const void *q;
+    void *out;
+    float *lse;
+    int64_t q_token_stride, q_head_stride, out_token_stride, out_head_stride;
+    const w8a16_kv_plan_t *plan;
+    float scale;
+    uint32_t q_heads, dtype, causal, window, max_kv;
+} w8a16_kv_attention_args_t;
+
+/* Sums and softmax statistics are FP32 and every order of addition is fixed
+ * by the plan, so a plan gives the same bits on every run.  A plan with
+ * chunks uses the (device, stream) workspace under the rules at the top of
+ * this file (growth is refused during capture). */
+int w8a16_kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
+                       const w8a16_kv_attention_args_t *args, void *stream);
+
+/* Default plan of the attention.  Pure: no GPU call. */
+int w8a16_plan_kv_attention(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_heads,
+                            uint32_t kv_heads, uint32_t head_dim, uint32_t window,
+                            uint32_t cu_count, w8a16_kv_plan_t *out);
 
 /* Static text for a status code (never null). */
 const char *w8a16_status_string(int status);
