@@ -23,7 +23,7 @@ import os
 from typing import Optional
 
 from . import attention as _attention
-from .attention import (KV_BLOCK, KV_KERNEL_ROWS, KVCache, KVPlan, kv_append, kv_attention, kv_cache,
+from .attention import (KV_BLOCK, KV_KERNEL_ROWS, KV_KERNEL_TILE, KVCache, KVPlan, kv_append, kv_attention, kv_cache,
                         plan_kv_attention, rope, rope_table)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))

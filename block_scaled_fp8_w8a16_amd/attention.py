@@ -21,6 +21,7 @@ ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "bands": 3}
 KV_BLOCK = 16
 KV_KERNEL_ROWS = 1
+KV_KERNEL_TILE = 2
 
 _vp, _u32, _i64, _u64 = ctypes.c_void_p, ctypes.c_uint32, ctypes.c_int64, ctypes.c_uint64
 

@@ -98,5 +98,10 @@ hipError_t launch_rope(const RopeArgs &a, uint32_t dtype, hipStream_t stream);
 hipError_t launch_kv_append(const AppendArgs &a, uint32_t dtype, hipStream_t stream);
 hipError_t launch_kv_rows(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t dtype,
                           hipStream_t stream);
+hipError_t launch_kv_tile(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t dtype,
+                          hipStream_t stream);
+// Adds the chunks' partial results of either kernel.
+hipError_t launch_kv_join(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t dtype,
+                          hipStream_t stream);
 
 }  // namespace w8a16

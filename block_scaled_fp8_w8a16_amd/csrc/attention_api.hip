@@ -407,16 +407,20 @@ int kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
     a.row_tiles = p.row_tiles;
     a.chunks = p.chunks;
     a.chunk_tiles = p.chunk_tiles;
-    e = launch_kv_rows(a, p, g->dtype, stream);
+    e = p.kernel == W8A16_KV_ROWS ? launch_kv_rows(a, p, g->dtype, stream)
+                                  : launch_kv_tile(a, p, g->dtype, stream);
+    if (e == hipSuccess && p.chunks > 1)
+        e = launch_kv_join(a, p, g->dtype, stream);
     if (e != hipSuccess)
         return named(hip_fail(e, "kernel launch"), entry);
     if (log_enabled()) {
         char line[320];
         snprintf(line, sizeof line,
                  "w8a16: %s tokens=%u seqs=%u q_heads=%u kv_heads=%u head_dim=%u max_new=%u max_kv=%u "
-                 "window=%u: row_blocks=%u row_tiles=%u chunks=%u (%u tiles each) grid=%u "
+                 "window=%u: kernel=%s row_blocks=%u row_tiles=%u chunks=%u (%u tiles each) grid=%u "
                  "workspace=%llu%s\n", entry, seqs->tokens, seqs->seqs, g->q_heads, cache->kv_heads,
-                 cache->head_dim, seqs->max_new, max_kv, window, p.row_blocks, p.row_tiles, p.chunks,
+                 cache->head_dim, seqs->max_new, max_kv, window,
+                 p.kernel == W8A16_KV_ROWS ? "kv-rows" : "kv-tile", p.row_blocks, p.row_tiles, p.chunks,
                  p.chunk_tiles, p.grid, (unsigned long long)p.workspace_bytes,
                  g->plan ? ": caller's plan" : "");
         log_line(line);

@@ -525,12 +525,6 @@ hipError_t launch_dim(const AttnArgs &a, const w8a16_kv_plan_t &p, hipStream_t s
         hipLaunchKernelGGL((w8a16_kv_rows_kernel<Q, DP, 1>), grid, block, 0, stream, a);
     else
         hipLaunchKernelGGL((w8a16_kv_rows_kernel<Q, DP, 2>), grid, block, 0, stream, a);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.chunks == 1)
-        return e;
-    const uint32_t rows = 16u * p.row_blocks, total = p.grid / p.chunks * rows;
-    hipLaunchKernelGGL((w8a16_kv_join_kernel<typename Q::elem>), dim3((total + 3u) / 4u), block, 0,
-                       stream, a, rows, p.grid * rows, total);
     return hipGetLastError();
 }
 
@@ -552,6 +546,18 @@ hipError_t launch_kv_rows(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t 
 {
     return dtype == W8A16_BF16 ? launch_type<QueryBf16>(a, p, stream)
                                : launch_type<QueryF16>(a, p, stream);
+}
+
+hipError_t launch_kv_join(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t dtype,
+                          hipStream_t stream)
+{
+    const uint32_t rows = 16u * p.row_blocks, total = p.grid / p.chunks * rows;
+    const dim3 grid((total + 3u) / 4u), block(256);
+    if (dtype == W8A16_BF16)
+        hipLaunchKernelGGL(w8a16_kv_join_kernel<__bf16>, grid, block, 0, stream, a, rows, p.grid * rows, total);
+    else
+        hipLaunchKernelGGL(w8a16_kv_join_kernel<_Float16>, grid, block, 0, stream, a, rows, p.grid * rows, total);
+    return hipGetLastError();
 }
 
 }  // namespace w8a16

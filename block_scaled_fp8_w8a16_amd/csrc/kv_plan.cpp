@@ -21,9 +21,12 @@ uint64_t div_up(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 int kv_plan_finalize(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_heads,
                      uint32_t kv_heads, uint32_t head_dim, uint32_t window, w8a16_kv_plan_t *p)
 {
-    if (p->kernel != W8A16_KV_ROWS || p->row_blocks < 1 || p->row_blocks > 2 || p->chunk_tiles < 1)
-        return fail(W8A16_ERR_BAD_PLAN, "w8a16_kv_attention: plan needs kernel W8A16_KV_ROWS, "
-                                        "row_blocks 1 or 2 and chunk_tiles of at least 1");
+    const bool rows_ok = p->kernel == W8A16_KV_ROWS && (p->row_blocks == 1 || p->row_blocks == 2);
+    const bool tile_ok = p->kernel == W8A16_KV_TILE && p->row_blocks == 8;
+    if ((!rows_ok && !tile_ok) || p->chunk_tiles < 1)
+        return fail(W8A16_ERR_BAD_PLAN, "w8a16_kv_attention: plan needs kernel W8A16_KV_ROWS with "
+                                        "row_blocks 1 or 2, or W8A16_KV_TILE with row_blocks 8, and "
+                                        "chunk_tiles of at least 1");
     // the tiles a row tile can see: all of the cache, or the window's and
     // those its rows' positions add
     const uint64_t tile_rows = 16ull * p->row_blocks, rows = (uint64_t)max_new * (q_heads / kv_heads);
@@ -62,9 +65,9 @@ int make_kv_plan(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_he
     const uint64_t cus = cu_count ? cu_count : kDefaultCUs;
     w8a16_kv_plan_t p;
     std::memset(&p, 0, sizeof p);
-    p.kernel = W8A16_KV_ROWS;
     const uint64_t rows = (uint64_t)max_new * (q_heads / kv_heads);
-    p.row_blocks = rows <= 16 ? 1 : 2;
+    p.kernel = rows <= 32 ? W8A16_KV_ROWS : W8A16_KV_TILE;
+    p.row_blocks = rows <= 16 ? 1 : (rows <= 32 ? 2 : 8);
     // two workgroups fit a CU; cut the keys until there are four for each,
     // but leave every wave two tiles
     p.chunk_tiles = 1u << 30;

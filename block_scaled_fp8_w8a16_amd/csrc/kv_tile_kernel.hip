@@ -1,0 +1,520 @@
+// Attention of many rows (prompts, prompt chunks) over the paged FP8 cache.
+//
+// The mathematics is that of the row kernel (kv_attention.hip): S^T = K Q^T,
+// p = 2^(S k_scale scale log2(e) - m) with a reference m that moves only by
+// more than 2^8, O^T += V^T p^T with p in FP16 and V widened by 2^(e - E).
+// Here the products bound the time, so a workgroup takes 128 rows and its
+// four waves 32 each, with 32x32x16 matrix instructions:
+//   * 64 keys at a time, K and V as codes, staged in LDS by DMA (each wave
+//     brings one block of 16 keys; page lookups are scalar) while the
+//     previous 64 are computed: two buffers, one barrier per tile.
+//   * Row 8a + 4h + b of the K operand holds key 16h + 4a + b, so a lane
+//     ends up with the 16 scores of one block in order, and its p are the
+//     second product's operand as they stand, whose other side is one
+//     16-byte read of V (16 keys of one channel).
+//   * K rows lie in LDS with their 16-byte chunks permuted (xor) so that the
+//     8 lanes served together hit different banks; V needs no permutation.
+// Codes are widened in registers, 128 conversions per 32 matrix
+// instructions and wave; keeping codes in LDS halves its reads.  Two
+// workgroups share a CU, so that one wave's exponentials and conversions
+// run under the other's matrix instructions.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "attention.h"
+#include "attention_device.h"
+#include "device_common.h"
+#include "kernels.h"
+
+namespace w8a16 {
+
+namespace {
+
+using namespace dev;
+
+typedef float f32x16_t __attribute__((ext_vector_type(16)));
+
+constexpr uint32_t kRows = 128;      // rows per workgroup
+constexpr float kLazy = 8.0f;
+constexpr int32_t kHeadroom = 7;
+constexpr int32_t kNoExp = -100000;
+
+template <bool V> struct Constant {
+    static constexpr bool value = V;
+};
+
+template <class Q> __device__ __forceinline__ f32x16_t mfma32(u32x4_t a, u32x4_t b, f32x16_t c);
+template <> __device__ __forceinline__ f32x16_t mfma32<QueryBf16>(u32x4_t a, u32x4_t b, f32x16_t c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+template <> __device__ __forceinline__ f32x16_t mfma32<QueryF16>(u32x4_t a, u32x4_t b, f32x16_t c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, a),
+                                                  __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+}
+
+// max of x over lanes l and l ^ 32
+__device__ __forceinline__ float max_halves(float x)
+{
+    const uint32_t u = __builtin_bit_cast(uint32_t, x);
+    auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
+
+template <class Q, int DP>
+__device__ __forceinline__ void kv_tile(const AttnArgs &a)
+{
+    constexpr int QC = DP / 32;             // 32-channel groups of the first product
+    constexpr int VT = DP / 32;             // 32-channel tiles of the second
+    constexpr uint32_t BLK = 16 * DP;       // LDS bytes of one block of K, and of V
+    constexpr uint32_t SWZ = DP == 128 || DP == 256 ? 7 : 3;
+    struct Scale { uint32_t ks, vs; };
+    // two buffers of K and V codes, then the blocks' scale bytes
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    Scale (*const scl)[4] = reinterpret_cast<Scale (*)[4]>(lds + 16 * BLK);
+    const uint32_t lane = threadIdx.x & 63u;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t col = lane & 31u, h = lane >> 5;
+    const KvPool &pool = a.pool;
+
+    // KV heads fastest: with 8 or more of them a head's row tiles share an
+    // XCD's L2; the row tiles with the longest rows start first.
+    const uint32_t groups = a.seqs.seqs * pool.heads;
+    uint32_t id = blockIdx.x;
+    const uint32_t grp = id % groups;
+    id /= groups;
+    const uint32_t chunk = id % a.chunks, rtile = a.row_tiles - 1u - id / a.chunks;
+    const uint32_t head = grp % pool.heads, b = grp / pool.heads;
+
+    RowTile t;
+    if (!seq_extent(a.seqs, b, t))
+        return;
+    t.rows = t.count * a.group;
+    t.row0 = rtile * kRows;
+    if (t.row0 >= t.rows)
+        return;
+    tile_range(a, kRows, t);
+    const uint32_t tile0 = (uint32_t)t.lo / kKvTile;
+    const uint32_t tiles = ((uint32_t)t.hi + kKvTile - 1) / kKvTile - tile0;
+    const uint32_t begin = chunk * a.chunk_tiles;
+    if (begin >= tiles && chunk > 0)
+        return;
+    const uint32_t end = chunk + 1 == a.chunks || begin + a.chunk_tiles > tiles
+                             ? tiles : begin + a.chunk_tiles;
+    const bool alone = a.chunks == 1 || tiles <= a.chunk_tiles;
+
+    // this wave's rows, and the keys they see
+    RowTile w = t;
+    w.row0 = t.row0 + 32u * wave;
+    if (w.row0 < t.rows)
+        tile_range(a, 32u, w);
+    else
+        w.lo = w.hi = w.all_lo = w.all_hi = 0;
+    const uint32_t row = w.row0 + col;
+    int32_t rlo, rhi;
+    row_range(a, t, row, rlo, rhi);
+    const uint32_t tok = a.by_group.div(row), hq = head * a.group + row - tok * a.group;
+    u32x4_t q[QC][2];
+    {
+        const typename Q::elem *src = reinterpret_cast<const typename Q::elem *>(a.q) +
+                                      (int64_t)(t.first + tok) * a.q_token + (int64_t)hq * a.q_head;
+#pragma unroll
+        for (int i = 0; i < QC; ++i) {
+            const uint32_t d = 32u * i + 16u * h;
+            q[i][0] = q[i][1] = u32x4_t{0u, 0u, 0u, 0u};
+            if (row < t.rows && d < pool.dim) {
+                if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
+                    q[i][0] = *reinterpret_cast<const u32x4_t *>(src + d);
+                    q[i][1] = *reinterpret_cast<const u32x4_t *>(src + d + 8);
+                } else {
+                    const uint16_t *s16 = reinterpret_cast<const uint16_t *>(src + d);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        q[i][x >> 2][x & 3] = (uint32_t)s16[2 * x] | ((uint32_t)s16[2 * x + 1] << 16);
+                }
+            }
+        }
+    }
+
+    // staging: wave x brings block x of a tile
+    const uint32_t last_block = t.kv_len > 0 ? (uint32_t)(t.kv_len - 1) / 16u : 0u;
+    // (read through the scalar cache: a vector load would have to be waited
+    // for together with the DMA in flight)
+    typedef const __attribute__((address_space(4))) int32_t *scalar_ptr;
+    const scalar_ptr bt = (scalar_ptr)(uintptr_t)(a.seqs.block_table + (size_t)b * a.seqs.bt_stride);
+    struct Where { uint32_t page, slot, ok; };
+    auto locate = [&](uint32_t tile) {
+        uint32_t blk = 4u * tile + wave;
+        blk = blk < last_block ? blk : last_block;
+        const uint32_t c = pool.by_blocks.div(blk);
+        Where p;
+        p.slot = head * pool.blocks + blk - c * pool.blocks;
+        const bool in = c < a.seqs.bt_width;
+        p.page = (uint32_t)bt[in ? c : 0u];
+        p.ok = in && p.page < pool.pages ? 1u : 0u;
+        p.page = p.ok ? p.page : 0u;
+        return p;
+    };
+    // lane's place in each 1 KiB piece of a block
+    uint32_t koff[DP / 64], voff[DP / 64];
+#pragma unroll
+    for (int j = 0; j < DP / 64; ++j) {
+        const uint32_t byte = 1024u * j + 16u * lane, r = byte / DP, slot = byte % DP / 16u;
+        const uint32_t f = SWZ == 7 ? (r & 3u) | ((wave & 1u) << 2) : ((r >> 1) & 1u) | ((wave & 1u) << 1);
+        uint32_t c = slot ^ f;
+        c = 16u * c < pool.dim ? c : 0u;      // channels past the head meet queries of zero
+        koff[j] = r * pool.dim + 16u * c;
+        const uint32_t d = 64u * j + lane;
+        voff[j] = 16u * (d < pool.dim ? d : 0u);
+    }
+    auto stage = [&](const Where &p, uint32_t buf) {
+        const size_t base = (size_t)p.slot * 16u * pool.dim;
+        const uint8_t *kp = pool.k + p.page * pool.k_page + base;
+        const uint8_t *vp = pool.v + p.page * pool.v_page + base;
+#pragma unroll
+        for (int j = 0; j < DP / 64; ++j) {
+            __builtin_amdgcn_global_load_lds(kp + koff[j], (lds_void_t *)(lds + buf * (8 * BLK) + wave * BLK + 1024u * j),
+                                             16, 0, 0);
+            __builtin_amdgcn_global_load_lds(vp + voff[j], (lds_void_t *)(lds + buf * (8 * BLK) + (4 + wave) * BLK + 1024u * j),
+                                             16, 0, 0);
+        }
+    };
+    auto scales = [&](const Where &p) {
+        Scale s;
+        s.ks = pool.k_scale[p.page * pool.ks_page + p.slot];
+        s.vs = pool.v_scale[p.page * pool.vs_page + p.slot];
+        return s;       // of page 0 where p.ok is 0
+    };
+
+    f32x16_t o[VT];
+#pragma unroll
+    for (int x = 0; x < VT; ++x)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            o[x][i] = 0.f;
+    float m = kNegInf, l = 0.f;
+    int32_t exp_ref = kNoExp;
+
+    // LDS offsets of the lane's K row for each chunk pair, and of its V row
+    const uint32_t krow = 16u * ((col >> 2) & 1u) + 4u * (col >> 3) + (col & 3u);
+    const uint32_t kf = SWZ == 7 ? (krow & 3u) | ((krow >> 4) << 2) : ((krow >> 1) & 1u) | ((krow >> 4) << 1);
+    const uint32_t kbase = krow * DP;
+
+    // MASKED: some row may not see all of the tile, or a block has no V scale.
+    auto compute = [&](uint32_t tile, uint32_t buf, auto masked_tag) {
+        constexpr bool MASKED = decltype(masked_tag)::value;
+        const int32_t tk = (int32_t)(tile * kKvTile);
+        float ksc[2], vsc[2];
+        int32_t e[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const Scale s = scl[buf][2 * x + h];
+            ksc[x] = s.ks - 1u < 254u ? pow2_byte(s.ks) * a.scale_log2 : __builtin_nanf("");
+            e[x] = s.vs - 1u < 254u ? (int32_t)s.vs - 127 : kNoExp;
+            if (tk + 32 * x + 16 * (int32_t)h >= w.hi)
+                e[x] = kNoExp;
+        }
+        int32_t emax = e[0] > e[1] ? e[0] : e[1];
+        const int32_t e_low = __builtin_amdgcn_readlane(emax, 0), e_high = __builtin_amdgcn_readlane(emax, 32);
+        emax = e_low > e_high ? e_low : e_high;
+        float vrescale = 1.0f;
+        if (emax > exp_ref + kHeadroom) {
+            vrescale = exp_ref == kNoExp ? 0.0f : exp2_fast((float)(exp_ref - emax));
+            exp_ref = emax;
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            vsc[x] = e[x] == kNoExp || e[x] - exp_ref < -120 ? pow2_byte(7)
+                                                             : pow2_byte((uint32_t)(e[x] - exp_ref + 127));
+
+        f32x16_t s[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                s[x][i] = 0.f;
+#pragma unroll
+            for (int i = 0; i < QC; ++i) {
+                const uint32_t c = (2u * i + h) ^ kf;
+                const u32x4_t raw = *reinterpret_cast<const u32x4_t *>(lds + buf * (8 * BLK) + x * 2 * BLK + kbase + 16u * c);
+                s[x] = mfma32<Q>(Q::widen(raw.x, raw.y), q[i][0], s[x]);
+                s[x] = mfma32<Q>(Q::widen(raw.z, raw.w), q[i][1], s[x]);
+            }
+        }
+        if (MASKED) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int32_t key = tk + 32 * x + 16 * (int32_t)h + i;
+                    s[x][i] = key >= rlo && key < rhi ? s[x][i] : kNegInf;
+                }
+        }
+        float mx[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            mx[x] = s[x][0];
+#pragma unroll
+            for (int i = 1; i < 16; ++i)
+                mx[x] = fmaxf(mx[x], s[x][i]);
+            mx[x] *= ksc[x];
+        }
+        const float top = max_halves(fmaxf(mx[0], mx[1]));
+        if (__ballot(top > m + kLazy || vrescale != 1.0f)) {
+            const float mn = top > m + kLazy ? top : m;
+            const float grow = m == kNegInf ? 0.0f : exp2_fast(m - mn);
+            l *= grow;
+            m = mn;
+            const float f = grow * vrescale;
+#pragma unroll
+            for (int x = 0; x < VT; ++x)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    o[x][i] *= f;
+        }
+        const float mu = m == kNegInf ? 0.0f : m;
+        u32x4_t p[2][2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float v = exp2_fast(fmaf(s[x][i], ksc[x], -mu));
+                if (MASKED)      // a NaN scale must not reach hidden keys
+                    v = s[x][i] == kNegInf ? 0.f : v;
+                s[x][i] = v;
+                sum += v;
+            }
+            l += sum;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                p[x][u].x = f16_pair(s[x][8 * u + 0], s[x][8 * u + 1]);
+                p[x][u].y = f16_pair(s[x][8 * u + 2], s[x][8 * u + 3]);
+                p[x][u].z = f16_pair(s[x][8 * u + 4], s[x][8 * u + 5]);
+                p[x][u].w = f16_pair(s[x][8 * u + 6], s[x][8 * u + 7]);
+            }
+        }
+        if (MASKED) {
+            // Blocks without a V scale read as NaN codes; codes of keys no
+            // row sees are dropped; a NaN code is counted for the rows that
+            // see it by a product of its own, then dropped.
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int32_t key0 = tk + 32 * x + 16 * (int32_t)h;
+                const uint32_t bad_scale = scl[buf][2 * x + h].vs - 1u >= 254u ? 0x7f7f7f7fu : 0u;
+                u32x4_t keep;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    keep[i] = 0u;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int32_t key = key0 + 4 * i + j;
+                        keep[i] |= key >= w.lo && key < w.hi ? 0xffu << (8 * j) : 0u;
+                    }
+                }
+#pragma unroll
+                for (int d = 0; d < VT; ++d) {
+                    u32x4_t raw = *reinterpret_cast<const u32x4_t *>(
+                        lds + buf * (8 * BLK) + (4u + 2u * x + h) * BLK + (32u * d + col) * 16u);
+                    raw = (raw | bad_scale) & keep;
+                    uint32_t any = 0;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        any |= nan_bytes(raw[i]);
+                    if (__ballot(any != 0)) {
+                        u32x4_t bad[2], seen[2];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t nb = nan_bytes(raw[i]) >> 7;
+                            raw[i] &= ~(nb * 0xffu);
+                            bad[i >> 1][2 * (i & 1)] = ((nb & 1u) | ((nb & 0x100u) << 8)) * 0x3c00u;
+                            bad[i >> 1][2 * (i & 1) + 1] =
+                                (((nb >> 16) & 1u) | ((nb >> 8) & 0x10000u)) * 0x3c00u;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int32_t key = key0 + 2 * i;
+                            seen[i >> 2][i & 3] = (key >= rlo && key < rhi ? 0x3c00u : 0u) |
+                                                  (key + 1 >= rlo && key + 1 < rhi ? 0x3c000000u : 0u);
+                        }
+                        f32x16_t n;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            n[i] = 0.f;
+                        n = mfma32<QueryF16>(bad[0], seen[0], n);
+                        n = mfma32<QueryF16>(bad[1], seen[1], n);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            o[d][i] = n[i] > 0.f ? __builtin_nanf("") : o[d][i];
+                    }
+                    o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.x, raw.y, vsc[x]), p[x][0], o[d]);
+                    o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.z, raw.w, vsc[x]), p[x][1], o[d]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int d = 0; d < VT; ++d)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const u32x4_t raw = *reinterpret_cast<const u32x4_t *>(
+                        lds + buf * (8 * BLK) + (4u + 2u * x + h) * BLK + (32u * d + col) * 16u);
+                    o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.x, raw.y, vsc[x]), p[x][0], o[d]);
+                    o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.z, raw.w, vsc[x]), p[x][1], o[d]);
+                }
+        }
+    };
+
+    if (begin < end) {
+        // Tiles every row of the workgroup sees run in a loop of their own,
+        // without the handling of hidden keys; it ends early at a block
+        // without a V scale.
+        uint32_t whole0 = ((uint32_t)t.all_lo + kKvTile - 1) / kKvTile, whole1 = (uint32_t)t.all_hi / kKvTile;
+        whole0 = whole0 > tile0 + begin ? whole0 - tile0 : begin;
+        whole1 = whole1 > tile0 + end ? end : (whole1 > tile0 ? whole1 - tile0 : 0u);
+        Where at = locate(tile0 + begin);
+        stage(at, 0);
+        Scale sc = scales(at);
+        uint32_t ok = at.ok;
+        if (lane == 0)
+            scl[0][wave] = Scale{ok ? sc.ks : 0u, ok ? sc.vs : 0u};
+        at = locate(tile0 + begin + 1);
+        wait_vm<0>();
+        __syncthreads();
+        uint32_t tile = begin, buf = 0;
+        // every wave has left the other buffer: fill it while this one is
+        // computed (after the last tile with one that is not used)
+        auto ahead = [&]() {
+            stage(at, buf ^ 1u);
+            sc = scales(at);
+            ok = at.ok;
+            at = locate(tile0 + tile + 2);
+        };
+        auto turn = [&]() {
+            if (lane == 0)
+                scl[buf ^ 1u][wave] = Scale{ok ? sc.ks : 0u, ok ? sc.vs : 0u};
+            wait_vm<0>();
+            __syncthreads();
+            ++tile;
+            buf ^= 1u;
+        };
+        auto general = [&](uint32_t stop) {
+            while (tile < stop) {
+                ahead();
+                const int32_t tk = (int32_t)((tile0 + tile) * kKvTile);
+                if (tk < w.hi && tk + (int32_t)kKvTile > w.lo)    // some key of it is for this wave
+                    compute(tile0 + tile, buf, Constant<true>());
+                turn();
+            }
+        };
+        general(whole0 < end ? whole0 : end);
+        while (tile < whole1 && !__ballot(scl[buf][lane & 3u].vs - 1u >= 254u)) {
+            ahead();
+            compute(tile0 + tile, buf, Constant<false>());
+            turn();
+        }
+        general(end);
+    }
+
+    // a row's sum is in two lanes; its output in both, 4 channels at a time
+    l += __shfl_xor(l, 32, 64);
+    if (row >= t.rows)
+        return;
+    const bool none = m == kNegInf && l == 0.f;
+    if (alone) {
+        const float inv = none ? 0.f : 1.0f / l;
+        const float unit = exp_ref == kNoExp ? 0.f : ldexpf(1.0f, exp_ref);
+        typename Q::elem *dst = reinterpret_cast<typename Q::elem *>(a.out) +
+                                (int64_t)(t.first + tok) * a.out_token + (int64_t)hq * a.out_head;
+        const bool wide = (reinterpret_cast<uintptr_t>(dst) & 7u) == 0;
+#pragma unroll
+        for (int d = 0; d < VT; ++d)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const uint32_t c = 32u * d + 8u * g + 4u * h;
+                if (c >= pool.dim)
+                    continue;
+                typename Q::elem v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    v[i] = static_cast<typename Q::elem>(o[d][4 * g + i] * inv * unit);
+                if (wide) {
+                    u32x2_t pk;
+                    pk.x = (uint32_t)__builtin_bit_cast(uint16_t, v[0]) |
+                           ((uint32_t)__builtin_bit_cast(uint16_t, v[1]) << 16);
+                    pk.y = (uint32_t)__builtin_bit_cast(uint16_t, v[2]) |
+                           ((uint32_t)__builtin_bit_cast(uint16_t, v[3]) << 16);
+                    *reinterpret_cast<u32x2_t *>(dst + c) = pk;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        dst[c + i] = v[i];
+                }
+            }
+        if (a.lse && h == 0)
+            a.lse[(size_t)(t.first + tok) * a.q_heads + hq] =
+                none ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
+        return;
+    }
+    // partial rows in the join kernel's order: ((b, head), rtile, chunk)
+    const size_t part = (((size_t)grp * a.row_tiles + rtile) * a.chunks + chunk) * kRows + 32u * wave + col;
+    float *wo = a.ws + part * pool.dim;
+    float *wst = a.ws + (size_t)gridDim.x * kRows * pool.dim + part * 4u;
+#pragma unroll
+    for (int d = 0; d < VT; ++d)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const uint32_t c = 32u * d + 8u * g + 4u * h;
+            if (c < pool.dim)
+                *reinterpret_cast<f32x4_t *>(wo + c) =
+                    f32x4_t{o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
+        }
+    if (h == 0) {
+        wst[0] = m;
+        wst[1] = l;
+        wst[2] = (float)exp_ref;
+    }
+}
+
+template <class Q, int DP>
+__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void w8a16_kv_tile_kernel(AttnArgs a)
+{
+    kv_tile<Q, DP>(a);
+}
+
+template <class Q, int DP>
+hipError_t launch_dim(const AttnArgs &a, const w8a16_kv_plan_t &p, hipStream_t stream)
+{
+    const uint32_t bytes = 16 * 16 * DP + 64;
+    static std::atomic<uint64_t> lds_set{0};
+    auto kern = w8a16_kv_tile_kernel<Q, DP>;
+    hipError_t e = allow_lds(reinterpret_cast<const void *>(kern), bytes, bytes, lds_set);
+    if (e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL(kern, dim3(p.grid), dim3(256), bytes, stream, a);
+    return hipGetLastError();
+}
+
+template <class Q>
+hipError_t launch_type(const AttnArgs &a, const w8a16_kv_plan_t &p, hipStream_t stream)
+{
+    switch ((a.pool.dim + 63u) / 64u) {
+    case 1: return launch_dim<Q, 64>(a, p, stream);
+    case 2: return launch_dim<Q, 128>(a, p, stream);
+    case 3: return launch_dim<Q, 192>(a, p, stream);
+    default: return launch_dim<Q, 256>(a, p, stream);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_kv_tile(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t dtype,
+                          hipStream_t stream)
+{
+    return dtype == W8A16_BF16 ? launch_type<QueryBf16>(a, p, stream)
+                               : launch_type<QueryF16>(a, p, stream);
+}
+
+}  // namespace w8a16

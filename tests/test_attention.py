@@ -496,6 +496,29 @@ def test_attention_plans(w8, row_blocks, chunk_tiles, case):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("chunk_tiles", [1, 2, 100])
+@pytest.mark.parametrize("case", range(len(ATTEND)), ids=str)
+def test_attention_tile_kernel(w8, chunk_tiles, case):
+    plan = w8.KVPlan(kernel=w8.KV_KERNEL_TILE, row_blocks=8, chunk_tiles=chunk_tiles)
+    check_attention(w8, *ATTEND[case], seed=250, plan=plan, padded=chunk_tiles == 2,
+                    strided=chunk_tiles == 2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [
+    ([150], [700], 4, 1, 128, 64, 0, True, "bf16"),        # whole tiles between hidden ones
+    ([70, 3], [400, 333], 3, 1, 64, 16, 250, True, "fp16"),
+    ([300], [300], 2, 1, 80, 48, 0, False, "bf16"),
+    ([40], [600], 5, 1, 256, 32, 0, True, "bf16"),
+    ([64], [500], 2, 1, 192, 32, 300, True, "fp16")], ids=[str(i) for i in range(5)])
+def test_attention_many_rows(w8, case):
+    check_attention(w8, *case, seed=260)
+    for kernel, blocks, tiles in ((w8.KV_KERNEL_TILE, 8, 3), (w8.KV_KERNEL_ROWS, 2, 4)):
+        plan = w8.KVPlan(kernel=kernel, row_blocks=blocks, chunk_tiles=tiles)
+        check_attention(w8, *case, seed=261, plan=plan)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("case", [1, 7, 8, 12], ids=str)
 def test_attention_strides_and_small_bounds(w8, case):
     # padded pages, strided queries and outputs, offsets given though uniform,
@@ -538,8 +561,9 @@ def test_attention_hidden_nan_does_not_leak(w8, case):
                     kc[p % ref.BLOCK, 3] = 0xFF
     check_attention(w8, *ATTEND[case], seed=600, mutate=mutate)
     for tiles in (1, 2):
-        plan = w8.KVPlan(kernel=w8.KV_KERNEL_ROWS, row_blocks=2, chunk_tiles=tiles)
-        check_attention(w8, *ATTEND[case], seed=601, mutate=mutate, plan=plan)
+        for kernel, blocks in ((w8.KV_KERNEL_ROWS, 2), (w8.KV_KERNEL_TILE, 8)):
+            plan = w8.KVPlan(kernel=kernel, row_blocks=blocks, chunk_tiles=tiles)
+            check_attention(w8, *ATTEND[case], seed=601, mutate=mutate, plan=plan)
 
 
 @pytest.mark.gpu
@@ -549,6 +573,10 @@ def test_attention_unwritten_block_is_nan(w8, byte):
         cache.ks[table[0, 1], 0, 0] = byte       # tokens 32.. of sequence 0, head 0
         cache.vs[table[1, 0], 1, 1] = byte       # tokens 16.. of sequence 1, head 1
     check_attention(w8, [20, 20], [60, 60], 4, 2, 64, 32, seed=700, mutate=mutate)
+    # blocks that every row sees, in the kernels' loops without masks
+    for kernel, blocks in ((w8.KV_KERNEL_ROWS, 2), (w8.KV_KERNEL_TILE, 8)):
+        plan = w8.KVPlan(kernel=kernel, row_blocks=blocks, chunk_tiles=100)
+        check_attention(w8, [20, 20], [360, 460], 4, 2, 64, 32, seed=701, mutate=mutate, plan=plan)
 
 
 @pytest.mark.gpu
@@ -564,6 +592,18 @@ def test_attention_page_outside_the_cache_is_nan(w8):
         # sequence 1 names no page; sequence 2 is longer than its table
         assert (out[0] == 0).all() and out[1].isnan().all() and out[2].isnan().all()
         assert lse[0].isfinite().all() and lse[1:].isnan().all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("plan", [dict(row_blocks=0), dict(row_blocks=3), dict(kernel=3),
+                                  dict(kernel=2, row_blocks=2), dict(chunk_tiles=0)])
+def test_attention_plan_refusals(w8, plan):
+    p = w8.KVPlan(**dict(dict(kernel=1, row_blocks=1, chunk_tiles=1), **plan))
+    cache = ref.Cache(1, 1, 16, 16, None).to(w8)
+    q = torch.ones(1, 1, 16, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(w8.W8A16Error) as e:
+        w8.kv_attention(q, cache, i32([[0]]), i32([5]), plan_=p)
+    assert e.value.status == w8.ERR_BAD_PLAN
 
 
 @pytest.mark.gpu
