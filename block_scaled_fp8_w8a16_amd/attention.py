@@ -94,19 +94,20 @@ _state = None
 
 
 def _setup():
-    """(library, torch, dtype codes, raise function), resolved once."""
+    """(library, torch, dtype codes, raise function, raw stream of a device
+    index), resolved once."""
     global _state
     if _state is None:
         import torch
 
         from . import _raise_if, library
+        # what current_stream(device).cuda_stream returns, an order of
+        # magnitude faster (0.06 against 1.8 us of a call's 8)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+            (lambda index: torch.cuda.current_stream(index).cuda_stream)
         _state = (library(), torch,
-                  {torch.bfloat16: 1, torch.float16: 2, torch.float32: 3}, _raise_if)
+                  {torch.bfloat16: 1, torch.float16: 2, torch.float32: 3}, _raise_if, raw)
     return _state
-
-
-def _stream(torch, t, stream):
-    return (torch.cuda.current_stream(t.device) if stream is None else stream).cuda_stream
 
 
 class KVCache(NamedTuple):
@@ -135,37 +136,51 @@ def kv_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, device="c
                    zeros(pages, kv_heads, blocks), zeros(pages, kv_heads, blocks))
 
 
+def _page_stride(name, t, inside):
+    """Page stride of a cache tensor whose pages are contiguous inside."""
+    st, want = t.stride(), 1
+    for n, have in zip(reversed(t.shape[1:]), reversed(st[1:])):
+        if n > 1 and have != want:
+            raise ValueError("the inside of a %s page must be contiguous" % name)
+        want *= n
+    return max(st[0], inside) if t.shape[0] < 2 else st[0]
+
+
 def _cache_desc(cache) -> KVCacheDesc:
     k, v, ks, vs = cache
     pages, heads, page, dim = k.shape
-    kst, vst, ksst, vsst = k.stride(), v.stride(), ks.stride(), vs.stride()
     blocks = page // KV_BLOCK
-    if tuple(v.shape) != (pages, heads, blocks, dim, KV_BLOCK) or \
-            tuple(ks.shape) != (pages, heads, blocks) or tuple(vs.shape) != (pages, heads, blocks):
+    if v.shape != (pages, heads, blocks, dim, KV_BLOCK) or ks.shape != (pages, heads, blocks) or \
+            vs.shape != ks.shape:
         raise ValueError("cache must be k [pages, heads, page, dim], v [pages, heads, page/16, dim, "
                          "16] and scales [pages, heads, page/16]")
-    if kst[1:] != (page * dim, dim, 1) or vst[1:] != (page * dim, dim * KV_BLOCK, KV_BLOCK, 1) or \
-            ksst[1:] != (blocks, 1) or vsst[1:] != (blocks, 1):
-        raise ValueError("the inside of a cache page must be contiguous")
     if k.element_size() + v.element_size() + ks.element_size() + vs.element_size() != 4:
         raise ValueError("cache tensors must be uint8 or float8")
     if not (k.is_cuda and v.is_cuda and ks.is_cuda and vs.is_cuda):
         raise ValueError("cache must be GPU tensors")
-    return KVCacheDesc(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), kst[0], vst[0],
-                       ksst[0], vsst[0], pages, page, heads, dim)
+    codes, bytes_ = heads * page * dim, heads * blocks
+    return KVCacheDesc(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(),
+                       codes if k.is_contiguous() else _page_stride("k", k, codes),
+                       codes if v.is_contiguous() else _page_stride("v", v, codes),
+                       bytes_ if ks.is_contiguous() else _page_stride("k_scale", ks, bytes_),
+                       bytes_ if vs.is_contiguous() else _page_stride("v_scale", vs, bytes_),
+                       pages, page, heads, dim)
 
 
-def _seqs_desc(torch, block_table, kv_lens, cu_seqlens, tokens, max_new) -> KVSeqs:
-    i32 = torch.int32
-    seqs = kv_lens.shape[0]
-    if block_table.dtype != i32 or kv_lens.dtype != i32 or kv_lens.dim() != 1 or \
-            block_table.dim() != 2 or block_table.shape[0] != seqs:
+def _seqs_desc(i32, block_table, kv_lens, cu_seqlens, tokens, max_new) -> KVSeqs:
+    if block_table.dtype != i32 or kv_lens.dtype != i32 or kv_lens.dim() != 1:
         raise ValueError("block_table must be int32 [seqs, pages] and kv_lens int32 [seqs]")
-    if not (block_table.is_cuda and kv_lens.is_cuda):
-        raise ValueError("block_table and kv_lens must be GPU tensors")
-    width = block_table.shape[1]
-    if (width > 1 and block_table.stride(1) != 1) or not kv_lens.is_contiguous():
-        raise ValueError("block_table rows and kv_lens must be contiguous")
+    seqs = kv_lens.shape[0]
+    rows, width = block_table.shape
+    if rows != seqs or not (block_table.is_cuda and kv_lens.is_cuda):
+        raise ValueError("block_table and kv_lens must be GPU tensors of the same sequences")
+    pitch = width
+    if not block_table.is_contiguous():
+        pitch = block_table.stride(0) if seqs > 1 else width
+        if width > 1 and block_table.stride(1) != 1:
+            raise ValueError("block_table rows must be contiguous")
+    if not kv_lens.is_contiguous():
+        raise ValueError("kv_lens must be contiguous")
     cu = 0
     if cu_seqlens is not None:
         if cu_seqlens.dtype != i32 or cu_seqlens.shape != (seqs + 1,) or \
@@ -176,21 +191,22 @@ def _seqs_desc(torch, block_table, kv_lens, cu_seqlens, tokens, max_new) -> KVSe
             max_new = tokens
     elif max_new is None:
         max_new = tokens // max(1, seqs)
-    return KVSeqs(block_table.data_ptr(), kv_lens.data_ptr(), cu,
-                  max(block_table.stride(0), width) if seqs < 2 else block_table.stride(0), width,
-                  seqs, tokens, max_new)
+    return KVSeqs(block_table.data_ptr(), kv_lens.data_ptr(), cu, pitch, width, seqs, tokens, max_new)
 
 
-def _rows(name, t, heads, dim, dtype):
+def _rows(name, t, tokens, heads, dim, dtype):
     """Token and head strides of a [tokens, heads, dim] operand."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim or t.dtype != dtype:
-        raise ValueError("%s must be %s [tokens, %d, %d]" % (name, dtype, heads, dim))
-    s = t.stride()
-    if s[2] != 1:
+    if t.shape != (tokens, heads, dim) or t.dtype != dtype or not t.is_cuda:
+        raise ValueError("%s must be a %s GPU tensor [%d, %d, %d]" % (name, dtype, tokens, heads, dim))
+    st, sh, sd = t.stride()
+    if sd != 1 and dim > 1:
         raise ValueError("%s needs a unit stride along head_dim" % name)
-    if not t.is_cuda:
-        raise ValueError("%s must be a GPU tensor" % name)
-    return s[0], s[1]
+    return st, sh
+
+
+def _like(torch, t):
+    """A new contiguous tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def rope_table(positions: int, rot_dim: int, *, base: float = 10000.0, scaling: Optional[str] = None,
@@ -199,25 +215,26 @@ def rope_table(positions: int, rot_dim: int, *, base: float = 10000.0, scaling: 
     """float32 [positions, rot_dim / 2, 2]: (cos, sin) of every position and
     pair, times `magnitude`.  scaling: None, "linear", "base" or "bands"
     (w8a16_rope_scaling in include/w8a16.h)."""
-    lib, torch, _, check = _setup()
+    lib, torch, _, check, raw = _setup()
     if scaling not in ROPE_SCALINGS:
         raise ValueError("scaling must be None, 'linear', 'base' or 'bands'")
     shape = (positions, rot_dim // 2, 2)
     if out is None:
         out = torch.empty(shape, dtype=torch.float32, device=device)
-    if out.dtype != torch.float32 or tuple(out.shape) != shape or not out.is_contiguous() or \
-            not out.is_cuda:
+    if out.dtype != torch.float32 or out.shape != shape or not out.is_contiguous() or not out.is_cuda:
         raise ValueError("out must be a contiguous float32 GPU tensor [positions, rot_dim/2, 2]")
     cfg = RopeConfig(base, factor, original, low_turns, high_turns, magnitude, ROPE_SCALINGS[scaling])
-    check(lib.w8a16_rope_table(cfg, out.data_ptr(), positions, rot_dim, _stream(torch, out, stream)))
+    check(lib.w8a16_rope_table(cfg, out.data_ptr(), positions, rot_dim,
+                               raw(out.get_device()) if stream is None else stream.cuda_stream))
     return out
 
 
-def _check_table(torch, table, dim):
-    if table.dim() != 3 or table.shape[2] != 2 or table.dtype != torch.float32 or \
+def _check_table(f32, table):
+    if table.dtype != f32 or table.dim() != 3 or table.shape[2] != 2 or \
             not table.is_contiguous() or not table.is_cuda:
         raise ValueError("table must be a contiguous float32 GPU tensor [positions, rot_dim/2, 2]")
-    return table.data_ptr(), table.shape[0], 2 * table.shape[1]
+    positions, pairs, _ = table.shape
+    return table.data_ptr(), positions, 2 * pairs
 
 
 def rope(x, table, positions, out=None, *, layout: str = "half", inverse: bool = False, stream=None):
@@ -225,23 +242,26 @@ def rope(x, table, positions, out=None, *, layout: str = "half", inverse: bool =
     first 2 * table.shape[1] elements of each head rotated to `positions`
     (int32 [tokens]).  inverse=True rotates back, which is also the gradient:
     dx = rope(dy, ..., inverse=True).  out may be x.  Returns out."""
-    lib, torch, dtypes, check = _setup()
-    if x.dim() != 3 or x.dtype not in dtypes:
+    lib, torch, dtypes, check, raw = _setup()
+    dtype = x.dtype
+    if x.dim() != 3 or dtype not in dtypes:
         raise ValueError("x must be bfloat16, float16 or float32 [tokens, heads, head_dim]")
     tokens, heads, dim = x.shape
-    xt, xh = _rows("x", x, heads, dim, x.dtype)
+    xt, xh = _rows("x", x, tokens, heads, dim, dtype)
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=x.dtype, device=x.device)
-    yt, yh = _rows("out", out, heads, dim, x.dtype)
-    if out.shape[0] != tokens or positions.shape != (tokens,) or positions.dtype != torch.int32 or \
+        out = _like(torch, x)
+        yt, yh = heads * dim, dim
+    else:
+        yt, yh = _rows("out", out, tokens, heads, dim, dtype)
+    if positions.shape != (tokens,) or positions.dtype != torch.int32 or \
             not positions.is_contiguous() or not positions.is_cuda:
-        raise ValueError("out must have x's shape and positions be a contiguous int32 GPU tensor [tokens]")
+        raise ValueError("positions must be a contiguous int32 GPU tensor [tokens]")
     if layout not in ROPE_LAYOUTS:
         raise ValueError("layout must be 'half' or 'interleaved'")
-    tp, tn, rot = _check_table(torch, table, dim)
-    st = lib.w8a16_rope(x.data_ptr(), xt, xh, out.data_ptr(), yt, yh, dtypes[x.dtype], tokens, heads,
-                        dim, tp, tn, rot, positions.data_ptr(), ROPE_LAYOUTS[layout], inverse,
-                        _stream(torch, x, stream))
+    tp, tn, rot = _check_table(torch.float32, table)
+    st = lib.w8a16_rope(x.data_ptr(), xt, xh, out.data_ptr(), yt, yh, dtypes[dtype], tokens, heads, dim,
+                        tp, tn, rot, positions.data_ptr(), ROPE_LAYOUTS[layout], inverse,
+                        raw(x.get_device()) if stream is None else stream.cuda_stream)
     if st:
         check(st)
     return out
@@ -258,39 +278,40 @@ def kv_append(cache, k, v, block_table, kv_lens, *, cu_seqlens=None, max_new: Op
     offsets of the sequences' new tokens; None: tokens / seqs each.  max_new:
     at least the most new tokens of one sequence (None: all tokens; a closer
     bound launches less).  Returns q_out (None without q)."""
-    lib, torch, dtypes, check = _setup()
-    if k.dim() != 3 or k.dtype not in dtypes:
+    lib, torch, dtypes, check, raw = _setup()
+    dtype = k.dtype
+    if k.dim() != 3 or dtype not in dtypes:
         raise ValueError("k must be bfloat16, float16 or float32 [tokens, kv_heads, head_dim]")
     tokens, heads, dim = k.shape
-    dtype = k.dtype
     desc = _cache_desc(cache)
     if heads != desc.kv_heads or dim != desc.head_dim:
         raise ValueError("k must have the cache's heads and head_dim")
-    kt, kh = _rows("k", k, heads, dim, dtype)
-    vt, vh = _rows("v", v, heads, dim, dtype)
-    if v.shape[0] != tokens:
-        raise ValueError("k and v must have the same tokens")
+    kt, kh = _rows("k", k, tokens, heads, dim, dtype)
+    vt, vh = _rows("v", v, tokens, heads, dim, dtype)
     if layout not in ROPE_LAYOUTS:
         raise ValueError("layout must be 'half' or 'interleaved'")
-    args = KVAppendArgs(k.data_ptr(), v.data_ptr(), None, None, kt, kh, vt, vh)
-    args.dtype = dtypes[dtype]
+    tp = tn = rot = qp = op = hq = qt = qh = ot = oh = 0
     if table is not None:
-        args.table, args.table_positions, args.rot_dim = _check_table(torch, table, dim)
-        args.layout = ROPE_LAYOUTS[layout]
+        tp, tn, rot = _check_table(torch.float32, table)
     if q is not None:
         hq = q.shape[1] if q.dim() == 3 else 0
-        args.q_token_stride, args.q_head_stride = _rows("q", q, hq, dim, dtype)
+        qt, qh = _rows("q", q, tokens, hq, dim, dtype)
         if q_out is None:
-            q_out = torch.empty((tokens, hq, dim), dtype=dtype, device=q.device)
-        args.q_out_token_stride, args.q_out_head_stride = _rows("q_out", q_out, hq, dim, dtype)
-        if q.shape[0] != tokens or q_out.shape[0] != tokens:
-            raise ValueError("q and q_out must have k's tokens")
-        args.q, args.q_out, args.q_heads = q.data_ptr(), q_out.data_ptr(), hq
-    seqs = _seqs_desc(torch, block_table, kv_lens, cu_seqlens, tokens, max_new)
-    st = lib.w8a16_kv_append(desc, seqs, args, _stream(torch, k, stream))
+            q_out = _like(torch, q)
+            ot, oh = hq * dim, dim
+        else:
+            ot, oh = _rows("q_out", q_out, tokens, hq, dim, dtype)
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    else:
+        q_out = None
+    seqs = _seqs_desc(torch.int32, block_table, kv_lens, cu_seqlens, tokens, max_new)
+    args = KVAppendArgs(k.data_ptr(), v.data_ptr(), qp, op, kt, kh, vt, vh, qt, qh, ot, oh, tp, tn, rot,
+                        ROPE_LAYOUTS[layout], dtypes[dtype], hq)
+    st = lib.w8a16_kv_append(desc, seqs, args,
+                             raw(k.get_device()) if stream is None else stream.cuda_stream)
     if st:
         check(st)
-    return q_out if q is not None else None
+    return q_out
 
 
 def kv_attention(q, cache, block_table, kv_lens, out=None, *, cu_seqlens=None,
@@ -304,30 +325,31 @@ def kv_attention(q, cache, block_table, kv_lens, out=None, *, cu_seqlens=None,
     what the block table can hold).  scale: None for 1 / sqrt(head_dim).
     window: keys a query sees at most, itself counted (0: all).  Returns
     out, or (out, lse) with lse float32 [tokens, q_heads]."""
-    lib, torch, dtypes, check = _setup()
+    lib, torch, dtypes, check, raw = _setup()
     desc = _cache_desc(cache)
-    dim = desc.head_dim
-    if q.dim() != 3:
-        raise ValueError("q must be [tokens, q_heads, head_dim]")
-    tokens, heads = q.shape[0], q.shape[1]
-    dtype = q.dtype
-    if dtype not in dtypes:
-        raise ValueError("q must be bfloat16 or float16")
-    qt, qh = _rows("q", q, heads, dim, dtype)
+    dim, dtype = desc.head_dim, q.dtype
+    if q.dim() != 3 or dtype not in dtypes:
+        raise ValueError("q must be bfloat16 or float16 [tokens, q_heads, head_dim]")
+    tokens, heads, _ = q.shape
+    qt, qh = _rows("q", q, tokens, heads, dim, dtype)
     if out is None:
-        out = torch.empty((tokens, heads, dim), dtype=dtype, device=q.device)
-    elif out.shape[0] != tokens:
-        raise ValueError("out must have q's tokens")
-    ot, oh = _rows("out", out, heads, dim, dtype)
-    lse = torch.empty((tokens, heads), dtype=torch.float32, device=q.device) if return_lse else None
+        out = _like(torch, q)
+        ot, oh = heads * dim, dim
+    else:
+        ot, oh = _rows("out", out, tokens, heads, dim, dtype)
+    lse, lp = None, 0
+    if return_lse:
+        lse = q.new_empty((tokens, heads), dtype=torch.float32)
+        lp = lse.data_ptr()
     if window < 0:
         raise ValueError("window must not be negative")
-    seqs = _seqs_desc(torch, block_table, kv_lens, cu_seqlens, tokens, max_new)
-    args = KVAttentionArgs(q.data_ptr(), out.data_ptr(), None if lse is None else lse.data_ptr(),
-                           qt, qh, ot, oh, None if plan_ is None else ctypes.pointer(plan_),
+    seqs = _seqs_desc(torch.int32, block_table, kv_lens, cu_seqlens, tokens, max_new)
+    args = KVAttentionArgs(q.data_ptr(), out.data_ptr(), lp, qt, qh, ot, oh,
+                           None if plan_ is None else ctypes.pointer(plan_),
                            dim ** -0.5 if scale is None else scale, heads, dtypes[dtype], causal,
                            window, max_kv or 0)
-    st = lib.w8a16_kv_attention(desc, seqs, args, _stream(torch, q, stream))
+    st = lib.w8a16_kv_attention(desc, seqs, args,
+                                raw(q.get_device()) if stream is None else stream.cuda_stream)
     if st:
         check(st)
     return (out, lse) if return_lse else out

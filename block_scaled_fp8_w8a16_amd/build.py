@@ -36,7 +36,8 @@ DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 # expensive part of its loop.  The VGPR form of the MFMA keeps them in VGPRs.
 _VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
 EXTRA_FLAGS = {"tile_m64.hip": _VGPR_FORM, "tile_m128.hip": _VGPR_FORM,
-               "w8a8_kernel.hip": _VGPR_FORM}
+               "w8a8_kernel.hip": _VGPR_FORM, "kv_attention.hip": _VGPR_FORM,
+               "kv_tile_kernel.hip": _VGPR_FORM}
 
 
 def _compile_cmd(src: str, obj: str) -> list:

@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "plan.h"
 #include "w8a16.h"
 
 namespace w8a16 {
@@ -82,6 +83,7 @@ struct AttnArgs {
     const uint8_t *q;
     uint8_t *out;
     float *lse, *ws;
+    uint32_t *counters;        // arrival counters of the row kernel, zero between calls
     int64_t q_token, q_head, out_token, out_head;
     float scale_log2;          // scale * log2(e)
     uint32_t group;            // query heads per KV head
@@ -100,8 +102,9 @@ hipError_t launch_kv_rows(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t 
                           hipStream_t stream);
 hipError_t launch_kv_tile(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t dtype,
                           hipStream_t stream);
-// Adds the chunks' partial results of either kernel.
-hipError_t launch_kv_join(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t dtype,
-                          hipStream_t stream);
+// Adds the chunks' partial results of either kernel; max_rows: rows of the
+// longest sequence.
+hipError_t launch_kv_join(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t max_rows,
+                          uint32_t dtype, hipStream_t stream);
 
 }  // namespace w8a16

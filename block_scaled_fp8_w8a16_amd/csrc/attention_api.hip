@@ -383,11 +383,14 @@ int kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
         w8a16_plan_t need;
         std::memset(&need, 0, sizeof need);
         need.workspace_bytes = p.workspace_bytes;
+        if (p.kernel == W8A16_KV_ROWS)
+            need.counter_count = p.grid / p.chunks * kKvCounterStride;
         Workspace ws;
         st = get_workspace(dev, stream, need, &ws);
         if (st != W8A16_OK)
             return named(st, entry);
         a.ws = ws.ws;
+        a.counters = ws.counters;
     }
     a.pool = pool_of(*cache);
     a.seqs = seqs_of(*seqs);
@@ -409,8 +412,8 @@ int kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
     a.chunk_tiles = p.chunk_tiles;
     e = p.kernel == W8A16_KV_ROWS ? launch_kv_rows(a, p, g->dtype, stream)
                                   : launch_kv_tile(a, p, g->dtype, stream);
-    if (e == hipSuccess && p.chunks > 1)
-        e = launch_kv_join(a, p, g->dtype, stream);
+    if (e == hipSuccess && p.kernel == W8A16_KV_TILE && p.chunks > 1)
+        e = launch_kv_join(a, p, seqs->max_new * group, g->dtype, stream);
     if (e != hipSuccess)
         return named(hip_fail(e, "kernel launch"), entry);
     if (log_enabled()) {

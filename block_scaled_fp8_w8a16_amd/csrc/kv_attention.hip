@@ -45,6 +45,24 @@ constexpr int kWaves = 4;
 constexpr float kLazy = 8.0f;       // log2 growth of a row's maximum that is left alone
 constexpr int32_t kHeadroom = 7;    // V operands reach 448 * 2^7 < 65504
 constexpr int32_t kNoExp = -100000;
+constexpr uint32_t kInFlight = 16;  // partial loads of a thread at a time in the join: each is a
+                                    // round trip past the L2
+
+// Four outputs of a row, rounded to its type.
+template <class E> __device__ __forceinline__ void store_row4(E *dst, f32x4_t v)
+{
+    const E e[4] = {static_cast<E>(v.x), static_cast<E>(v.y), static_cast<E>(v.z), static_cast<E>(v.w)};
+    if ((reinterpret_cast<uintptr_t>(dst) & 7u) == 0) {
+        u32x2_t p;
+        p.x = (uint32_t)__builtin_bit_cast(uint16_t, e[0]) | ((uint32_t)__builtin_bit_cast(uint16_t, e[1]) << 16);
+        p.y = (uint32_t)__builtin_bit_cast(uint16_t, e[2]) | ((uint32_t)__builtin_bit_cast(uint16_t, e[3]) << 16);
+        *reinterpret_cast<u32x2_t *>(dst) = p;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            dst[i] = e[i];
+    }
+}
 
 // What a wave needs to know to load a tile.
 struct TileAt {
@@ -53,35 +71,41 @@ struct TileAt {
     bool ok;
 };
 
-template <class Q, int DP, int RB>
-__global__ __launch_bounds__(256, 2) void w8a16_kv_rows_kernel(AttnArgs a)
+template <class Q, int DP>
+__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void w8a16_kv_rows_kernel(AttnArgs a)
 {
     constexpr int QC = DP / 64;       // 64-channel groups of the first product
     constexpr int VT = DP / 16;       // 16-channel tiles of the second
     constexpr int SEG = DP < 128 ? DP : 128;
-    __shared__ float part[kWaves][16][SEG + 4];
-    __shared__ float stat[kWaves][RB * 16][2];
+    constexpr int NR = 16;            // rows
+    constexpr int PART = 16 * (SEG + 4);
+    static_assert(kWaves * PART >= (int)kKvMaxChunks * NR && kWaves * PART >= 4 * 256, "LDS of the join");
+    __shared__ __attribute__((aligned(16))) float part[kWaves * PART];   // [wave][16][SEG + 4]
+    __shared__ float stat[kWaves][NR][2];
+    __shared__ float red[512];
     __shared__ int32_t exps[kWaves];
+    __shared__ uint32_t last;
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t col = lane & 15u, g = lane >> 4;
     const KvPool &pool = a.pool;
 
-    uint32_t id = blockIdx.x;
-    const uint32_t chunk = id % a.chunks;
-    id /= a.chunks;
-    const uint32_t rtile = id % a.row_tiles;
-    id /= a.row_tiles;
-    const uint32_t head = id % pool.heads, b = id / pool.heads;
+    // (sequence, KV head) pairs fastest and chunks slowest: were chunks
+    // fastest, a power of two of them would put each chunk on its own XCD,
+    // and ragged lengths leave the later chunks empty
+    const uint32_t groups = a.seqs.seqs * pool.heads;
+    const uint32_t grp = blockIdx.x % groups, rest = blockIdx.x / groups;
+    const uint32_t rtile = rest % a.row_tiles, chunk = rest / a.row_tiles;
+    const uint32_t head = grp % pool.heads, b = grp / pool.heads;
 
     RowTile t;
     if (!seq_extent(a.seqs, b, t))
         return;
     t.rows = t.count * a.group;
-    t.row0 = rtile * (16u * RB);
+    t.row0 = rtile * NR;
     if (t.row0 >= t.rows)
         return;
-    tile_range(a, 16u * RB, t);
+    tile_range(a, NR, t);
     const uint32_t tile0 = (uint32_t)t.lo / kKvTile;
     const uint32_t tiles = ((uint32_t)t.hi + kKvTile - 1) / kKvTile - tile0;
     const uint32_t begin = chunk * a.chunk_tiles;
@@ -95,43 +119,37 @@ __global__ __launch_bounds__(256, 2) void w8a16_kv_rows_kernel(AttnArgs a)
 
     // queries: column col of matrix rb is row row0 + 16 rb + col; the lane's
     // channels of group i are 64 i + 16 g .. + 15 (8 for each of two products)
-    u32x4_t q[RB][QC][2];
-    int32_t rlo[RB], rhi[RB];
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-        const uint32_t row = t.row0 + 16u * rb + col;
-        row_range(a, t, row, rlo[rb], rhi[rb]);
+    u32x4_t q[QC][2];
+    int32_t rlo, rhi;
+    {
+        const uint32_t row = t.row0 + col;
+        row_range(a, t, row, rlo, rhi);
         const uint32_t tok = a.by_group.div(row), hq = head * a.group + row - tok * a.group;
         const typename Q::elem *src = reinterpret_cast<const typename Q::elem *>(a.q) +
                                       (int64_t)(t.first + tok) * a.q_token + (int64_t)hq * a.q_head;
 #pragma unroll
         for (int i = 0; i < QC; ++i) {
             const uint32_t d = 64u * i + 16u * g;
-            q[rb][i][0] = q[rb][i][1] = u32x4_t{0u, 0u, 0u, 0u};
+            q[i][0] = q[i][1] = u32x4_t{0u, 0u, 0u, 0u};
             if (row < t.rows && d < pool.dim) {
                 if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
-                    q[rb][i][0] = *reinterpret_cast<const u32x4_t *>(src + d);
-                    q[rb][i][1] = *reinterpret_cast<const u32x4_t *>(src + d + 8);
+                    q[i][0] = *reinterpret_cast<const u32x4_t *>(src + d);
+                    q[i][1] = *reinterpret_cast<const u32x4_t *>(src + d + 8);
                 } else {
                     const uint16_t *s16 = reinterpret_cast<const uint16_t *>(src + d);
 #pragma unroll
                     for (int w = 0; w < 8; ++w)
-                        q[rb][i][w >> 2][w & 3] = (uint32_t)s16[2 * w] | ((uint32_t)s16[2 * w + 1] << 16);
+                        q[i][w >> 2][w & 3] = (uint32_t)s16[2 * w] | ((uint32_t)s16[2 * w + 1] << 16);
                 }
             }
         }
     }
 
-    f32x4_t o[RB][VT];
-    float m[RB], l[RB];
+    f32x4_t o[VT];
+    float m = kNegInf, l = 0.f;
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-        m[rb] = kNegInf;
-        l[rb] = 0.f;
-#pragma unroll
-        for (int v = 0; v < VT; ++v)
-            o[rb][v] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    }
+    for (int v = 0; v < VT; ++v)
+        o[v] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     int32_t exp_ref = kNoExp;
 
     const uint32_t last_block = t.kv_len > 0 ? (uint32_t)(t.kv_len - 1) / 16u : 0u;
@@ -201,22 +219,16 @@ __global__ __launch_bounds__(256, 2) void w8a16_kv_rows_kernel(AttnArgs a)
 
         const bool masked = (int32_t)(tile * kKvTile) < t.all_lo ||
                             (int32_t)(tile * kKvTile + kKvTile) > t.all_hi;
-        f32x4_t s[RB][4];
+        f32x4_t s[4];
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                s[rb][x] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int x = 0; x < 4; ++x)
+            s[x] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < QC; ++i)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const u32x4_t k0 = Q::widen(k[i][x].x, k[i][x].y), k1 = Q::widen(k[i][x].z, k[i][x].w);
-#pragma unroll
-                for (int rb = 0; rb < RB; ++rb) {
-                    s[rb][x] = Q::mfma16(k0, q[rb][i][0], s[rb][x]);
-                    s[rb][x] = Q::mfma16(k1, q[rb][i][1], s[rb][x]);
-                }
+                s[x] = Q::mfma16(Q::widen(k[i][x].x, k[i][x].y), q[i][0], s[x]);
+                s[x] = Q::mfma16(Q::widen(k[i][x].z, k[i][x].w), q[i][1], s[x]);
             }
 
         if (__ballot(!at.ok || at.vs - 1u >= 254u)) {
@@ -247,72 +259,59 @@ __global__ __launch_bounds__(256, 2) void w8a16_kv_rows_kernel(AttnArgs a)
             hit = __ballot(any != 0) != 0 ? 1u : 0u;
         }
 
-        u32x4_t p[RB][2], seen[RB][2];
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-            if (masked) {
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int32_t key = key0 + 4 * x + i;
-                        s[rb][x][i] = key >= rlo[rb] && key < rhi[rb] ? s[rb][x][i] : kNegInf;
-                    }
-            }
-            float mx = kNegInf;
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mx = fmaxf(mx, s[rb][x][i]);
-            mx *= ksc;
-            mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-            mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-            float alpha = vrescale;
-            if (__ballot(mx > m[rb] + kLazy || vrescale != 1.0f)) {
-                const float mn = mx > m[rb] + kLazy ? mx : m[rb];
-                const float grow = m[rb] == kNegInf ? 0.0f : exp2_fast(m[rb] - mn);
-                l[rb] *= grow;
-                alpha *= grow;
-                m[rb] = mn;
-#pragma unroll
-                for (int x = 0; x < VT; ++x)
-                    o[rb][x] *= alpha;
-            }
-            const float mu = m[rb] == kNegInf ? 0.0f : m[rb];
-            float sum = 0.f;
+        if (masked) {
 #pragma unroll
             for (int x = 0; x < 4; ++x)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float e2 = exp2_fast(fmaf(s[rb][x][i], ksc, -mu));
-                    if (masked)   // a NaN scale must not reach hidden keys
-                        e2 = s[rb][x][i] == kNegInf ? 0.f : e2;
-                    s[rb][x][i] = e2;
-                    sum += e2;
+                    const int32_t key = key0 + 4 * x + i;
+                    s[x][i] = key >= rlo && key < rhi ? s[x][i] : kNegInf;
                 }
-            l[rb] += sum;
+        }
+        float mx = kNegInf;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                p[rb][u].x = f16_pair(s[rb][2 * u][0], s[rb][2 * u][1]);
-                p[rb][u].y = f16_pair(s[rb][2 * u][2], s[rb][2 * u][3]);
-                p[rb][u].z = f16_pair(s[rb][2 * u + 1][0], s[rb][2 * u + 1][1]);
-                p[rb][u].w = f16_pair(s[rb][2 * u + 1][2], s[rb][2 * u + 1][3]);
-            }
-            if (hit) {
+        for (int x = 0; x < 4; ++x)
 #pragma unroll
-                for (int w = 0; w < 8; ++w) {
-                    const int32_t key = key0 + 2 * w;
-                    seen[rb][w >> 2][w & 3] = (key >= rlo[rb] && key < rhi[rb] ? 0x3c00u : 0u) |
-                                              (key + 1 >= rlo[rb] && key + 1 < rhi[rb] ? 0x3c000000u : 0u);
-                }
+            for (int i = 0; i < 4; ++i)
+                mx = fmaxf(mx, s[x][i]);
+        mx *= ksc;
+        mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
+        mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
+        if (__ballot(mx > m + kLazy || vrescale != 1.0f)) {
+            const float mn = mx > m + kLazy ? mx : m;
+            const float grow = m == kNegInf ? 0.0f : exp2_fast(m - mn);
+            l *= grow;
+            m = mn;
+#pragma unroll
+            for (int x = 0; x < VT; ++x)
+                o[x] *= grow * vrescale;
+        }
+        const float mu = m == kNegInf ? 0.0f : m;
+        u32x4_t p[2];
+        float sum = 0.f;
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float e2 = exp2_fast(fmaf(s[x][i], ksc, -mu));
+                if (masked)   // a NaN scale must not reach hidden keys
+                    e2 = s[x][i] == kNegInf ? 0.f : e2;
+                s[x][i] = e2;
+                sum += e2;
             }
+        l += sum;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            p[u].x = f16_pair(s[2 * u][0], s[2 * u][1]);
+            p[u].y = f16_pair(s[2 * u][2], s[2 * u][3]);
+            p[u].z = f16_pair(s[2 * u + 1][0], s[2 * u + 1][1]);
+            p[u].w = f16_pair(s[2 * u + 1][2], s[2 * u + 1][3]);
         }
 #pragma unroll
         for (int x = 0; x < VT; ++x) {
             if (hit) {
                 // NaN codes: counted for the rows that see them, then zeroed
-                u32x4_t bad[2];
+                u32x4_t bad[2], seen[2];
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const uint32_t nb = nan_bytes(v[x][w]) >> 7;
@@ -321,21 +320,20 @@ __global__ __launch_bounds__(256, 2) void w8a16_kv_rows_kernel(AttnArgs a)
                     bad[w >> 1][2 * (w & 1) + 1] = (((nb >> 16) & 1u) | ((nb >> 8) & 0x10000u)) * 0x3c00u;
                 }
 #pragma unroll
-                for (int rb = 0; rb < RB; ++rb) {
-                    f32x4_t n = {0.f, 0.f, 0.f, 0.f};
-                    n = mfma16_f16(bad[0], seen[rb][0], n);
-                    n = mfma16_f16(bad[1], seen[rb][1], n);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        o[rb][x][i] = n[i] > 0.f ? __builtin_nanf("") : o[rb][x][i];
+                for (int w = 0; w < 8; ++w) {
+                    const int32_t key = key0 + 2 * w;
+                    seen[w >> 2][w & 3] = (key >= rlo && key < rhi ? 0x3c00u : 0u) |
+                                          (key + 1 >= rlo && key + 1 < rhi ? 0x3c000000u : 0u);
                 }
-            }
-            const u32x4_t v0 = f16_from_fp8x8(v[x].x, v[x].y, vsc), v1 = f16_from_fp8x8(v[x].z, v[x].w, vsc);
+                f32x4_t n = {0.f, 0.f, 0.f, 0.f};
+                n = mfma16_f16(bad[0], seen[0], n);
+                n = mfma16_f16(bad[1], seen[1], n);
 #pragma unroll
-            for (int rb = 0; rb < RB; ++rb) {
-                o[rb][x] = mfma16_f16(v0, p[rb][0], o[rb][x]);
-                o[rb][x] = mfma16_f16(v1, p[rb][1], o[rb][x]);
+                for (int i = 0; i < 4; ++i)
+                    o[x][i] = n[i] > 0.f ? __builtin_nanf("") : o[x][i];
             }
+            o[x] = mfma16_f16(f16_from_fp8x8(v[x].x, v[x].y, vsc), p[0], o[x]);
+            o[x] = mfma16_f16(f16_from_fp8x8(v[x].z, v[x].w, vsc), p[1], o[x]);
         }
     };
 
@@ -366,14 +364,11 @@ __global__ __launch_bounds__(256, 2) void w8a16_kv_rows_kernel(AttnArgs a)
     }
 
     // join the waves: a common reference per row and a common exponent
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-        l[rb] += __shfl_xor(l[rb], 16, 64);
-        l[rb] += __shfl_xor(l[rb], 32, 64);
-        if (g == 0) {
-            stat[wave][rb * 16 + col][0] = m[rb];
-            stat[wave][rb * 16 + col][1] = l[rb];
-        }
+    l += __shfl_xor(l, 16, 64);
+    l += __shfl_xor(l, 32, 64);
+    if (g == 0) {
+        stat[wave][col][0] = m;
+        stat[wave][col][1] = l;
     }
     if (lane == 0)
         exps[wave] = exp_ref;
@@ -383,88 +378,188 @@ __global__ __launch_bounds__(256, 2) void w8a16_kv_rows_kernel(AttnArgs a)
     for (int w = 1; w < kWaves; ++w)
         exp_all = exp_all > exps[w] ? exp_all : exps[w];
     const float efac = exp_ref == kNoExp ? 0.f : exp2_fast((float)(exp_ref - exp_all));
-    const size_t slot = ((size_t)blockIdx.x) * (16u * RB);    // partial rows of this workgroup
-    float *wo = a.ws + slot * pool.dim;
-    float *wst = a.ws + (size_t)gridDim.x * (16u * RB) * pool.dim + slot * 4u;
+    const uint32_t n_rows = t.rows - t.row0 < (uint32_t)NR ? t.rows - t.row0 : (uint32_t)NR;
+    const uint32_t dim4 = pool.dim / 4;
+    // partial rows: [(b, head, rtile)][chunk][row][dim], then as many (m, l,
+    // exponent) quadruples
+    const size_t tile_id = (size_t)grp * a.row_tiles + rtile;
+    f32x4_t *const wo = reinterpret_cast<f32x4_t *>(a.ws) + tile_id * a.chunks * NR * dim4;
+    f32x4_t *const wst = reinterpret_cast<f32x4_t *>(a.ws) + (size_t)gridDim.x * NR * dim4 +
+                         tile_id * a.chunks * NR;
+    const float unit = exp_all == kNoExp ? 0.f : ldexpf(1.0f, exp_all);
+    float mall = kNegInf;
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-        float mall = kNegInf;
+    for (int w = 0; w < kWaves; ++w)
+        mall = fmaxf(mall, stat[w][col][0]);
+    // a wave that saw no key of the row (m = -inf) adds zeros
+    const float wave_fac = m == kNegInf ? 0.f : efac * exp2_fast(m - mall);
+    const uint32_t tr = threadIdx.x >> 4, row = t.row0 + tr;
+    float mr = kNegInf, lr = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w)
-            mall = fmaxf(mall, stat[w][rb * 16 + col][0]);
-        const float fac = m[rb] == kNegInf ? 0.f : efac * exp2_fast(m[rb] - mall);
+    for (int w = 0; w < kWaves; ++w)
+        mr = fmaxf(mr, stat[w][tr][0]);
 #pragma unroll
-        for (int s0 = 0; s0 < DP; s0 += SEG) {
+    for (int w = 0; w < kWaves; ++w)
+        lr += stat[w][tr][1] *     // m = -inf: l is 0, or NaN
+              (stat[w][tr][0] == kNegInf ? 1.f : exp2_fast(stat[w][tr][0] - mr));
+    const uint32_t tok = a.by_group.div(row), hq = head * a.group + row - tok * a.group;
+    const bool none = mr == kNegInf && lr == 0.f;    // the row sees nothing
+    const float inv = (none ? 0.f : 1.0f / lr) * unit;
+    typename Q::elem *const dst = reinterpret_cast<typename Q::elem *>(a.out) +
+                                  (int64_t)(t.first + tok) * a.out_token + (int64_t)hq * a.out_head;
+#pragma unroll
+    for (int s0 = 0; s0 < DP; s0 += SEG) {
+        if (s0)
             __syncthreads();
-            // a wave that saw no key of the row (m = -inf) adds zeros
 #pragma unroll
-            for (int x = 0; x < SEG / 16; ++x)
-                *reinterpret_cast<f32x4_t *>(&part[wave][col][16 * x + 4 * g]) =
-                    o[rb][s0 / 16 + x] * fac;
-            __syncthreads();
-            const uint32_t r = threadIdx.x >> 4, row = t.row0 + 16u * rb + r;
-            float mr = kNegInf, lr = 0.f;
+        for (int x = 0; x < SEG / 16; ++x)
+            *reinterpret_cast<f32x4_t *>(&part[wave * PART + col * (SEG + 4) + 16 * x + 4 * g]) =
+                o[s0 / 16 + x] * wave_fac;
+        __syncthreads();
+        if (tr >= n_rows)
+            continue;
 #pragma unroll
-            for (int w = 0; w < kWaves; ++w)
-                mr = fmaxf(mr, stat[w][rb * 16 + r][0]);
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w)
-                lr += stat[w][rb * 16 + r][1] *     // m = -inf: l is 0, or NaN
-                      (stat[w][rb * 16 + r][0] == kNegInf ? 1.f : exp2_fast(stat[w][rb * 16 + r][0] - mr));
-            if (row >= t.rows)
+        for (int i = 0; i < SEG / 64; ++i) {
+            const uint32_t c = 4u * (threadIdx.x & 15u) + 64u * i;
+            if (s0 + c >= pool.dim)
                 continue;
-            const uint32_t tok = a.by_group.div(row), hq = head * a.group + row - tok * a.group;
-            const uint32_t c0 = (threadIdx.x & 15u) * (SEG / 16);
-            if (s0 + c0 < pool.dim) {
-                float acc[SEG / 16];
+            f32x4_t acc = *reinterpret_cast<const f32x4_t *>(&part[tr * (SEG + 4) + c]);
 #pragma unroll
-                for (int i = 0; i < SEG / 16; ++i) {
-                    acc[i] = part[0][r][c0 + i];
-#pragma unroll
-                    for (int w = 1; w < kWaves; ++w)
-                        acc[i] += part[w][r][c0 + i];
-                }
-                if (alone) {
-                    // O counts in 2^exp_all; a row that sees nothing is zero
-                    const float unit = exp_all == kNoExp ? 0.f : ldexpf(1.0f, exp_all);
-                    const float inv = mr == kNegInf && lr == 0.f ? 0.f : 1.0f / lr;
-                    typename Q::elem *dst = reinterpret_cast<typename Q::elem *>(a.out) +
-                        (int64_t)(t.first + tok) * a.out_token + (int64_t)hq * a.out_head + s0 + c0;
-#pragma unroll
-                    for (int i = 0; i < SEG / 16; ++i)
-                        dst[i] = static_cast<typename Q::elem>(acc[i] * inv * unit);
-                } else {
-                    float *dst = wo + (size_t)(16 * rb + r) * pool.dim + s0 + c0;
-#pragma unroll
-                    for (int i = 0; i < SEG / 16; ++i)
-                        dst[i] = acc[i];
-                }
-            }
-            if (s0 == 0 && (threadIdx.x & 15u) == 0) {
-                if (!alone) {
-                    wst[(16 * rb + r) * 4 + 0] = mr;
-                    wst[(16 * rb + r) * 4 + 1] = lr;
-                    wst[(16 * rb + r) * 4 + 2] = (float)exp_all;
-                } else if (a.lse) {
-                    a.lse[(size_t)(t.first + tok) * a.q_heads + hq] =
-                        mr == kNegInf && lr == 0.f ? kNegInf : (mr + log2f(lr)) * 0.69314718055994531f;
-                }
-            }
+            for (int w = 1; w < kWaves; ++w)
+                acc += *reinterpret_cast<const f32x4_t *>(&part[w * PART + tr * (SEG + 4) + c]);
+            if (alone)
+                store_row4(dst + s0 + c, acc * inv);
+            else
+                store_agent(wo + ((size_t)chunk * NR + tr) * dim4 + (s0 + c) / 4, acc);
         }
+    }
+    if (tr < n_rows && (threadIdx.x & 15u) == 0) {
+        if (!alone)
+            store_agent(wst + (size_t)chunk * NR + tr, f32x4_t{mr, lr, (float)exp_all, 0.f});
+        else if (a.lse)
+            a.lse[(size_t)(t.first + tok) * a.q_heads + hq] =
+                none ? kNegInf : (mr + log2f(lr)) * 0.69314718055994531f;
+    }
+    if (alone)
+        return;
+
+    // The last of the row tile's chunks to arrive joins them, in chunk
+    // order.  The partial rows were written through to where any XCD's loads
+    // past the L1 see them, and are complete before the arrival counts.
+    uint32_t n = (tiles + a.chunk_tiles - 1) / a.chunk_tiles;
+    n = n < a.chunks ? n : a.chunks;
+    wait_vm<0>();
+    __syncthreads();
+    uint32_t *const counter = a.counters + tile_id * kKvCounterStride;
+    const uint32_t tid = threadIdx.x;
+    if (tid == 0)
+        last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u == n;
+    __syncthreads();
+    if (!last)
+        return;
+    if (tid == 0)      // ready for the next call that uses this workspace
+        __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    // statistics: thread (row sr, every SG-th chunk from sg on)
+    constexpr uint32_t SG = 256 / NR, PER = kKvMaxChunks / SG;
+    const uint32_t sr = tid % NR, sg = tid / NR;
+    f32x4_t st[PER];
+    float mj = kNegInf, ex = (float)kNoExp;
+#pragma unroll
+    for (uint32_t i = 0; i < PER; ++i) {
+        st[i] = f32x4_t{kNegInf, 0.f, (float)kNoExp, 0.f};
+        if (sr < n_rows && sg + i * SG < n)
+            st[i] = load_agent(wst + (size_t)(sg + i * SG) * NR + sr);
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < PER; ++i) {
+        mj = fmaxf(mj, st[i].x);
+        ex = fmaxf(ex, st[i].z);
+    }
+    red[tid] = mj;
+    red[256 + tid] = ex;
+    __syncthreads();
+    for (uint32_t k = 0; k < SG; ++k) {
+        mj = fmaxf(mj, red[k * NR + sr]);
+        ex = fmaxf(ex, red[256 + k * NR + sr]);
+    }
+    float lj = 0.f;
+    float *const fac = part;      // [chunk][row]
+#pragma unroll
+    for (uint32_t i = 0; i < PER; ++i)
+        if (sg + i * SG < n) {
+            const float f = st[i].x == kNegInf ? 1.f : exp2_fast(st[i].x - mj);   // -inf: l is 0, or NaN
+            lj += f * st[i].y;
+            fac[(sg + i * SG) * NR + sr] = f * exp2_fast(st[i].z - ex);
+        }
+    __syncthreads();
+    red[tid] = lj;
+    if (sg == 0) {
+        red[256 + sr] = mj;
+        red[256 + NR + sr] = ex;
+    }
+    __syncthreads();
+    if (tid < (uint32_t)NR) {
+        lj = 0.f;
+        for (uint32_t k = 0; k < SG; ++k)
+            lj += red[k * NR + tid];
+        red[256 + 2 * NR + tid] = lj;
+    }
+    __syncthreads();
+    // outputs: four channels of one row per thread; where that leaves half
+    // of the threads or more without any, they share the chunks
+    const uint32_t items = n_rows * dim4;
+    const uint32_t teams = items <= 128 ? 256u / items : 1u;
+    for (uint32_t base = 0; base < items; base += 256) {
+        const uint32_t team = teams > 1 ? tid / items : 0u, it = base + (teams > 1 ? tid - team * items : tid);
+        const bool on = it < items && team < teams;
+        const uint32_t jr = on ? it / dim4 : 0u, c4 = on ? it - jr * dim4 : 0u;
+        f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+        if (on)
+            for (uint32_t c = team; c < n; c += kInFlight * teams) {
+                f32x4_t v[kInFlight];
+#pragma unroll
+                for (uint32_t u = 0; u < kInFlight; ++u)
+                    if (c + u * teams < n)
+                        v[u] = load_agent(wo + ((size_t)(c + u * teams) * NR + jr) * dim4 + c4);
+#pragma unroll
+                for (uint32_t u = 0; u < kInFlight; ++u)
+                    if (c + u * teams < n)
+                        acc += fac[(c + u * teams) * NR + jr] * v[u];
+            }
+        if (teams > 1) {
+            __syncthreads();       // fac has been read
+            f32x4_t *const sums = reinterpret_cast<f32x4_t *>(part);
+            sums[tid] = acc;
+            __syncthreads();
+            for (uint32_t k = 1; on && team == 0 && k < teams; ++k)
+                acc += sums[k * items + it];
+        }
+        if (!on || team)
+            continue;
+        const float mg = red[256 + jr], eg = red[256 + NR + jr], lg = red[256 + 2 * NR + jr];
+        const uint32_t jtok = a.by_group.div(t.row0 + jr), jh = head * a.group + t.row0 + jr - jtok * a.group;
+        const bool empty = mg == kNegInf && lg == 0.f;
+        const float scale = empty ? 0.f : 1.0f / lg * ldexpf(1.0f, (int)eg);
+        store_row4(reinterpret_cast<typename Q::elem *>(a.out) + (int64_t)(t.first + jtok) * a.out_token +
+                       (int64_t)jh * a.out_head + 4 * c4, acc * scale);
+        if (c4 == 0 && a.lse)
+            a.lse[(size_t)(t.first + jtok) * a.q_heads + jh] =
+                empty ? kNegInf : (mg + log2f(lg)) * 0.69314718055994531f;
     }
 }
 
-// Adds the chunks' partial results of one row, in chunk order: one wave per
-// (row, KV head).
+// Adds the chunks' partial results of the tile kernel: one workgroup per (row, KV head).  Its
+// threads are groups of dim / 4, four channels each, that take the chunks in
+// turn; the groups' sums are added in group order.
 template <class E>
 __global__ __launch_bounds__(256) void w8a16_kv_join_kernel(AttnArgs a, uint32_t tile_rows,
-                                                            uint32_t grid_rows, uint32_t total)
+                                                            uint32_t rows_used, uint32_t grid_rows)
 {
-    const uint32_t unit = blockIdx.x * 4u + (threadIdx.x >> 6), lane = threadIdx.x & 63u;
-    if (unit >= total)
-        return;
-    const uint32_t r = unit % tile_rows;
-    uint32_t id = unit / tile_rows;       // ((b * heads) + head) * row_tiles + rtile
+    __shared__ float fac[256];
+    __shared__ float red[8];
+    __shared__ f32x4_t part[256];
+    const uint32_t tid = threadIdx.x;
+    const uint32_t r = blockIdx.x % rows_used, id = blockIdx.x / rows_used;   // id: ((b, head), rtile)
     const uint32_t rtile = id % a.row_tiles;
     const uint32_t head = id / a.row_tiles % a.pool.heads, b = id / a.row_tiles / a.pool.heads;
     RowTile t;
@@ -481,38 +576,73 @@ __global__ __launch_bounds__(256) void w8a16_kv_join_kernel(AttnArgs a, uint32_t
         return;      // one chunk: its workgroup has stored the row
     uint32_t n = (tiles + a.chunk_tiles - 1) / a.chunk_tiles;
     n = n < a.chunks ? n : a.chunks;
-    const uint32_t dim = a.pool.dim;
-    const float *wo = a.ws + ((size_t)id * a.chunks * tile_rows + r) * dim;
-    const float *wst = a.ws + (size_t)grid_rows * dim + ((size_t)id * a.chunks * tile_rows + r) * 4u;
+    const uint32_t dim = a.pool.dim, per = dim / 4, groups = 256u / per;
+    const size_t first = (size_t)id * a.chunks * tile_rows + r;
+    const float *wo = a.ws + first * dim;
+    const float *wst = a.ws + (size_t)grid_rows * dim + first * 4u;
+
+    // the row's largest reference and exponent over all chunks
     float m = kNegInf, ex = (float)kNoExp;
-    for (uint32_t c = 0; c < n; ++c) {
-        m = fmaxf(m, wst[(size_t)c * tile_rows * 4u]);
-        ex = fmaxf(ex, wst[(size_t)c * tile_rows * 4u + 2]);
+    for (uint32_t c = tid; c < n; c += 256u) {
+        const f32x4_t st = *reinterpret_cast<const f32x4_t *>(wst + (size_t)c * tile_rows * 4u);
+        m = fmaxf(m, st.x);
+        ex = fmaxf(ex, st.z);
     }
-    float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (uint32_t c = 0; c < n; ++c) {
-        const float *st = wst + (size_t)c * tile_rows * 4u;
-        const float f = st[0] == kNegInf ? 1.f : exp2_fast(st[0] - m);   // -inf: l is 0, or NaN
-        l += f * st[1];
-        const float fe = f * exp2_fast(st[2] - ex);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t d = lane + 64u * i;
-            if (d < dim)
-                acc[i] += fe * wo[(size_t)c * tile_rows * dim + d];
-        }
+    for (int off = 32; off >= 1; off >>= 1) {
+        m = fmaxf(m, __shfl_xor(m, off, 64));
+        ex = fmaxf(ex, __shfl_xor(ex, off, 64));
     }
+    if ((tid & 63u) == 0) {
+        red[tid >> 6] = m;
+        red[4 + (tid >> 6)] = ex;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        m = fmaxf(m, red[w]);
+        ex = fmaxf(ex, red[4 + w]);
+    }
+    const uint32_t grp = tid / per, d = tid % per * 4u;
+    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
+    float l = 0.f;       // this thread's chunks c = tid, tid + 256, ...
+    for (uint32_t c0 = 0; c0 < n; c0 += 256u) {
+        __syncthreads();
+        if (c0 + tid < n) {
+            const f32x4_t st = *reinterpret_cast<const f32x4_t *>(wst + (size_t)(c0 + tid) * tile_rows * 4u);
+            const float f = st.x == kNegInf ? 1.f : exp2_fast(st.x - m);   // -inf: l is 0, or NaN
+            l += f * st.y;
+            fac[tid] = f * exp2_fast(st.z - ex);
+        }
+        __syncthreads();
+        const uint32_t stop = n - c0 < 256u ? n - c0 : 256u;
+        if (grp < groups)
+#pragma unroll 4
+            for (uint32_t c = grp; c < stop; c += groups)
+                acc += fac[c] * *reinterpret_cast<const f32x4_t *>(wo + (size_t)(c0 + c) * tile_rows * dim + d);
+    }
+    // sum of l: over the lanes, then over the waves
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1)
+        l += __shfl_xor(l, off, 64);
+    __syncthreads();
+    if ((tid & 63u) == 0)
+        red[tid >> 6] = l;
+    part[tid] = acc;
+    __syncthreads();
+    if (tid >= per)
+        return;
+    l = red[0] + red[1] + red[2] + red[3];
+    for (uint32_t k = 1; k < groups; ++k)
+        acc += part[k * per + tid];
     const uint32_t tok = a.by_group.div(row), hq = head * a.group + row - tok * a.group;
     const bool none = m == kNegInf && l == 0.f;
     const float inv = none ? 0.f : 1.0f / l, unit_e = none ? 0.f : ldexpf(1.0f, (int)ex);
     E *dst = reinterpret_cast<E *>(a.out) + (int64_t)(t.first + tok) * a.out_token + (int64_t)hq * a.out_head;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t d = lane + 64u * i;
-        if (d < dim)
-            dst[d] = static_cast<E>(acc[i] * inv * unit_e);
-    }
-    if (lane == 0 && a.lse)
+    for (int i = 0; i < 4; ++i)
+        dst[d + i] = static_cast<E>(acc[i] * inv * unit_e);
+    if (tid == 0 && a.lse)
         a.lse[(size_t)(t.first + tok) * a.q_heads + hq] =
             none ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
 }
@@ -520,11 +650,7 @@ __global__ __launch_bounds__(256) void w8a16_kv_join_kernel(AttnArgs a, uint32_t
 template <class Q, int DP>
 hipError_t launch_dim(const AttnArgs &a, const w8a16_kv_plan_t &p, hipStream_t stream)
 {
-    const dim3 grid(p.grid), block(256);
-    if (p.row_blocks == 1)
-        hipLaunchKernelGGL((w8a16_kv_rows_kernel<Q, DP, 1>), grid, block, 0, stream, a);
-    else
-        hipLaunchKernelGGL((w8a16_kv_rows_kernel<Q, DP, 2>), grid, block, 0, stream, a);
+    hipLaunchKernelGGL((w8a16_kv_rows_kernel<Q, DP>), dim3(p.grid), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -548,15 +674,16 @@ hipError_t launch_kv_rows(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t 
                                : launch_type<QueryF16>(a, p, stream);
 }
 
-hipError_t launch_kv_join(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t dtype,
-                          hipStream_t stream)
+hipError_t launch_kv_join(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t max_rows,
+                          uint32_t dtype, hipStream_t stream)
 {
-    const uint32_t rows = 16u * p.row_blocks, total = p.grid / p.chunks * rows;
-    const dim3 grid((total + 3u) / 4u), block(256);
+    const uint32_t rows = 16u * p.row_blocks;
+    const uint32_t used = max_rows < rows ? max_rows : rows;     // rows of a tile that exist
+    const dim3 grid(p.grid / p.chunks * used), block(256);
     if (dtype == W8A16_BF16)
-        hipLaunchKernelGGL(w8a16_kv_join_kernel<__bf16>, grid, block, 0, stream, a, rows, p.grid * rows, total);
+        hipLaunchKernelGGL(w8a16_kv_join_kernel<__bf16>, grid, block, 0, stream, a, rows, used, p.grid * rows);
     else
-        hipLaunchKernelGGL(w8a16_kv_join_kernel<_Float16>, grid, block, 0, stream, a, rows, p.grid * rows, total);
+        hipLaunchKernelGGL(w8a16_kv_join_kernel<_Float16>, grid, block, 0, stream, a, rows, used, p.grid * rows);
     return hipGetLastError();
 }
 

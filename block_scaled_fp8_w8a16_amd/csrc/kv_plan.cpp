@@ -11,6 +11,7 @@ namespace w8a16 {
 namespace {
 
 constexpr uint64_t kKeysPerTile = 64;
+constexpr uint64_t kCutTiles = 16;
 
 uint64_t div_up(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
@@ -21,11 +22,11 @@ uint64_t div_up(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 int kv_plan_finalize(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_heads,
                      uint32_t kv_heads, uint32_t head_dim, uint32_t window, w8a16_kv_plan_t *p)
 {
-    const bool rows_ok = p->kernel == W8A16_KV_ROWS && (p->row_blocks == 1 || p->row_blocks == 2);
+    const bool rows_ok = p->kernel == W8A16_KV_ROWS && p->row_blocks == 1;
     const bool tile_ok = p->kernel == W8A16_KV_TILE && p->row_blocks == 8;
     if ((!rows_ok && !tile_ok) || p->chunk_tiles < 1)
         return fail(W8A16_ERR_BAD_PLAN, "w8a16_kv_attention: plan needs kernel W8A16_KV_ROWS with "
-                                        "row_blocks 1 or 2, or W8A16_KV_TILE with row_blocks 8, and "
+                                        "row_blocks 1, or W8A16_KV_TILE with row_blocks 8, and "
                                         "chunk_tiles of at least 1");
     // the tiles a row tile can see: all of the cache, or the window's and
     // those its rows' positions add
@@ -43,6 +44,12 @@ int kv_plan_finalize(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t 
     p->row_tiles = (uint32_t)row_tiles;
     p->chunks = (uint32_t)chunks;
     p->grid = (uint32_t)grid;
+    if (p->kernel == W8A16_KV_ROWS && chunks > kKvMaxChunks) {
+        char buf[128];
+        snprintf(buf, sizeof buf, "w8a16_kv_attention: %llu chunks, the row kernel joins at most %u",
+                 (unsigned long long)chunks, kKvMaxChunks);
+        return fail(W8A16_ERR_BAD_PLAN, buf);
+    }
     p->workspace_bytes = chunks > 1 ? grid * tile_rows * (head_dim + 4) * 4 : 0;
     return W8A16_OK;
 }
@@ -67,9 +74,7 @@ int make_kv_plan(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_he
     std::memset(&p, 0, sizeof p);
     const uint64_t rows = (uint64_t)max_new * (q_heads / kv_heads);
     p.kernel = rows <= 32 ? W8A16_KV_ROWS : W8A16_KV_TILE;
-    p.row_blocks = rows <= 16 ? 1 : (rows <= 32 ? 2 : 8);
-    // two workgroups fit a CU; cut the keys until there are four for each,
-    // but leave every wave two tiles
+    p.row_blocks = p.kernel == W8A16_KV_ROWS ? 1 : 8;
     p.chunk_tiles = 1u << 30;
     int st = kv_plan_finalize(seqs, max_new, max_kv, q_heads, kv_heads, head_dim, window, &p);
     if (st != W8A16_OK)
@@ -78,10 +83,18 @@ int make_kv_plan(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_he
                                 ? (uint64_t)window + max_new : max_kv, kKeysPerTile) + (window ? 1 : 0);
     if (tiles < 1)
         tiles = 1;
-    const uint64_t want = div_up(4 * cus, p.grid);
-    uint64_t per = div_up(tiles, want);
+    // Cut the keys until the CUs are full: two workgroups each, one of heads
+    // above 128 channels (their registers).  A wave keeps at least two tiles,
+    // and a cut has to spare more than kCutTiles tiles of a workgroup's time,
+    // about what joining the chunks costs.
+    const uint64_t slots = head_dim <= 128 ? 2 * cus : cus;
+    uint64_t per = div_up(tiles * p.grid, slots);
     if (per < 8)
         per = 8;
+    if (p.kernel == W8A16_KV_ROWS && per < div_up(tiles, kKvMaxChunks))
+        per = div_up(tiles, kKvMaxChunks);
+    if (per + kCutTiles >= tiles)
+        per = tiles;
     p.chunk_tiles = (uint32_t)per;
     st = kv_plan_finalize(seqs, max_new, max_kv, q_heads, kv_heads, head_dim, window, &p);
     if (st != W8A16_OK)

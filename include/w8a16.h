@@ -488,9 +488,10 @@ int w8a16_kv_append(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
 
 /* Launch plan of the attention. */
 typedef enum w8a16_kv_kernel {
-    /* Row kernel: a workgroup takes 16 * row_blocks (query, head) rows of
-     * one KV head and a chunk of the keys; its four waves take interleaved
-     * 64-key tiles straight from the cache into matrix operands. */
+    /* Row kernel: a workgroup takes 16 (query, head) rows of one KV head
+     * (row_blocks 1) and a chunk of the keys; its four waves take interleaved
+     * 64-key tiles straight from the cache into matrix operands.  The last
+     * chunk of a row tile to finish joins them (at most 128). */
     W8A16_KV_ROWS = 1,
     /* Tile kernel: 128 rows (row_blocks 8), 32 per wave; K and V tiles of 64
      * keys are staged in LDS for the four waves. */
@@ -498,7 +499,7 @@ typedef enum w8a16_kv_kernel {
 } w8a16_kv_kernel;
 typedef struct w8a16_kv_plan {
     uint32_t kernel;          /* w8a16_kv_kernel */
-    uint32_t row_blocks;      /* 16-row blocks per workgroup: rows 1 or 2, tile 8 */
+    uint32_t row_blocks;      /* 16-row blocks per workgroup: rows 1, tile 8 */
     uint32_t row_tiles;       /* row tiles of the longest sequence (derived) */
     uint32_t chunk_tiles;     /* 64-key tiles per chunk */
     uint32_t chunks;          /* chunks the longest sequence is cut into (derived) */
