@@ -42,12 +42,15 @@ struct RopeRows {
     uint32_t pairs;                             // P: pairs per item (1, 4 or 8)
 };
 
+// Heads a thread rotates where there are enough of them to fill the chip.
+constexpr uint32_t kRopeHeads = 4;
+
 struct RopeArgs {
     RopeRows r;
     const int32_t *positions;
-    uint32_t total;                             // tokens * heads * items
-    FastDiv by_row;                             // heads * items
-    uint32_t inverse;
+    uint32_t total;                             // threads: tokens * head groups * items
+    FastDiv by_row;                             // head groups * items
+    uint32_t inverse, heads_per_thread;         // 1 or kRopeHeads
 };
 
 struct KvPool {
@@ -68,12 +71,13 @@ struct AppendArgs {
     KvSeqs seqs;
     const uint8_t *k, *v;
     int64_t k_token, k_head, v_token, v_head;
-    uint32_t vec;              // rows are 16-byte aligned and rotate in whole 8-element chunks
+    uint32_t vec;              // elements of a load (8, 4 or 1): aligned, and whole in the rotated halves
     uint32_t seq_blocks;       // blocks a sequence's new tokens may touch
     uint32_t kv_groups;        // workgroups of the append; the rest rotate queries
     FastDiv by_units, by_seq_units;
     RopeRows q;                // q.x null: no queries
     uint32_t q_groups;         // workgroups per token of the queries
+    uint32_t q_heads_per_thread;
     FastDiv by_q_groups;
 };
 

@@ -74,6 +74,11 @@ void fill_rope(RopeRows &r, const void *x, void *y, const int64_t strides[4], co
     r.by_items = FastDiv(r.items);
 }
 
+uint32_t rope_heads_per_thread(uint64_t items)
+{
+    return items >= 512ull * kDefaultCUs * kRopeHeads ? kRopeHeads : 1;
+}
+
 // A rotation's shape: dtype, layout, an even part of the head.
 int check_rope(const char *entry, uint32_t dtype, uint32_t head_dim, uint32_t rot, uint32_t layout)
 {
@@ -226,7 +231,10 @@ int rope(const void *x, const int64_t strides[4], void *y, uint32_t dtype, uint3
     RopeArgs a;
     std::memset(static_cast<void *>(&a), 0, sizeof a);
     fill_rope(a.r, x, y, strides, table, table_positions, rot, head_dim, layout, heads, dtype);
-    const uint64_t row = (uint64_t)heads * a.r.items, total = row * tokens;
+    // several heads per thread where that leaves every CU 512 threads
+    a.heads_per_thread = rope_heads_per_thread((uint64_t)heads * a.r.items * tokens);
+    const uint64_t row = (uint64_t)((heads + a.heads_per_thread - 1) / a.heads_per_thread) * a.r.items;
+    const uint64_t total = row * tokens;
     if (total >= (1ull << 31))
         return refuse(W8A16_ERR_SHAPE, "%s: %u tokens of %u heads are too many for one call", entry,
                       tokens, heads);
@@ -240,8 +248,8 @@ int rope(const void *x, const int64_t strides[4], void *y, uint32_t dtype, uint3
     if (log_enabled()) {
         char line[200];
         snprintf(line, sizeof line,
-                 "w8a16: %s tokens=%u heads=%u head_dim=%u rot_dim=%u: %u pairs per thread\n", entry,
-                 tokens, heads, head_dim, rot, a.r.pairs);
+                 "w8a16: %s tokens=%u heads=%u head_dim=%u rot_dim=%u: %u pairs of %u heads per thread\n",
+                 entry, tokens, heads, head_dim, rot, a.r.pairs, a.heads_per_thread);
         log_line(line);
     }
     return named(launched(stream), entry);
@@ -285,9 +293,15 @@ int kv_append(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
     a.v_head = g->v_head_stride;
     const uint32_t size = elem_size(g->dtype), dim = cache->head_dim, rot = g->table ? g->rot_dim : 0;
     const int64_t ks[4] = {a.k_token, a.k_head, a.v_token, a.v_head};
-    a.vec = aligned(g->k, 16) && aligned(g->v, 16) && rot % 16 == 0;
-    for (int i = 0; i < 4; ++i)
-        a.vec = a.vec && ks[i] * (int64_t)size % 16 == 0;
+    // widest whole pieces: of the rows' alignment, and of the rotated halves
+    a.vec = 1;
+    for (uint32_t n = 8; n >= 4 && a.vec == 1; n /= 2) {
+        const uint32_t bytes = n * size < 16 ? n * size : 16;
+        bool ok = aligned(g->k, bytes) && aligned(g->v, bytes) && rot % (2 * n) == 0;
+        for (int i = 0; i < 4; ++i)
+            ok = ok && ks[i] * (int64_t)size % bytes == 0;
+        a.vec = ok ? n : 1;
+    }
     // n tokens touch at most ceil((n + 15) / 16) blocks of 16 slots
     a.seq_blocks = (seqs->max_new - 1 + 2 * W8A16_KV_BLOCK - 1) / W8A16_KV_BLOCK;
     const uint64_t units = (uint64_t)seqs->seqs * a.seq_blocks * cache->kv_heads * 2;
@@ -301,7 +315,9 @@ int kv_append(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
     fill_rope(a.q, g->q, g->q_out, qs, g->table, g->table_positions, rot, dim, g->layout,
               g->q ? g->q_heads : 0, g->dtype);
     if (g->q) {
-        const uint64_t per = ((uint64_t)g->q_heads * a.q.items + 255) / 256;
+        a.q_heads_per_thread = rope_heads_per_thread((uint64_t)g->q_heads * a.q.items * seqs->tokens);
+        const uint64_t head_groups = (g->q_heads + a.q_heads_per_thread - 1) / a.q_heads_per_thread;
+        const uint64_t per = (head_groups * a.q.items + 255) / 256;
         a.q_groups = (uint32_t)per;
         a.by_q_groups = FastDiv(a.q_groups);
         groups += per * seqs->tokens;

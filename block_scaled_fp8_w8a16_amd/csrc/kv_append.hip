@@ -67,59 +67,58 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t raw, float f)
     return codes4(lo[0] * f, lo[1] * f, hi[0] * f, hi[1] * f);
 }
 
-// Elements 8c .. 8c+7 of a key row, rotated by cs (null: not rotated).
-template <class T>
-__device__ __forceinline__ void load_chunk(const AppendArgs &a, const T *x, uint32_t c,
-                                           const float *cs, float *out)
+// Elements 8c .. 8c+7 of a key row, rotated by cs (null: not rotated), in
+// loads of W elements that lie whole on one side of rot and of rot / 2.
+template <class T, int W>
+__device__ __forceinline__ void load_pieces(const AppendArgs &a, const T *x, uint32_t c, const float *cs,
+                                            float *out)
 {
-    const uint32_t rot = cs ? a.q.rot : 0u, e = 8 * c;
-    if (a.vec) {
-        typedef typename Vec<T, 8>::type V8;
-        const V8 v = *reinterpret_cast<const V8 *>(x + e);
+    typedef typename Vec<T, W>::type V;
+    const uint32_t rot = cs ? a.q.rot : 0u, h = rot / 2;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            out[i] = to_f32(v[i]);
+    for (int p = 0; p < 8; p += W) {
+        const uint32_t e = 8 * c + p;
+        const V v = *reinterpret_cast<const V *>(x + e);
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            out[p + i] = to_f32(v[i]);
         if (e >= rot)
-            return;
+            continue;
         if (a.q.half) {
-            const uint32_t h = rot / 2;
             const bool upper = e >= h;
             const uint32_t i0 = upper ? e - h : e;
-            const V8 w = *reinterpret_cast<const V8 *>(x + (upper ? i0 : e + h));
+            const V w = *reinterpret_cast<const V *>(x + (upper ? i0 : e + h));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float x0 = upper ? to_f32(w[i]) : out[i], x1 = upper ? out[i] : to_f32(w[i]);
+            for (int i = 0; i < W; ++i) {
+                const float own = out[p + i], other = to_f32(w[i]);
                 float y0, y1;
-                rotate(x0, x1, cs[2 * (i0 + i)], cs[2 * (i0 + i) + 1], y0, y1);
-                out[i] = upper ? y1 : y0;
+                rotate(upper ? other : own, upper ? own : other, cs[2 * (i0 + i)], cs[2 * (i0 + i) + 1], y0, y1);
+                out[p + i] = upper ? y1 : y0;
             }
+        } else if (W > 1) {
+#pragma unroll
+            for (int i = 0; i + 1 < W; i += 2)
+                rotate(out[p + i], out[p + i + 1], cs[e + i], cs[e + i + 1], out[p + i], out[p + i + 1]);
         } else {
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                float y0, y1;
-                rotate(out[i], out[i + 1], cs[e + i], cs[e + i + 1], y0, y1);
-                out[i] = y0;
-                out[i + 1] = y1;
-            }
+            const bool second = (e & 1u) != 0;
+            const float own = out[p], other = to_f32(x[e ^ 1u]);
+            float y0, y1;
+            rotate(second ? other : own, second ? own : other, cs[e & ~1u], cs[e | 1u], y0, y1);
+            out[p] = second ? y1 : y0;
         }
-        return;
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t d = e + i;
-        if (d >= rot) {
-            out[i] = to_f32(x[d]);
-            continue;
-        }
-        const uint32_t h = rot / 2;
-        const bool second = a.q.half ? d >= h : (d & 1u) != 0;
-        const uint32_t other = a.q.half ? (second ? d - h : d + h) : (d ^ 1u);
-        const uint32_t pair = a.q.half ? (second ? d - h : d) : d / 2;
-        const float u = to_f32(x[d]), w = to_f32(x[other]);
-        float y0, y1;
-        rotate(second ? w : u, second ? u : w, cs[2 * pair], cs[2 * pair + 1], y0, y1);
-        out[i] = second ? y1 : y0;
-    }
+}
+
+template <class T>
+__device__ __forceinline__ void load_chunk(const AppendArgs &a, const T *x, uint32_t c, const float *cs,
+                                           float *out)
+{
+    if (a.vec == 8)
+        load_pieces<T, 8>(a, x, c, cs, out);
+    else if (a.vec == 4)
+        load_pieces<T, 4>(a, x, c, cs, out);
+    else
+        load_pieces<T, 1>(a, x, c, cs, out);
 }
 
 // NV: 8-element chunks of a block per lane (16 * dim / 8 / 64, rounded up).
@@ -280,32 +279,47 @@ __device__ __forceinline__ void append_block(const AppendArgs &a, uint32_t unit,
         *scale = (uint8_t)byte;
 }
 
-template <class T, int P>
+template <class T, int P, int N>
 __device__ __forceinline__ void rotate_queries(const AppendArgs &a, uint32_t t, uint32_t part)
 {
     const uint32_t idx = part * 256u + threadIdx.x;
-    const uint32_t h = a.q.by_items.div(idx), item = idx - h * a.q.items;
+    const uint32_t hg = a.q.by_items.div(idx), h = hg * N, item = idx - hg * a.q.items;
     if (h >= a.q.heads)
         return;
     uint32_t b;
     int32_t pos = 0;
     const bool owned = token_place(a.seqs, t, b, pos);
-    const T *x = reinterpret_cast<const T *>(a.q.x) + (int64_t)t * a.q.x_token + (int64_t)h * a.q.x_head;
-    T *y = reinterpret_cast<T *>(a.q.y) + (int64_t)t * a.q.y_token + (int64_t)h * a.q.y_head;
-    if (!owned) {
-        const bool pair = item < a.q.pair_items;
-        const uint32_t e0 = pair ? (a.q.half ? item * P : 2 * item * P)
-                                 : a.q.rot + (item - a.q.pair_items) * 2 * P;
-        const uint32_t e1 = pair && a.q.half ? e0 + a.q.rot / 2 : e0 + P;
-        for (uint32_t i = 0; i < P; ++i) {
-            y[e0 + i] = static_cast<T>(0.f);
-            if (e1 + i < a.q.dim)
-                y[e1 + i] = static_cast<T>(0.f);
-        }
+    const T *x = reinterpret_cast<const T *>(a.q.x) + (int64_t)t * a.q.x_token;
+    T *y = reinterpret_cast<T *>(a.q.y) + (int64_t)t * a.q.y_token;
+    if (owned) {
+        const float *cs = (uint32_t)pos < a.q.table_positions ? a.q.table + (size_t)pos * a.q.rot : nullptr;
+        if (a.q.half)
+            rope_heads<T, P, N, true>(a.q, x, y, h, item, cs, false);
+        else
+            rope_heads<T, P, N, false>(a.q, x, y, h, item, cs, false);
         return;
     }
-    const float *cs = (uint32_t)pos < a.q.table_positions ? a.q.table + (size_t)pos * a.q.rot : nullptr;
-    rope_item<T, P>(a.q, x, y, item, cs, false);
+    const bool pair = item < a.q.pair_items;
+    const uint32_t e0 = pair ? (a.q.half ? item * P : 2 * item * P)
+                             : a.q.rot + (item - a.q.pair_items) * 2 * P;
+    const uint32_t e1 = pair && a.q.half ? e0 + a.q.rot / 2 : e0 + P;
+    for (uint32_t n = 0; n < N && h + n < a.q.heads; ++n)
+        for (uint32_t i = 0; i < P; ++i) {
+            T *row = y + (int64_t)(h + n) * a.q.y_head;
+            row[e0 + i] = static_cast<T>(0.f);
+            if (e1 + i < a.q.dim)
+                row[e1 + i] = static_cast<T>(0.f);
+        }
+}
+
+template <class T, int N>
+__device__ __forceinline__ void rotate_queries_by(const AppendArgs &a, uint32_t t, uint32_t part)
+{
+    switch (a.q.pairs) {
+    case 8: rotate_queries<T, 8, N>(a, t, part); break;
+    case 4: rotate_queries<T, 4, N>(a, t, part); break;
+    default: rotate_queries<T, 1, N>(a, t, part); break;
+    }
 }
 
 template <class T, int NV>
@@ -319,11 +333,10 @@ __global__ __launch_bounds__(256) void w8a16_kv_append_kernel(AppendArgs a)
     }
     const uint32_t g = blockIdx.x - a.kv_groups;
     const uint32_t t = a.by_q_groups.div(g), part = g - t * a.q_groups;
-    switch (a.q.pairs) {
-    case 8: rotate_queries<T, 8>(a, t, part); break;
-    case 4: rotate_queries<T, 4>(a, t, part); break;
-    default: rotate_queries<T, 1>(a, t, part); break;
-    }
+    if (a.q_heads_per_thread == 1)
+        rotate_queries_by<T, 1>(a, t, part);
+    else
+        rotate_queries_by<T, kRopeHeads>(a, t, part);
 }
 
 template <class T>

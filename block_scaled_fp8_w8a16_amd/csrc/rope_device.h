@@ -56,74 +56,78 @@ __device__ __forceinline__ bool token_place(const KvSeqs &s, uint32_t t, uint32_
     return pos >= 0;
 }
 
-// Item `item` of one head row: P pairs, or 2P elements past rot.  T: element
-// type.  cs: the position's table row, null for a position outside the table.
-template <class T, int P>
-__device__ __forceinline__ void rope_item(const RopeRows &r, const T *x, T *y, uint32_t item,
-                                          const float *cs, bool inverse)
+// Item `item` of N heads from head `h` on (those below r.heads): P pairs, or
+// 2P elements past rot.  T: element type; x, y: the token's rows; cs: the
+// position's table row, null for a position outside the table.  The heads'
+// loads are issued together and share the cosines and sines.
+template <class T, int P, int N, bool HALF>
+__device__ __forceinline__ void rope_heads(const RopeRows &r, const T *x, T *y, uint32_t h, uint32_t item,
+                                           const float *cs, bool inverse)
 {
     typedef typename Vec<T, P>::type V;
-    if (item >= r.pair_items) {
-        const uint32_t e = r.rot + (item - r.pair_items) * (2 * P);
-        if (P == 1) {   // an odd tail is possible: one element at a time
-            if (x != y)
-                for (uint32_t i = e; i < e + 2 && i < r.dim; ++i)
-                    y[i] = x[i];
+    x += (int64_t)h * r.x_head;
+    y += (int64_t)h * r.y_head;
+    const bool pair = item < r.pair_items;
+    const uint32_t p0 = item * P;
+    uint32_t e0, e1;
+    if (pair) {
+        e0 = HALF ? p0 : 2 * p0;
+        e1 = HALF ? p0 + r.rot / 2 : 2 * p0 + P;
+    } else {
+        e0 = r.rot + (item - r.pair_items) * (2 * P);
+        e1 = e0 + P;
+        if (x == y)
+            return;
+        if (P == 1) {   // the last item may hold one element
+            for (int n = 0; n < N && h + n < r.heads; ++n)
+                for (uint32_t i = e0; i < e0 + 2 && i < r.dim; ++i)
+                    y[(int64_t)n * r.y_head + i] = x[(int64_t)n * r.x_head + i];
             return;
         }
-        if (x != y) {
-            const V a = *reinterpret_cast<const V *>(x + e), b = *reinterpret_cast<const V *>(x + e + P);
-            *reinterpret_cast<V *>(y + e) = a;
-            *reinterpret_cast<V *>(y + e + P) = b;
-        }
-        return;
     }
-    const uint32_t p0 = item * P;
-    const uint32_t e0 = r.half ? p0 : 2 * p0, e1 = r.half ? p0 + r.rot / 2 : 2 * p0 + P;
-    const V a = *reinterpret_cast<const V *>(x + e0), b = *reinterpret_cast<const V *>(x + e1);
-    float c[P], s[P];
-    const float nan = __builtin_nanf("");
+    V a[N], b[N];
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-        c[i] = cs ? cs[2 * (p0 + i)] : nan;
-        s[i] = cs ? cs[2 * (p0 + i) + 1] : nan;
-        if (inverse)
-            s[i] = -s[i];
+    for (int n = 0; n < N; ++n) {
+        const T *row = x + (h + n < r.heads ? (int64_t)n * r.x_head : 0);
+        a[n] = *reinterpret_cast<const V *>(row + e0);
+        b[n] = *reinterpret_cast<const V *>(row + e1);
     }
-    float u[P], v[P];
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-        u[i] = to_f32(a[i]);
-        v[i] = to_f32(b[i]);
-    }
-    V ya, yb;
-    if (r.half || P == 1) {
+    if (pair) {
+        float c[P], s[P];
+        const float nan = __builtin_nanf("");
 #pragma unroll
         for (int i = 0; i < P; ++i) {
-            float y0, y1;
-            rotate(u[i], v[i], c[i], s[i], y0, y1);
-            ya[i] = static_cast<T>(y0);
-            yb[i] = static_cast<T>(y1);
+            c[i] = cs ? cs[2 * (p0 + i)] : nan;
+            s[i] = cs ? cs[2 * (p0 + i) + 1] : nan;
+            s[i] = inverse ? -s[i] : s[i];
         }
-    } else {
-        // pairs are adjacent: the first P/2 in a, the others in b
+        constexpr bool apart = HALF || P == 1;
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            const int j = 2 * i;
-            float y0, y1;
-            if (j < P) {
-                rotate(u[j], u[j + 1 < P ? j + 1 : 0], c[i], s[i], y0, y1);
-                ya[j] = static_cast<T>(y0);
-                ya[j + 1 < P ? j + 1 : 0] = static_cast<T>(y1);
-            } else {
-                rotate(v[j - P], v[j + 1 - P], c[i], s[i], y0, y1);
-                yb[j - P] = static_cast<T>(y0);
-                yb[j + 1 - P] = static_cast<T>(y1);
+        for (int n = 0; n < N; ++n) {
+            // adjacent pairs: the first P/2 of them are in a, the others in b
+            float u[2 * P], v[2 * P];
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                u[i] = to_f32(a[n][i]);
+                u[P + i] = to_f32(b[n][i]);
+            }
+#pragma unroll
+            for (int i = 0; i < P; ++i)
+                rotate(apart ? u[i] : u[2 * i], apart ? u[P + i] : u[2 * i + 1], c[i], s[i], v[2 * i],
+                       v[2 * i + 1]);
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                a[n][i] = static_cast<T>(apart ? v[2 * i] : v[i]);
+                b[n][i] = static_cast<T>(apart ? v[2 * i + 1] : v[P + i]);
             }
         }
     }
-    *reinterpret_cast<V *>(y + e0) = ya;
-    *reinterpret_cast<V *>(y + e1) = yb;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        if (h + n < r.heads) {
+            *reinterpret_cast<V *>(y + (int64_t)n * r.y_head + e0) = a[n];
+            *reinterpret_cast<V *>(y + (int64_t)n * r.y_head + e1) = b[n];
+        }
 }
 
 }  // namespace dev

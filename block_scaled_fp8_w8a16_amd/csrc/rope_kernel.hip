@@ -47,31 +47,40 @@ __global__ __launch_bounds__(256) void w8a16_rope_table_kernel(w8a16_rope_config
     reinterpret_cast<float2 *>(table)[idx] = v;
 }
 
-template <class T, int P>
+template <class T, int P, int N, bool HALF>
 __global__ __launch_bounds__(256) void w8a16_rope_kernel(RopeArgs a)
 {
     const uint32_t idx = blockIdx.x * 256u + threadIdx.x;
     if (idx >= a.total)
         return;
     const uint32_t t = a.by_row.div(idx), rest = idx - t * a.by_row.d;
-    const uint32_t h = a.r.by_items.div(rest), item = rest - h * a.r.items;
+    const uint32_t hg = a.r.by_items.div(rest), item = rest - hg * a.r.items;
     const uint32_t pos = (uint32_t)a.positions[t];
     const float *cs = pos < a.r.table_positions ? a.r.table + (size_t)pos * a.r.rot : nullptr;
-    const T *x = reinterpret_cast<const T *>(a.r.x) + (int64_t)t * a.r.x_token + (int64_t)h * a.r.x_head;
-    T *y = reinterpret_cast<T *>(a.r.y) + (int64_t)t * a.r.y_token + (int64_t)h * a.r.y_head;
-    rope_item<T, P>(a.r, x, y, item, cs, a.inverse != 0);
+    rope_heads<T, P, N, HALF>(a.r, reinterpret_cast<const T *>(a.r.x) + (int64_t)t * a.r.x_token,
+                        reinterpret_cast<T *>(a.r.y) + (int64_t)t * a.r.y_token, hg * N, item, cs,
+                        a.inverse != 0);
+}
+
+template <class T, int N, bool HALF>
+hipError_t launch_heads(const RopeArgs &a, hipStream_t stream)
+{
+    const dim3 grid((a.total + 255u) / 256u), block(256);
+    switch (a.r.pairs) {
+    case 8: hipLaunchKernelGGL((w8a16_rope_kernel<T, 8, N, HALF>), grid, block, 0, stream, a); break;
+    case 4: hipLaunchKernelGGL((w8a16_rope_kernel<T, 4, N, HALF>), grid, block, 0, stream, a); break;
+    default: hipLaunchKernelGGL((w8a16_rope_kernel<T, 1, N, HALF>), grid, block, 0, stream, a); break;
+    }
+    return hipGetLastError();
 }
 
 template <class T>
 hipError_t launch_type(const RopeArgs &a, hipStream_t stream)
 {
-    const dim3 grid((a.total + 255u) / 256u), block(256);
-    switch (a.r.pairs) {
-    case 8: hipLaunchKernelGGL((w8a16_rope_kernel<T, 8>), grid, block, 0, stream, a); break;
-    case 4: hipLaunchKernelGGL((w8a16_rope_kernel<T, 4>), grid, block, 0, stream, a); break;
-    default: hipLaunchKernelGGL((w8a16_rope_kernel<T, 1>), grid, block, 0, stream, a); break;
-    }
-    return hipGetLastError();
+    if (a.heads_per_thread == 1)
+        return a.r.half ? launch_heads<T, 1, true>(a, stream) : launch_heads<T, 1, false>(a, stream);
+    return a.r.half ? launch_heads<T, kRopeHeads, true>(a, stream)
+                    : launch_heads<T, kRopeHeads, false>(a, stream);
 }
 
 }  // namespace
