@@ -75,6 +75,7 @@ struct AppendArgs {
     uint32_t seq_blocks;       // blocks a sequence's new tokens may touch
     uint32_t kv_groups;        // workgroups of the append; the rest rotate queries
     FastDiv by_units, by_seq_units;
+    FastDiv by_chunks, by_k_items;   // 8-element chunks, and 2 * vec-element items, of a head
     RopeRows q;                // q.x null: no queries
     uint32_t q_groups;         // workgroups per token of the queries
     uint32_t q_heads_per_thread;

@@ -307,6 +307,8 @@ int kv_append(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
     const uint64_t units = (uint64_t)seqs->seqs * a.seq_blocks * cache->kv_heads * 2;
     uint64_t groups = (units + 3) / 4;
     a.by_units = FastDiv(cache->kv_heads * 2);
+    a.by_chunks = FastDiv(dim / 8);
+    a.by_k_items = FastDiv(dim / (2 * a.vec));
     const uint64_t seq_units = (uint64_t)a.seq_blocks * cache->kv_heads * 2;
     a.by_seq_units = FastDiv((uint32_t)(seq_units < 0x7fffffffu ? seq_units : 0x7fffffffu));
     a.kv_groups = (uint32_t)groups;

@@ -31,6 +31,9 @@ namespace {
 using namespace dev;
 
 constexpr uint32_t kBlock = W8A16_KV_BLOCK;
+// LDS bytes of 8 channels x 16 tokens, padded so that lanes writing the same
+// token's byte of different chunks use different banks.
+constexpr uint32_t kChunkPitch = 8 * kBlock + 16;
 
 __device__ __forceinline__ float power_of_two(int32_t field)   // 2^(field - 127), field 1..254
 {
@@ -45,18 +48,11 @@ __device__ __forceinline__ int32_t scale_byte(float amax)
     return b < 1 ? 1 : b;
 }
 
-// Saturates to +-448 (infinities too) and keeps NaN, which the hardware
-// conversion stores as NaN.
-__device__ __forceinline__ float saturate(float x)
-{
-    x = x > 448.0f ? 448.0f : x;
-    return x < -448.0f ? -448.0f : x;
-}
-
+// Codes of four values within +-448, or NaN.
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d)
 {
-    int v = __builtin_amdgcn_cvt_pk_fp8_f32(saturate(a), saturate(b), 0, false);
-    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(saturate(c), saturate(d), v, true);
+    int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+    return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
 }
 
 // Four codes of an older scale stored for one 2^-n times as fine.
@@ -67,76 +63,259 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t raw, float f)
     return codes4(lo[0] * f, lo[1] * f, hi[0] * f, hi[1] * f);
 }
 
-// Elements 8c .. 8c+7 of a key row, rotated by cs (null: not rotated), in
-// loads of W elements that lie whole on one side of rot and of rot / 2.
-template <class T, int W>
-__device__ __forceinline__ void load_pieces(const AppendArgs &a, const T *x, uint32_t c, const float *cs,
-                                            float *out)
+// The block a wave works on: slots lo .. hi-1 are new, slots below lo hold
+// older tokens; the token of slot lo is `first` of the token axis, at
+// position pos0 + lo.
+struct BlockAt {
+    uint32_t lo, hi, first, pos0, head, slot, page;
+};
+
+// The wave's largest finite |x| of N values per lane.
+template <int N> __device__ __forceinline__ float wave_amax(const float (&x)[N])
 {
-    typedef typename Vec<T, W>::type V;
-    const uint32_t rot = cs ? a.q.rot : 0u, h = rot / 2;
+    float amax = 0.f;
 #pragma unroll
-    for (int p = 0; p < 8; p += W) {
-        const uint32_t e = 8 * c + p;
-        const V v = *reinterpret_cast<const V *>(x + e);
+    for (int i = 0; i < N; ++i)
+        amax = fmaxf(amax, fabsf(x[i]));
+    if (__ballot(!(amax < __builtin_inff()))) {
+        // infinities (and NaN that the maximum has not skipped) leave the
+        // scale to the finite elements
+        amax = 0.f;
 #pragma unroll
-        for (int i = 0; i < W; ++i)
-            out[p + i] = to_f32(v[i]);
-        if (e >= rot)
-            continue;
-        if (a.q.half) {
-            const bool upper = e >= h;
-            const uint32_t i0 = upper ? e - h : e;
-            const V w = *reinterpret_cast<const V *>(x + (upper ? i0 : e + h));
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const float own = out[p + i], other = to_f32(w[i]);
-                float y0, y1;
-                rotate(upper ? other : own, upper ? own : other, cs[2 * (i0 + i)], cs[2 * (i0 + i) + 1], y0, y1);
-                out[p + i] = upper ? y1 : y0;
-            }
-        } else if (W > 1) {
-#pragma unroll
-            for (int i = 0; i + 1 < W; i += 2)
-                rotate(out[p + i], out[p + i + 1], cs[e + i], cs[e + i + 1], out[p + i], out[p + i + 1]);
-        } else {
-            const bool second = (e & 1u) != 0;
-            const float own = out[p], other = to_f32(x[e ^ 1u]);
-            float y0, y1;
-            rotate(second ? other : own, second ? own : other, cs[e & ~1u], cs[e | 1u], y0, y1);
-            out[p] = second ? y1 : y0;
+        for (int i = 0; i < N; ++i) {
+            const float m = fabsf(x[i]);
+            amax = m < __builtin_inff() ? fmaxf(amax, m) : amax;
         }
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1)
+        amax = fmaxf(amax, __shfl_xor(amax, off, 64));
+    return amax;
+}
+
+// A block's new scale byte, what its new elements are multiplied by, and
+// how far the byte grew.
+struct BlockScale {
+    int32_t byte, drop;
+    float inv, shrink;
+    __device__ __forceinline__ BlockScale(float amax, uint32_t lo, const uint8_t *held)
+    {
+        byte = scale_byte(amax);
+        int32_t old = byte;
+        if (lo > 0) {
+            old = *held;
+            byte = byte > old ? byte : old;
+        }
+        // byte <= 247 for amax below 2^128, and 255 at the most if held
+        inv = power_of_two(254 - byte < 1 ? 1 : 254 - byte);
+        drop = byte - old;
+        shrink = drop > 126 ? 0.f : power_of_two(127 - drop);
+    }
+    // |x| * inv <= 448 unless x is infinite
+    __device__ __forceinline__ float operator()(float x) const
+    {
+        return fabsf(x) == __builtin_inff() ? __builtin_copysignf(448.0f, x) : x * inv;
+    }
+};
+
+// N codes (1, 4 or 8) at dst, which is aligned to them.
+template <int N> __device__ __forceinline__ void store_codes(uint8_t *dst, const float *y)
+{
+    if constexpr (N == 1) {
+        *dst = (uint8_t)codes4(y[0], 0.f, 0.f, 0.f);
+    } else if constexpr (N == 4) {
+        *reinterpret_cast<uint32_t *>(dst) = codes4(y[0], y[1], y[2], y[3]);
+    } else {
+        *reinterpret_cast<u32x2_t *>(dst) =
+            u32x2_t{codes4(y[0], y[1], y[2], y[3]), codes4(y[4], y[5], y[6], y[7])};
     }
 }
 
-template <class T>
-__device__ __forceinline__ void load_chunk(const AppendArgs &a, const T *x, uint32_t c, const float *cs,
-                                           float *out)
+// Keys.  A lane's items are P pairs of one token (two pieces of P elements,
+// as in the rotation), or 2P elements past rot; NI items per lane.
+template <class T, int P, int NI, bool HALF>
+__device__ __forceinline__ void append_keys(const AppendArgs &a, const BlockAt &at)
 {
-    if (a.vec == 8)
-        load_pieces<T, 8>(a, x, c, cs, out);
-    else if (a.vec == 4)
-        load_pieces<T, 4>(a, x, c, cs, out);
-    else
-        load_pieces<T, 1>(a, x, c, cs, out);
+    typedef typename Vec<T, P>::type V;
+    const uint32_t lane = threadIdx.x & 63u, rot = a.q.table ? a.q.rot : 0u, dim = a.pool.dim;
+    const uint32_t pair_items = rot / 2 / P;
+    V va[NI], vb[NI];
+    float2 cs[NI][P];
+    uint32_t tok[NI], e0[NI], e1[NI];
+    bool on[NI], pair[NI];
+#pragma unroll
+    for (int n = 0; n < NI; ++n) {
+        const uint32_t id = lane + 64u * n, t = a.by_k_items.div(id), item = id - t * a.by_k_items.d;
+        tok[n] = t;
+        on[n] = t >= at.lo && t < at.hi;
+        pair[n] = item < pair_items;
+        const uint32_t q = item - pair_items;
+        e0[n] = pair[n] ? (HALF ? item * P : item * 2 * P) : rot + q * 2 * P;
+        e1[n] = pair[n] && HALF ? e0[n] + rot / 2 : e0[n] + P;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            va[n][i] = static_cast<T>(0.f);
+            vb[n][i] = static_cast<T>(0.f);
+            cs[n][i] = float2{1.f, 0.f};
+        }
+        if (on[n]) {
+            const T *x = reinterpret_cast<const T *>(a.k) + (int64_t)(at.first + t - at.lo) * a.k_token +
+                         (int64_t)at.head * a.k_head;
+            va[n] = *reinterpret_cast<const V *>(x + e0[n]);
+            vb[n] = *reinterpret_cast<const V *>(x + e1[n]);
+            const uint32_t pos = at.pos0 + t;
+            if (pair[n] && pos < a.q.table_positions) {
+                const float2 *row = reinterpret_cast<const float2 *>(a.q.table) +
+                                    (size_t)pos * (rot / 2) + item * P;
+#pragma unroll
+                for (int i = 0; i < P; ++i)
+                    cs[n][i] = row[i];
+            }
+        }
+    }
+    float x[NI * 2 * P];
+#pragma unroll
+    for (int n = 0; n < NI; ++n) {
+        float u[2 * P], *y = x + n * 2 * P;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            u[i] = to_f32(va[n][i]);
+            u[P + i] = to_f32(vb[n][i]);
+        }
+        // no angle for the position: NaN, as the rotation gives
+        const bool lost = on[n] && pair[n] && at.pos0 + tok[n] >= a.q.table_positions;
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            constexpr bool apart = HALF || P == 1;
+            const int i0 = apart ? i : 2 * i, i1 = apart ? P + i : 2 * i + 1;
+            float y0, y1;
+            rotate(u[i0], u[i1], cs[n][i].x, cs[n][i].y, y0, y1);
+            y[i0] = lost ? __builtin_nanf("") : (pair[n] ? y0 : u[i0]);
+            y[i1] = lost ? __builtin_nanf("") : (pair[n] ? y1 : u[i1]);
+        }
+    }
+    const float amax = wave_amax(x);
+    if (at.page >= a.pool.pages)
+        return;
+    uint8_t *scale = a.pool.k_scale + at.page * a.pool.ks_page + at.slot;
+    const BlockScale sc(amax, at.lo, scale);
+    uint8_t *row0 = a.pool.k + at.page * a.pool.k_page + (size_t)at.slot * kBlock * dim;
+#pragma unroll
+    for (int n = 0; n < NI; ++n) {
+        if (!on[n])
+            continue;
+        float y[2 * P];
+#pragma unroll
+        for (int i = 0; i < 2 * P; ++i)
+            y[i] = sc(x[n * 2 * P + i]);
+        store_codes<P>(row0 + tok[n] * dim + e0[n], y);
+        store_codes<P>(row0 + tok[n] * dim + e1[n], y + P);
+    }
+    if (sc.drop > 0)     // the older rows, of the new scale
+        for (uint32_t i = lane; i < at.lo * dim / 4; i += 64u) {
+            uint32_t *w = reinterpret_cast<uint32_t *>(row0) + i;
+            *w = rescale4(*w, sc.shrink);
+        }
+    if (lane == 0)
+        *scale = (uint8_t)sc.byte;
 }
 
-// NV: 8-element chunks of a block per lane (16 * dim / 8 / 64, rounded up).
-template <class T, int NV>
+// Values.  A lane's items are four consecutive tokens of one 8-element
+// chunk, so that four tokens' codes of a channel make one LDS word of the
+// transposition.  NP: items per lane; loads of W elements.
+template <class T, int W, int NP>
+__device__ __forceinline__ void append_values(const AppendArgs &a, const BlockAt &at, uint8_t *lds)
+{
+    typedef typename Vec<T, W>::type V;
+    const uint32_t lane = threadIdx.x & 63u, dim = a.pool.dim;
+    V raw[NP][4][8 / W];
+    uint32_t tg[NP], c[NP];
+#pragma unroll
+    for (int n = 0; n < NP; ++n) {
+        const uint32_t id = lane + 64u * n;
+        tg[n] = a.by_chunks.div(id);
+        c[n] = id - tg[n] * a.by_chunks.d;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t t = 4u * tg[n] + i;
+#pragma unroll
+            for (int p = 0; p < 8 / W; ++p)
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+                    raw[n][i][p][k] = static_cast<T>(0.f);
+            if (t >= at.lo && t < at.hi) {
+                const T *x = reinterpret_cast<const T *>(a.v) + (int64_t)(at.first + t - at.lo) * a.v_token +
+                             (int64_t)at.head * a.v_head + 8 * c[n];
+#pragma unroll
+                for (int p = 0; p < 8 / W; ++p)
+                    raw[n][i][p] = *reinterpret_cast<const V *>(x + p * W);
+            }
+        }
+    }
+    float x[NP * 32];       // [item][token][element]
+#pragma unroll
+    for (int n = 0; n < NP; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                x[n * 32 + i * 8 + j] = to_f32(raw[n][i][j / W][j % W]);
+    const float amax = wave_amax(x);
+    if (at.page >= a.pool.pages)
+        return;
+    uint8_t *scale = a.pool.v_scale + at.page * a.pool.vs_page + at.slot;
+    const BlockScale sc(amax, at.lo, scale);
+#pragma unroll
+    for (int n = 0; n < NP; ++n)
+        if (tg[n] < 4u) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<uint32_t *>(lds + c[n] * kChunkPitch + j * kBlock + 4u * tg[n]) =
+                    codes4(sc(x[n * 32 + j]), sc(x[n * 32 + 8 + j]), sc(x[n * 32 + 16 + j]),
+                           sc(x[n * 32 + 24 + j]));
+        }
+    // the wave's own LDS words: complete before they are read back
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+    uint8_t *blk0 = a.pool.v + at.page * a.pool.v_page + (size_t)at.slot * kBlock * dim;
+    const bool whole = at.lo == 0 && at.hi == kBlock;
+    for (uint32_t d = lane; d < dim; d += 64u) {
+        u32x4_t *dst = reinterpret_cast<u32x4_t *>(blk0 + d * kBlock);
+        u32x4_t v = *reinterpret_cast<const u32x4_t *>(lds + (d >> 3) * kChunkPitch + (d & 7u) * kBlock);
+        if (!whole) {
+            const u32x4_t have = *dst;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                uint32_t is_new = 0, is_old = 0;
+#pragma unroll
+                for (uint32_t j = 0; j < 4; ++j) {
+                    const uint32_t t = 4u * w + j;
+                    is_new |= t >= at.lo && t < at.hi ? 0xffu << (8 * j) : 0u;
+                    is_old |= t < at.lo ? 0xffu << (8 * j) : 0u;
+                }
+                const uint32_t kept = sc.drop > 0 ? rescale4(have[w], sc.shrink) : have[w];
+                v[w] = (v[w] & is_new) | (kept & is_old) | (have[w] & ~(is_new | is_old));
+            }
+        }
+        *dst = v;
+    }
+    if (lane == 0)
+        *scale = (uint8_t)sc.byte;
+}
+
+// DP: the head's channels rounded up to 128.
+template <class T, int DP, int W>
 __device__ __forceinline__ void append_block(const AppendArgs &a, uint32_t unit, uint8_t *lds)
 {
-    const uint32_t lane = threadIdx.x & 63u;
     const KvPool &pool = a.pool;
     const KvSeqs &sq = a.seqs;
     const uint32_t b = a.by_seq_units.div(unit);
     uint32_t rest = unit - b * a.by_seq_units.d;
     const uint32_t nth = a.by_units.div(rest);
     rest -= nth * a.by_units.d;
-    const uint32_t head = rest >> 1;
-    const bool is_v = (rest & 1u) != 0;
     if (b >= sq.seqs)
         return;
-    // the sequence's new tokens: first .. first + n - 1, at start ..
+    // the sequence's new tokens: first .. end - 1, at start ..
     uint32_t first = b * sq.uniform, end = first + sq.uniform;
     if (sq.cu) {
         first = (uint32_t)sq.cu[b];
@@ -155,128 +334,23 @@ __device__ __forceinline__ void append_block(const AppendArgs &a, uint32_t unit,
     if (p0 >= len || first >= end)
         return;
     const uint32_t col = pool.by_blocks.div((uint32_t)blk);
-    const uint32_t within = (uint32_t)blk - col * pool.blocks;
     if (col >= sq.bt_width)
         return;
-    const uint32_t page = (uint32_t)sq.block_table[(size_t)b * sq.bt_stride + col];
-    if (page >= pool.pages)
-        return;
-    // slots lo .. hi-1 are new, slots below lo hold older tokens
-    const uint32_t lo = start > p0 ? (uint32_t)(start - p0) : 0u;
-    const uint32_t hi = len - p0 < (int32_t)kBlock ? (uint32_t)(len - p0) : kBlock;
-    const uint32_t dim = pool.dim, chunks = dim / 8;
-    const uint32_t slot0 = head * pool.blocks + within;   // block inside the page
-
-    float x[NV][8];
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const uint32_t id = lane + 64u * i, t = id / chunks, c = id - t * chunks;
-        if (t < lo || t >= hi) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                x[i][j] = 0.f;
-            continue;
-        }
-        const uint32_t tok = first + (uint32_t)(p0 + (int32_t)t - start);
-        if (is_v) {
-            load_chunk<T>(a, reinterpret_cast<const T *>(a.v) + (int64_t)tok * a.v_token +
-                          (int64_t)head * a.v_head, c, nullptr, x[i]);
-        } else {
-            const uint32_t pos = (uint32_t)p0 + t;
-            const float *cs = a.q.table ? a.q.table + (size_t)pos * a.q.rot : nullptr;
-            if (cs && pos >= a.q.table_positions) {
-                // no angle for this position: NaN, as the rotation gives
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    x[i][j] = __builtin_nanf("");
-                if (8 * c >= a.q.rot)
-                    cs = nullptr;
-            }
-            if (!cs || pos < a.q.table_positions)
-                load_chunk<T>(a, reinterpret_cast<const T *>(a.k) + (int64_t)tok * a.k_token +
-                              (int64_t)head * a.k_head, c, cs, x[i]);
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float m = fabsf(x[i][j]);
-            amax = m < __builtin_inff() ? fmaxf(amax, m) : amax;
-        }
-    }
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1)
-        amax = fmaxf(amax, __shfl_xor(amax, off, 64));
-    uint8_t *scale = is_v ? pool.v_scale + page * pool.vs_page + slot0
-                          : pool.k_scale + page * pool.ks_page + slot0;
-    int32_t byte = scale_byte(amax), old = byte;
-    if (lo > 0) {
-        old = *scale;
-        byte = byte > old ? byte : old;
-    }
-    // 2^(127 - byte); byte <= 247 for amax below 2^128, and 254 at the most
-    // from an older block
-    const float inv = power_of_two(254 - byte < 1 ? 1 : 254 - byte);
-    const int32_t drop = byte - old;
-    const float shrink = drop > 126 ? 0.f : power_of_two(127 - drop);
-
-    if (!is_v) {
-        uint8_t *row0 = pool.k + page * pool.k_page + (size_t)slot0 * kBlock * dim;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const uint32_t id = lane + 64u * i, t = id / chunks, c = id - t * chunks;
-            u32x2_t *dst = reinterpret_cast<u32x2_t *>(row0 + t * dim + 8 * c);
-            u32x2_t v;
-            if (t >= lo && t < hi) {
-                v.x = codes4(x[i][0] * inv, x[i][1] * inv, x[i][2] * inv, x[i][3] * inv);
-                v.y = codes4(x[i][4] * inv, x[i][5] * inv, x[i][6] * inv, x[i][7] * inv);
-                *dst = v;
-            } else if (t < lo && drop > 0) {
-                v = *dst;
-                v.x = rescale4(v.x, shrink);
-                v.y = rescale4(v.y, shrink);
-                *dst = v;
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const uint32_t id = lane + 64u * i, t = id / chunks, c = id - t * chunks;
-            if (t < lo || t >= hi)
-                continue;
-            const uint32_t w0 = codes4(x[i][0] * inv, x[i][1] * inv, x[i][2] * inv, x[i][3] * inv);
-            const uint32_t w1 = codes4(x[i][4] * inv, x[i][5] * inv, x[i][6] * inv, x[i][7] * inv);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                lds[(8 * c + j) * kBlock + t] = (uint8_t)((j < 4 ? w0 : w1) >> (8 * (j & 3)));
-        }
-        // the wave's own LDS bytes: complete before they are read back
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        __builtin_amdgcn_wave_barrier();
-        uint8_t *blk0 = pool.v + page * pool.v_page + (size_t)slot0 * kBlock * dim;
-        const bool whole = lo == 0 && hi == kBlock;
-        for (uint32_t d = lane; d < dim; d += 64u) {
-            u32x4_t *dst = reinterpret_cast<u32x4_t *>(blk0 + d * kBlock);
-            u32x4_t v = *reinterpret_cast<const u32x4_t *>(lds + d * kBlock);
-            if (!whole) {
-                const u32x4_t have = *dst;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    uint32_t is_new = 0, is_old = 0;
-#pragma unroll
-                    for (uint32_t j = 0; j < 4; ++j) {
-                        const uint32_t t = 4u * w + j;
-                        is_new |= t >= lo && t < hi ? 0xffu << (8 * j) : 0u;
-                        is_old |= t < lo ? 0xffu << (8 * j) : 0u;
-                    }
-                    const uint32_t kept = drop > 0 ? rescale4(have[w], shrink) : have[w];
-                    v[w] = (v[w] & is_new) | (kept & is_old) | (have[w] & ~(is_new | is_old));
-                }
-            }
-            *dst = v;
-        }
-    }
-    if (lane == 0)
-        *scale = (uint8_t)byte;
+    BlockAt at;
+    at.head = rest >> 1;
+    at.slot = at.head * pool.blocks + (uint32_t)blk - col * pool.blocks;
+    // (checked once the tokens' loads are under way)
+    at.page = (uint32_t)sq.block_table[(size_t)b * sq.bt_stride + col];
+    at.pos0 = (uint32_t)p0;
+    at.lo = start > p0 ? (uint32_t)(start - p0) : 0u;
+    at.hi = len - p0 < (int32_t)kBlock ? (uint32_t)(len - p0) : kBlock;
+    at.first = first + (uint32_t)(p0 + (int32_t)at.lo - start);
+    if (rest & 1u)
+        append_values<T, W, DP / 128>(a, at, lds);
+    else if (a.q.half)
+        append_keys<T, W, DP / 8 / W, true>(a, at);
+    else
+        append_keys<T, W, DP / 8 / W, false>(a, at);
 }
 
 template <class T, int P, int N>
@@ -322,13 +396,13 @@ __device__ __forceinline__ void rotate_queries_by(const AppendArgs &a, uint32_t 
     }
 }
 
-template <class T, int NV>
+template <class T, int DP, int W>
 __global__ __launch_bounds__(256) void w8a16_kv_append_kernel(AppendArgs a)
 {
-    __shared__ __attribute__((aligned(16))) uint8_t lds[4][NV * 32 * kBlock];
+    __shared__ __attribute__((aligned(16))) uint8_t lds[4][DP / 8 * kChunkPitch];
     if (blockIdx.x < a.kv_groups) {
         const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-        append_block<T, NV>(a, blockIdx.x * 4u + wave, lds[wave]);
+        append_block<T, DP, W>(a, blockIdx.x * 4u + wave, lds[wave]);
         return;
     }
     const uint32_t g = blockIdx.x - a.kv_groups;
@@ -339,18 +413,23 @@ __global__ __launch_bounds__(256) void w8a16_kv_append_kernel(AppendArgs a)
         rotate_queries_by<T, kRopeHeads>(a, t, part);
 }
 
-template <class T>
-hipError_t launch_type(const AppendArgs &a, hipStream_t stream)
+template <class T, int DP>
+hipError_t launch_width(const AppendArgs &a, hipStream_t stream)
 {
     const uint32_t tokens = a.q.x ? a.seqs.tokens : 0u;
     const dim3 grid(a.kv_groups + tokens * a.q_groups), block(256);
-    switch ((a.pool.dim + 63u) / 64u) {
-    case 1: hipLaunchKernelGGL((w8a16_kv_append_kernel<T, 2>), grid, block, 0, stream, a); break;
-    case 2: hipLaunchKernelGGL((w8a16_kv_append_kernel<T, 4>), grid, block, 0, stream, a); break;
-    case 3: hipLaunchKernelGGL((w8a16_kv_append_kernel<T, 6>), grid, block, 0, stream, a); break;
-    default: hipLaunchKernelGGL((w8a16_kv_append_kernel<T, 8>), grid, block, 0, stream, a); break;
+    switch (a.vec) {
+    case 8: hipLaunchKernelGGL((w8a16_kv_append_kernel<T, DP, 8>), grid, block, 0, stream, a); break;
+    case 4: hipLaunchKernelGGL((w8a16_kv_append_kernel<T, DP, 4>), grid, block, 0, stream, a); break;
+    default: hipLaunchKernelGGL((w8a16_kv_append_kernel<T, DP, 1>), grid, block, 0, stream, a); break;
     }
     return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch_type(const AppendArgs &a, hipStream_t stream)
+{
+    return a.pool.dim <= 128 ? launch_width<T, 128>(a, stream) : launch_width<T, 256>(a, stream);
 }
 
 }  // namespace
