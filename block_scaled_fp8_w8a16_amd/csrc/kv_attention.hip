@@ -98,6 +98,69 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void w8a16_kv_rows_kernel(A
     const uint32_t rtile = rest % a.row_tiles, chunk = rest / a.row_tiles;
     const uint32_t head = grp % pool.heads, b = grp / pool.heads;
 
+    const uint32_t kx = col >> 2, kr = col & 3u;   // the lane's block and row of the K operand
+    // The tile's four page numbers are read through the scalar cache (a
+    // vector load would have to be waited for together with the tiles in
+    // flight) and picked by lane.
+    typedef const __attribute__((address_space(4))) int32_t *scalar_ptr;
+    const scalar_ptr bt = (scalar_ptr)(uintptr_t)(a.seqs.block_table + (size_t)b * a.seqs.bt_stride);
+    // Blocks past `last_block` are read as that one; none of their keys is
+    // visible.
+    auto place = [&](uint32_t tile, uint32_t last_block) {
+        uint32_t page[4];
+        const uint32_t last_col = a.seqs.bt_width - 1u;
+#pragma unroll
+        for (uint32_t x = 0; x < 4; ++x) {
+            const uint32_t c = pool.by_blocks.div(4u * tile + x < last_block ? 4u * tile + x : last_block);
+            page[x] = (uint32_t)bt[c < last_col ? c : last_col];
+        }
+        auto pick = [&](uint32_t x, uint32_t &pg, uint32_t &slot) {
+            const uint32_t lo = x & 1u ? page[1] : page[0], hi = x & 1u ? page[3] : page[2];
+            const uint32_t blk = 4u * tile + x < last_block ? 4u * tile + x : last_block;
+            const uint32_t c = pool.by_blocks.div(blk);
+            pg = x & 2u ? hi : lo;
+            slot = head * pool.blocks + blk - c * pool.blocks;
+            const bool ok = pg < pool.pages && c <= last_col;
+            pg = ok ? pg : 0u;
+            return ok;
+        };
+        TileAt at;
+        uint32_t pk, sk, pv, sv;
+        pick(kx, pk, sk);
+        at.ok = pick(g, pv, sv);
+        at.k = pool.k + pk * pool.k_page + ((size_t)sk * 16u + kr) * pool.dim;
+        at.v = pool.v + pv * pool.v_page + ((size_t)sv * pool.dim + col) * 16u;
+        at.ks = pool.k_scale[pv * pool.ks_page + sv];
+        at.vs = pool.v_scale[pv * pool.vs_page + sv];
+        return at;
+    };
+    auto load = [&](const TileAt &at, u32x4_t (&k)[QC][4], u32x4_t (&v)[VT]) {
+#pragma unroll
+        for (int i = 0; i < QC; ++i) {
+            // channels past the head meet queries of zero: read any of the row
+            const uint32_t d = 64u * i + 16u * g;
+            const uint8_t *p = at.k + (d < pool.dim ? d : 0u);
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                k[i][x] = *reinterpret_cast<const u32x4_t *>(p + (size_t)(4 * x) * pool.dim);
+        }
+#pragma unroll
+        for (int x = 0; x < VT; ++x)
+            v[x] = *reinterpret_cast<const u32x4_t *>(at.v + (16u * x < pool.dim ? 256u * x : 0u));
+    };
+
+    // Without a window the first chunk starts with key 0 whatever the
+    // sequence's length: its first tiles are under way before the length is
+    // known.  (Past the sequence's end the block table may hold anything:
+    // what no page of the cache is reads as page 0.)
+    u32x4_t k[QC][4], v[VT];
+    TileAt at;
+    const bool early = chunk == 0 && !a.window;
+    if (early) {
+        at = place(wave, ~0u);
+        load(at, k, v);
+    }
+
     RowTile t;
     if (!seq_extent(a.seqs, b, t))
         return;
@@ -117,7 +180,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void w8a16_kv_rows_kernel(A
                              ? tiles : begin + a.chunk_tiles;
     const bool alone = a.chunks == 1 || tiles <= a.chunk_tiles;
 
-    // queries: column col of matrix rb is row row0 + 16 rb + col; the lane's
+    // queries: column col is row row0 + col; the lane's
     // channels of group i are 64 i + 16 g .. + 15 (8 for each of two products)
     u32x4_t q[QC][2];
     int32_t rlo, rhi;
@@ -152,51 +215,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void w8a16_kv_rows_kernel(A
         o[v] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     int32_t exp_ref = kNoExp;
 
-    const uint32_t last_block = t.kv_len > 0 ? (uint32_t)(t.kv_len - 1) / 16u : 0u;
-    const int32_t *bt = a.seqs.block_table + (size_t)b * a.seqs.bt_stride;
-    const uint32_t kx = col >> 2, kr = col & 3u;   // the lane's block and row of the K operand
-
-    // Page and place of block 4 * tile + x.  Blocks past the sequence are
-    // read as its last one; none of their keys is visible.
-    auto locate = [&](uint32_t tile, uint32_t x, uint32_t &page, uint32_t &slot) {
-        uint32_t blk = 4u * tile + x;
-        blk = blk < last_block ? blk : last_block;
-        const uint32_t c = pool.by_blocks.div(blk);
-        slot = head * pool.blocks + blk - c * pool.blocks;
-        const bool in = c < a.seqs.bt_width;
-        page = (uint32_t)bt[in ? c : 0u];
-        page = in ? page : pool.pages;
-    };
-    auto place = [&](uint32_t tile) {
-        TileAt at;
-        uint32_t pk, sk, pv, sv;
-        locate(tile, kx, pk, sk);
-        locate(tile, g, pv, sv);
-        at.ok = pv < pool.pages;
-        pk = pk < pool.pages ? pk : 0u;
-        pv = at.ok ? pv : 0u;
-        at.k = pool.k + pk * pool.k_page + ((size_t)sk * 16u + kr) * pool.dim;
-        at.v = pool.v + pv * pool.v_page + ((size_t)sv * pool.dim + col) * 16u;
-        at.ks = pool.k_scale[pv * pool.ks_page + sv];
-        at.vs = pool.v_scale[pv * pool.vs_page + sv];
-        return at;
-    };
-    auto load = [&](const TileAt &at, u32x4_t (&k)[QC][4], u32x4_t (&v)[VT]) {
-#pragma unroll
-        for (int i = 0; i < QC; ++i) {
-            // channels past the head meet queries of zero: read any of the row
-            const uint32_t d = 64u * i + 16u * g;
-            const uint8_t *p = at.k + (d < pool.dim ? d : 0u);
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-                k[i][x] = *reinterpret_cast<const u32x4_t *>(p + (size_t)(4 * x) * pool.dim);
-        }
-#pragma unroll
-        for (int x = 0; x < VT; ++x)
-            v[x] = *reinterpret_cast<const u32x4_t *>(at.v + (16u * x < pool.dim ? 256u * x : 0u));
-    };
-
-    auto compute = [&](uint32_t tile, const TileAt &at, const u32x4_t (&k)[QC][4], u32x4_t (&v)[VT]) {
+    auto compute = [&](uint32_t tile) {
         const int32_t key0 = (int32_t)(tile * kKvTile + 16u * g);   // the lane's first key
         const float ksc = at.ok && at.ks - 1u < 254u ? pow2_byte(at.ks) * a.scale_log2
                                                      : __builtin_nanf("");
@@ -341,14 +360,16 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void w8a16_kv_rows_kernel(A
     // next tile's loads are in flight while one is computed
     uint32_t tile = begin + wave;
     if (tile < end) {
-        u32x4_t k[QC][4], v[VT];
-        TileAt at = place(tile0 + tile);
-        load(at, k, v);
+        const uint32_t last_block = t.kv_len > 0 ? (uint32_t)(t.kv_len - 1) / 16u : 0u;
+        if (!early) {
+            at = place(tile0 + tile, last_block);
+            load(at, k, v);
+        }
         while (tile + kWaves < end) {
             u32x4_t kn[QC][4], vn[VT];
-            const TileAt next = place(tile0 + tile + kWaves);
+            const TileAt next = place(tile0 + tile + kWaves, last_block);
             load(next, kn, vn);
-            compute(tile0 + tile, at, k, v);
+            compute(tile0 + tile);
             at = next;
 #pragma unroll
             for (int i = 0; i < QC; ++i)
@@ -360,7 +381,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void w8a16_kv_rows_kernel(A
                 v[x] = vn[x];
             tile += kWaves;
         }
-        compute(tile0 + tile, at, k, v);
+        compute(tile0 + tile);
     }
 
     // join the waves: a common reference per row and a common exponent
