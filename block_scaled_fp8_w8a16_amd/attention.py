@@ -59,7 +59,7 @@ class KVAppendArgs(ctypes.Structure):
 
 class KVPlan(ctypes.Structure):
     """w8a16_kv_plan_t"""
-    _fields_ = [("kernel", _u32), ("row_blocks", _u32), ("row_tiles", _u32), ("chunk_tiles", _u32),
+    _fields_ = [("kernel", _u32), ("row_blocks", _u32), ("waves", _u32), ("row_tiles", _u32), ("chunk_tiles", _u32),
                 ("chunks", _u32), ("grid", _u32), ("workspace_bytes", _u64)]
 
     def as_dict(self) -> dict:

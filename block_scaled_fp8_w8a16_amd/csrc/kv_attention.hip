@@ -41,7 +41,6 @@ namespace {
 
 using namespace dev;
 
-constexpr int kWaves = 4;
 constexpr float kLazy = 8.0f;       // log2 growth of a row's maximum that is left alone
 constexpr int32_t kHeadroom = 7;    // V operands reach 448 * 2^7 < 65504
 constexpr int32_t kNoExp = -100000;
@@ -71,19 +70,20 @@ struct TileAt {
     bool ok;
 };
 
-template <class Q, int DP>
-__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void w8a16_kv_rows_kernel(AttnArgs a)
+template <class Q, int DP, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w8a16_kv_rows_kernel(AttnArgs a)
 {
     constexpr int QC = DP / 64;       // 64-channel groups of the first product
     constexpr int VT = DP / 16;       // 16-channel tiles of the second
-    constexpr int SEG = DP < 128 ? DP : 128;
+    constexpr uint32_t THREADS = 64 * WAVES;
+    constexpr int SEG = DP < 128 || WAVES > 4 ? 64 : 128;    // channels joined at a time
     constexpr int NR = 16;            // rows
     constexpr int PART = 16 * (SEG + 4);
-    static_assert(kWaves * PART >= (int)kKvMaxChunks * NR && kWaves * PART >= 4 * 256, "LDS of the join");
-    __shared__ __attribute__((aligned(16))) float part[kWaves * PART];   // [wave][16][SEG + 4]
-    __shared__ float stat[kWaves][NR][2];
-    __shared__ float red[512];
-    __shared__ int32_t exps[kWaves];
+    static_assert(WAVES * PART >= (int)kKvMaxChunks * NR && WAVES * PART >= 4 * (int)THREADS, "LDS of the join");
+    __shared__ __attribute__((aligned(16))) float part[WAVES * PART];   // [wave][16][SEG + 4]
+    __shared__ float stat[WAVES][NR][2];
+    __shared__ float red[2 * THREADS];
+    __shared__ int32_t exps[WAVES];
     __shared__ uint32_t last;
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -365,9 +365,9 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void w8a16_kv_rows_kernel(A
             at = place(tile0 + tile, last_block);
             load(at, k, v);
         }
-        while (tile + kWaves < end) {
+        while (tile + WAVES < end) {
             u32x4_t kn[QC][4], vn[VT];
-            const TileAt next = place(tile0 + tile + kWaves, last_block);
+            const TileAt next = place(tile0 + tile + WAVES, last_block);
             load(next, kn, vn);
             compute(tile0 + tile);
             at = next;
@@ -379,7 +379,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void w8a16_kv_rows_kernel(A
 #pragma unroll
             for (int x = 0; x < VT; ++x)
                 v[x] = vn[x];
-            tile += kWaves;
+            tile += WAVES;
         }
         compute(tile0 + tile);
     }
@@ -396,7 +396,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void w8a16_kv_rows_kernel(A
     __syncthreads();
     int32_t exp_all = exps[0];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w)
+    for (int w = 1; w < WAVES; ++w)
         exp_all = exp_all > exps[w] ? exp_all : exps[w];
     const float efac = exp_ref == kNoExp ? 0.f : exp2_fast((float)(exp_ref - exp_all));
     const uint32_t n_rows = t.rows - t.row0 < (uint32_t)NR ? t.rows - t.row0 : (uint32_t)NR;
@@ -410,17 +410,18 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void w8a16_kv_rows_kernel(A
     const float unit = exp_all == kNoExp ? 0.f : ldexpf(1.0f, exp_all);
     float mall = kNegInf;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w)
+    for (int w = 0; w < WAVES; ++w)
         mall = fmaxf(mall, stat[w][col][0]);
     // a wave that saw no key of the row (m = -inf) adds zeros
     const float wave_fac = m == kNegInf ? 0.f : efac * exp2_fast(m - mall);
-    const uint32_t tr = threadIdx.x >> 4, row = t.row0 + tr;
+    constexpr uint32_t TPR = THREADS / NR;       // threads per row
+    const uint32_t tr = threadIdx.x / TPR, row = t.row0 + tr;
     float mr = kNegInf, lr = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w)
+    for (int w = 0; w < WAVES; ++w)
         mr = fmaxf(mr, stat[w][tr][0]);
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w)
+    for (int w = 0; w < WAVES; ++w)
         lr += stat[w][tr][1] *     // m = -inf: l is 0, or NaN
               (stat[w][tr][0] == kNegInf ? 1.f : exp2_fast(stat[w][tr][0] - mr));
     const uint32_t tok = a.by_group.div(row), hq = head * a.group + row - tok * a.group;
@@ -440,13 +441,13 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void w8a16_kv_rows_kernel(A
         if (tr >= n_rows)
             continue;
 #pragma unroll
-        for (int i = 0; i < SEG / 64; ++i) {
-            const uint32_t c = 4u * (threadIdx.x & 15u) + 64u * i;
-            if (s0 + c >= pool.dim)
+        for (uint32_t i = 0; i < SEG; i += 4 * TPR) {
+            const uint32_t c = 4u * (threadIdx.x % TPR) + i;
+            if (c >= (uint32_t)SEG || s0 + c >= pool.dim)
                 continue;
             f32x4_t acc = *reinterpret_cast<const f32x4_t *>(&part[tr * (SEG + 4) + c]);
 #pragma unroll
-            for (int w = 1; w < kWaves; ++w)
+            for (int w = 1; w < WAVES; ++w)
                 acc += *reinterpret_cast<const f32x4_t *>(&part[w * PART + tr * (SEG + 4) + c]);
             if (alone)
                 store_row4(dst + s0 + c, acc * inv);
@@ -454,7 +455,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void w8a16_kv_rows_kernel(A
                 store_agent(wo + ((size_t)chunk * NR + tr) * dim4 + (s0 + c) / 4, acc);
         }
     }
-    if (tr < n_rows && (threadIdx.x & 15u) == 0) {
+    if (tr < n_rows && threadIdx.x % TPR == 0) {
         if (!alone)
             store_agent(wst + (size_t)chunk * NR + tr, f32x4_t{mr, lr, (float)exp_all, 0.f});
         else if (a.lse)
@@ -481,7 +482,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void w8a16_kv_rows_kernel(A
     if (tid == 0)      // ready for the next call that uses this workspace
         __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     // statistics: thread (row sr, every SG-th chunk from sg on)
-    constexpr uint32_t SG = 256 / NR, PER = kKvMaxChunks / SG;
+    constexpr uint32_t SG = THREADS / NR, PER = kKvMaxChunks / SG;
     const uint32_t sr = tid % NR, sg = tid / NR;
     f32x4_t st[PER];
     float mj = kNegInf, ex = (float)kNoExp;
@@ -497,11 +498,11 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void w8a16_kv_rows_kernel(A
         ex = fmaxf(ex, st[i].z);
     }
     red[tid] = mj;
-    red[256 + tid] = ex;
+    red[THREADS + tid] = ex;
     __syncthreads();
     for (uint32_t k = 0; k < SG; ++k) {
         mj = fmaxf(mj, red[k * NR + sr]);
-        ex = fmaxf(ex, red[256 + k * NR + sr]);
+        ex = fmaxf(ex, red[THREADS + k * NR + sr]);
     }
     float lj = 0.f;
     float *const fac = part;      // [chunk][row]
@@ -515,22 +516,22 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void w8a16_kv_rows_kernel(A
     __syncthreads();
     red[tid] = lj;
     if (sg == 0) {
-        red[256 + sr] = mj;
-        red[256 + NR + sr] = ex;
+        red[THREADS + sr] = mj;
+        red[THREADS + NR + sr] = ex;
     }
     __syncthreads();
     if (tid < (uint32_t)NR) {
         lj = 0.f;
         for (uint32_t k = 0; k < SG; ++k)
             lj += red[k * NR + tid];
-        red[256 + 2 * NR + tid] = lj;
+        red[THREADS + 2 * NR + tid] = lj;
     }
     __syncthreads();
     // outputs: four channels of one row per thread; where that leaves half
     // of the threads or more without any, they share the chunks
     const uint32_t items = n_rows * dim4;
-    const uint32_t teams = items <= 128 ? 256u / items : 1u;
-    for (uint32_t base = 0; base < items; base += 256) {
+    const uint32_t teams = items <= THREADS / 2 ? THREADS / items : 1u;
+    for (uint32_t base = 0; base < items; base += THREADS) {
         const uint32_t team = teams > 1 ? tid / items : 0u, it = base + (teams > 1 ? tid - team * items : tid);
         const bool on = it < items && team < teams;
         const uint32_t jr = on ? it / dim4 : 0u, c4 = on ? it - jr * dim4 : 0u;
@@ -557,7 +558,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void w8a16_kv_rows_kernel(A
         }
         if (!on || team)
             continue;
-        const float mg = red[256 + jr], eg = red[256 + NR + jr], lg = red[256 + 2 * NR + jr];
+        const float mg = red[THREADS + jr], eg = red[THREADS + NR + jr], lg = red[THREADS + 2 * NR + jr];
         const uint32_t jtok = a.by_group.div(t.row0 + jr), jh = head * a.group + t.row0 + jr - jtok * a.group;
         const bool empty = mg == kNegInf && lg == 0.f;
         const float scale = empty ? 0.f : 1.0f / lg * ldexpf(1.0f, (int)eg);
@@ -671,7 +672,13 @@ __global__ __launch_bounds__(256) void w8a16_kv_join_kernel(AttnArgs a, uint32_t
 template <class Q, int DP>
 hipError_t launch_dim(const AttnArgs &a, const w8a16_kv_plan_t &p, hipStream_t stream)
 {
-    hipLaunchKernelGGL((w8a16_kv_rows_kernel<Q, DP>), dim3(p.grid), dim3(256), 0, stream, a);
+    if constexpr (DP <= 128) {
+        if (p.waves == 8) {
+            hipLaunchKernelGGL((w8a16_kv_rows_kernel<Q, DP, 8>), dim3(p.grid), dim3(512), 0, stream, a);
+            return hipGetLastError();
+        }
+    }
+    hipLaunchKernelGGL((w8a16_kv_rows_kernel<Q, DP, 4>), dim3(p.grid), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 

@@ -22,11 +22,13 @@ uint64_t div_up(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 int kv_plan_finalize(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_heads,
                      uint32_t kv_heads, uint32_t head_dim, uint32_t window, w8a16_kv_plan_t *p)
 {
-    const bool rows_ok = p->kernel == W8A16_KV_ROWS && p->row_blocks == 1;
-    const bool tile_ok = p->kernel == W8A16_KV_TILE && p->row_blocks == 8;
+    const bool rows_ok = p->kernel == W8A16_KV_ROWS && p->row_blocks == 1 &&
+                         (p->waves == 4 || (p->waves == 8 && head_dim <= 128));
+    const bool tile_ok = p->kernel == W8A16_KV_TILE && p->row_blocks == 8 && p->waves == 4;
     if ((!rows_ok && !tile_ok) || p->chunk_tiles < 1)
         return fail(W8A16_ERR_BAD_PLAN, "w8a16_kv_attention: plan needs kernel W8A16_KV_ROWS with "
-                                        "row_blocks 1, or W8A16_KV_TILE with row_blocks 8, and "
+                                        "row_blocks 1 and 4 waves (or 8, of heads up to 128), or "
+                                        "W8A16_KV_TILE with row_blocks 8 and 4 waves, and "
                                         "chunk_tiles of at least 1");
     // the tiles a row tile can see: all of the cache, or the window's and
     // those its rows' positions add
@@ -75,6 +77,7 @@ int make_kv_plan(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_he
     const uint64_t rows = (uint64_t)max_new * (q_heads / kv_heads);
     p.kernel = rows <= 32 ? W8A16_KV_ROWS : W8A16_KV_TILE;
     p.row_blocks = p.kernel == W8A16_KV_ROWS ? 1 : 8;
+    p.waves = 4;
     p.chunk_tiles = 1u << 30;
     int st = kv_plan_finalize(seqs, max_new, max_kv, q_heads, kv_heads, head_dim, window, &p);
     if (st != W8A16_OK)
@@ -83,12 +86,20 @@ int make_kv_plan(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_he
                                 ? (uint64_t)window + max_new : max_kv, kKeysPerTile) + (window ? 1 : 0);
     if (tiles < 1)
         tiles = 1;
-    // Cut the keys until the CUs are full: two workgroups each, one of heads
-    // above 128 channels (their registers).  A wave keeps at least two tiles,
-    // and a cut has to spare more than kCutTiles tiles of a workgroup's time,
-    // about what joining the chunks costs.
-    const uint64_t slots = head_dim <= 128 ? 2 * cus : cus;
-    uint64_t per = div_up(tiles * p.grid, slots);
+    // Cut the keys while that leaves no more workgroups than run at once: two
+    // per CU, one of 8 waves or of heads above 128 channels.  Eight waves
+    // where the row tiles alone do not give every CU a workgroup: half as
+    // many chunks to join (131072 tokens of 8 KV heads 66 -> 57 us, 3
+    // sequences of 9000 15.4 -> 14.6), but slower where several rounds of
+    // short workgroups run (256 sequences of 500 46 -> 74 us).  A cut has to
+    // spare more than kCutTiles tiles of a workgroup's time, about what the
+    // join costs, and a chunk has at least 8 tiles.
+    const bool narrow = head_dim <= 128;
+    if (p.kernel == W8A16_KV_ROWS && narrow && p.grid <= cus)
+        p.waves = 8;
+    const uint64_t slots = narrow && p.waves == 4 ? 2 * cus : cus;
+    const uint64_t cuts = slots > p.grid ? slots / p.grid : 1;
+    uint64_t per = div_up(tiles, cuts);
     if (per < 8)
         per = 8;
     if (p.kernel == W8A16_KV_ROWS && per < div_up(tiles, kKvMaxChunks))

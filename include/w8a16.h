@@ -489,7 +489,7 @@ int w8a16_kv_append(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
 /* Launch plan of the attention. */
 typedef enum w8a16_kv_kernel {
     /* Row kernel: a workgroup takes 16 (query, head) rows of one KV head
-     * (row_blocks 1) and a chunk of the keys; its four waves take interleaved
+     * (row_blocks 1) and a chunk of the keys; its waves take interleaved
      * 64-key tiles straight from the cache into matrix operands.  The last
      * chunk of a row tile to finish joins them (at most 128). */
     W8A16_KV_ROWS = 1,
@@ -500,6 +500,7 @@ typedef enum w8a16_kv_kernel {
 typedef struct w8a16_kv_plan {
     uint32_t kernel;          /* w8a16_kv_kernel */
     uint32_t row_blocks;      /* 16-row blocks per workgroup: rows 1, tile 8 */
+    uint32_t waves;           /* waves per workgroup: 4; rows also 8, of heads up to 128 */
     uint32_t row_tiles;       /* row tiles of the longest sequence (derived) */
     uint32_t chunk_tiles;     /* 64-key tiles per chunk */
     uint32_t chunks;          /* chunks the longest sequence is cut into (derived) */

@@ -488,10 +488,12 @@ def test_attention(w8, case):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("chunk_tiles", [1, 2, 3, 100])
+@pytest.mark.parametrize("waves,chunk_tiles", [(4, 1), (4, 2), (4, 3), (4, 100), (8, 1), (8, 2), (8, 100)])
 @pytest.mark.parametrize("case", [1, 3, 6, 8, 10, 13], ids=str)
-def test_attention_plans(w8, chunk_tiles, case):
-    plan = w8.KVPlan(kernel=w8.KV_KERNEL_ROWS, row_blocks=1, chunk_tiles=chunk_tiles)
+def test_attention_plans(w8, waves, chunk_tiles, case):
+    if waves == 8 and ATTEND[case][4] > 128:
+        waves, chunk_tiles = 4, 4
+    plan = w8.KVPlan(kernel=w8.KV_KERNEL_ROWS, row_blocks=1, waves=waves, chunk_tiles=chunk_tiles)
     check_attention(w8, *ATTEND[case], seed=200, plan=plan)
 
 
@@ -499,7 +501,7 @@ def test_attention_plans(w8, chunk_tiles, case):
 @pytest.mark.parametrize("chunk_tiles", [1, 2, 100])
 @pytest.mark.parametrize("case", range(len(ATTEND)), ids=str)
 def test_attention_tile_kernel(w8, chunk_tiles, case):
-    plan = w8.KVPlan(kernel=w8.KV_KERNEL_TILE, row_blocks=8, chunk_tiles=chunk_tiles)
+    plan = w8.KVPlan(kernel=w8.KV_KERNEL_TILE, row_blocks=8, waves=4, chunk_tiles=chunk_tiles)
     check_attention(w8, *ATTEND[case], seed=250, plan=plan, padded=chunk_tiles == 2,
                     strided=chunk_tiles == 2)
 
@@ -514,7 +516,7 @@ def test_attention_tile_kernel(w8, chunk_tiles, case):
 def test_attention_many_rows(w8, case):
     check_attention(w8, *case, seed=260)
     for kernel, blocks, tiles in ((w8.KV_KERNEL_TILE, 8, 3), (w8.KV_KERNEL_ROWS, 1, 4)):
-        plan = w8.KVPlan(kernel=kernel, row_blocks=blocks, chunk_tiles=tiles)
+        plan = w8.KVPlan(kernel=kernel, row_blocks=blocks, waves=4, chunk_tiles=tiles)
         check_attention(w8, *case, seed=261, plan=plan)
 
 
@@ -523,7 +525,7 @@ def test_attention_many_rows(w8, case):
 def test_attention_strides_and_small_bounds(w8, case):
     # padded pages, strided queries and outputs, offsets given though uniform,
     # and a max_kv below the longest sequence (the last chunk takes the rest)
-    plan = w8.KVPlan(kernel=w8.KV_KERNEL_ROWS, row_blocks=1, chunk_tiles=1)
+    plan = w8.KVPlan(kernel=w8.KV_KERNEL_ROWS, row_blocks=1, waves=4, chunk_tiles=1)
     check_attention(w8, *ATTEND[case], seed=300, padded=True, strided=True, uniform=False)
     check_attention(w8, *ATTEND[case], seed=301, plan=plan, max_kv=64)
 
@@ -562,7 +564,7 @@ def test_attention_hidden_nan_does_not_leak(w8, case):
     check_attention(w8, *ATTEND[case], seed=600, mutate=mutate)
     for tiles in (1, 2):
         for kernel, blocks in ((w8.KV_KERNEL_ROWS, 1), (w8.KV_KERNEL_TILE, 8)):
-            plan = w8.KVPlan(kernel=kernel, row_blocks=blocks, chunk_tiles=tiles)
+            plan = w8.KVPlan(kernel=kernel, row_blocks=blocks, waves=4, chunk_tiles=tiles)
             check_attention(w8, *ATTEND[case], seed=601, mutate=mutate, plan=plan)
 
 
@@ -575,7 +577,7 @@ def test_attention_unwritten_block_is_nan(w8, byte):
     check_attention(w8, [20, 20], [60, 60], 4, 2, 64, 32, seed=700, mutate=mutate)
     # blocks that every row sees, in the kernels' loops without masks
     for kernel, blocks in ((w8.KV_KERNEL_ROWS, 1), (w8.KV_KERNEL_TILE, 8)):
-        plan = w8.KVPlan(kernel=kernel, row_blocks=blocks, chunk_tiles=100)
+        plan = w8.KVPlan(kernel=kernel, row_blocks=blocks, waves=4, chunk_tiles=100)
         check_attention(w8, [20, 20], [360, 460], 4, 2, 64, 32, seed=701, mutate=mutate, plan=plan)
 
 
@@ -596,9 +598,10 @@ def test_attention_page_outside_the_cache_is_nan(w8):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("plan", [dict(row_blocks=0), dict(row_blocks=2), dict(kernel=3),
-                                  dict(kernel=2, row_blocks=2), dict(chunk_tiles=0)])
+                                  dict(kernel=2, row_blocks=2), dict(chunk_tiles=0), dict(waves=0),
+                                  dict(waves=6), dict(kernel=2, row_blocks=8, waves=8)])
 def test_attention_plan_refusals(w8, plan):
-    p = w8.KVPlan(**dict(dict(kernel=1, row_blocks=1, chunk_tiles=1), **plan))
+    p = w8.KVPlan(**dict(dict(kernel=1, row_blocks=1, waves=4, chunk_tiles=1), **plan))
     cache = ref.Cache(1, 1, 16, 16, None).to(w8)
     q = torch.ones(1, 1, 16, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(w8.W8A16Error) as e:
