@@ -3,21 +3,34 @@
 // The mathematics is that of the row kernel (kv_attention.hip): S^T = K Q^T,
 // p = 2^(S k_scale scale log2(e) - m) with a reference m that moves only by
 // more than 2^8, O^T += V^T p^T with p in FP16 and V widened by 2^(e - E).
-// Here the products bound the time, so a workgroup takes 128 rows and its
-// four waves 32 each, with 32x32x16 matrix instructions:
-//   * 64 keys at a time, K and V as codes, staged in LDS by DMA (each wave
-//     brings one block of 16 keys; page lookups are scalar) while the
-//     previous 64 are computed: two buffers, one barrier per tile.
+// The issue of vector instructions bounds the time: a wave needs about 330
+// of them (exponentials, conversions of codes and p, sums, LDS reads) beside
+// the 64 matrix instructions of 64 keys and 128 channels.  So a workgroup
+// takes 128 rows, its four waves 32 each with 32x32x16 matrix instructions,
+// two workgroups share a CU where registers allow (up to 128 channels), and:
+//   * 64 keys at a time, K and V as codes (half of what 16-bit operands
+//     would read from LDS), brought to LDS by DMA three tiles ahead: four
+//     buffers, one barrier per tile.  Each wave brings one block of 16 keys;
+//     page lookups are scalar.
 //   * Row 8a + 4h + b of the K operand holds key 16h + 4a + b, so a lane
 //     ends up with the 16 scores of one block in order, and its p are the
 //     second product's operand as they stand, whose other side is one
-//     16-byte read of V (16 keys of one channel).
+//     16-byte read of V (16 keys of one channel), widened in registers.
 //   * K rows lie in LDS with their 16-byte chunks permuted (xor) so that the
 //     8 lanes served together hit different banks; V needs no permutation.
-// Codes are widened in registers, 128 conversions per 32 matrix
-// instructions and wave; keeping codes in LDS halves its reads.  Two
-// workgroups share a CU, so that one wave's exponentials and conversions
-// run under the other's matrix instructions.
+//   * Tiles that every row sees take a loop without masks.  In it the first
+//     products run at a raised wave priority, so that the waves of a SIMD
+//     fall out of step and one's exponentials run under another's matrix
+//     instructions; the second product follows each half's exponentials at
+//     once.
+// Measured, 2 x 2048 rows of 8 heads over 8192 keys of 128 channels: 488 to
+// 498 us by run, 965 to 986 TFLOP/s (a plain FP16 matrix product of 8192^3
+// reaches 1151 here).  Before the priority 512, with two buffers and one
+// loop for all tiles 530.  Slower: widening once per workgroup into LDS as
+// 16-bit operands 584, the next tile's scores under this one's exponentials
+// 602, the raised priority for the second product as well 503 or for the
+// exponentials 516.  FP8 products of queries split in two E4M3 numbers took
+// 508 and summed too coarsely (errors of 2e-3 in a row's log-sum).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -39,10 +52,7 @@ constexpr uint32_t kRows = 128;      // rows per workgroup
 constexpr float kLazy = 8.0f;
 constexpr int32_t kHeadroom = 7;
 constexpr int32_t kNoExp = -100000;
-
-template <bool V> struct Constant {
-    static constexpr bool value = V;
-};
+constexpr uint32_t kBuffers = 4;     // tiles in LDS: one in use, three on their way
 
 template <class Q> __device__ __forceinline__ f32x16_t mfma32(u32x4_t a, u32x4_t b, f32x16_t c);
 template <> __device__ __forceinline__ f32x16_t mfma32<QueryBf16>(u32x4_t a, u32x4_t b, f32x16_t c)
@@ -70,11 +80,12 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
     constexpr int QC = DP / 32;             // 32-channel groups of the first product
     constexpr int VT = DP / 32;             // 32-channel tiles of the second
     constexpr uint32_t BLK = 16 * DP;       // LDS bytes of one block of K, and of V
+    constexpr uint32_t BUF = 8 * BLK;       // of one buffer
     constexpr uint32_t SWZ = DP == 128 || DP == 256 ? 7 : 3;
     struct Scale { uint32_t ks, vs; };
-    // two buffers of K and V codes, then the blocks' scale bytes
+    // kBuffers buffers of K and V codes, then the blocks' scale bytes
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    Scale (*const scl)[4] = reinterpret_cast<Scale (*)[4]>(lds + 16 * BLK);
+    Scale (*const scl)[4] = reinterpret_cast<Scale (*)[4]>(lds + kBuffers * BUF);
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t col = lane & 31u, h = lane >> 5;
@@ -121,21 +132,25 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
     {
         const typename Q::elem *src = reinterpret_cast<const typename Q::elem *>(a.q) +
                                       (int64_t)(t.first + tok) * a.q_token + (int64_t)hq * a.q_head;
-#pragma unroll
-        for (int i = 0; i < QC; ++i) {
-            const uint32_t d = 32u * i + 16u * h;
-            q[i][0] = q[i][1] = u32x4_t{0u, 0u, 0u, 0u};
+        const bool wide = (reinterpret_cast<uintptr_t>(src) & 15u) == 0;
+        auto eight = [&](uint32_t d) {
+            u32x4_t v = {0u, 0u, 0u, 0u};
             if (row < t.rows && d < pool.dim) {
-                if ((reinterpret_cast<uintptr_t>(src) & 15u) == 0) {
-                    q[i][0] = *reinterpret_cast<const u32x4_t *>(src + d);
-                    q[i][1] = *reinterpret_cast<const u32x4_t *>(src + d + 8);
+                if (wide) {
+                    v = *reinterpret_cast<const u32x4_t *>(src + d);
                 } else {
                     const uint16_t *s16 = reinterpret_cast<const uint16_t *>(src + d);
 #pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        q[i][x >> 2][x & 3] = (uint32_t)s16[2 * x] | ((uint32_t)s16[2 * x + 1] << 16);
+                    for (int x = 0; x < 4; ++x)
+                        v[x] = (uint32_t)s16[2 * x] | ((uint32_t)s16[2 * x + 1] << 16);
                 }
             }
+            return v;
+        };
+#pragma unroll
+        for (int i = 0; i < QC; ++i) {
+            q[i][0] = eight(32u * i + 16u * h);
+            q[i][1] = eight(32u * i + 16u * h + 8u);
         }
     }
 
@@ -176,9 +191,9 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
         const uint8_t *vp = pool.v + p.page * pool.v_page + base;
 #pragma unroll
         for (int j = 0; j < DP / 64; ++j) {
-            __builtin_amdgcn_global_load_lds(kp + koff[j], (lds_void_t *)(lds + buf * (8 * BLK) + wave * BLK + 1024u * j),
+            __builtin_amdgcn_global_load_lds(kp + koff[j], (lds_void_t *)(lds + buf * BUF + wave * BLK + 1024u * j),
                                              16, 0, 0);
-            __builtin_amdgcn_global_load_lds(vp + voff[j], (lds_void_t *)(lds + buf * (8 * BLK) + (4 + wave) * BLK + 1024u * j),
+            __builtin_amdgcn_global_load_lds(vp + voff[j], (lds_void_t *)(lds + buf * BUF + (4 + wave) * BLK + 1024u * j),
                                              16, 0, 0);
         }
     };
@@ -203,78 +218,134 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
     const uint32_t kf = SWZ == 7 ? (krow & 3u) | ((krow >> 4) << 2) : ((krow >> 1) & 1u) | ((krow >> 4) << 1);
     const uint32_t kbase = krow * DP;
 
-    // MASKED: some row may not see all of the tile, or a block has no V scale.
-    auto compute = [&](uint32_t tile, uint32_t buf, auto masked_tag) {
-        constexpr bool MASKED = decltype(masked_tag)::value;
-        const int32_t tk = (int32_t)(tile * kKvTile);
-        float ksc[2], vsc[2];
-        int32_t e[2];
+    // Scores of 32 keys (half x of the tile), as the codes have them.
+    auto products = [&](uint32_t buf, int x) {
+        f32x16_t s;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const Scale s = scl[buf][2 * x + h];
-            ksc[x] = s.ks - 1u < 254u ? pow2_byte(s.ks) * a.scale_log2 : __builtin_nanf("");
-            e[x] = s.vs - 1u < 254u ? (int32_t)s.vs - 127 : kNoExp;
-            if (tk + 32 * x + 16 * (int32_t)h >= w.hi)
-                e[x] = kNoExp;
+        for (int i = 0; i < 16; ++i)
+            s[i] = 0.f;
+        const uint8_t *const kl = lds + buf * BUF + x * 2 * BLK + kbase;
+#pragma unroll
+        for (int i = 0; i < QC; ++i) {
+            const u32x4_t raw = *reinterpret_cast<const u32x4_t *>(kl + 16u * ((2u * i + h) ^ kf));
+            s = mfma32<Q>(Q::widen(raw.x, raw.y), q[i][0], s);
+            s = mfma32<Q>(Q::widen(raw.z, raw.w), q[i][1], s);
         }
-        int32_t emax = e[0] > e[1] ? e[0] : e[1];
-        const int32_t e_low = __builtin_amdgcn_readlane(emax, 0), e_high = __builtin_amdgcn_readlane(emax, 32);
-        emax = e_low > e_high ? e_low : e_high;
-        float vrescale = 1.0f;
+        return s;
+    };
+    auto v_frag = [&](uint32_t buf, int x, int d) {
+        return *reinterpret_cast<const u32x4_t *>(lds + buf * BUF + (4u + 2u * x + h) * BLK +
+                                                  (32u * d + col) * 16u);
+    };
+    // The outputs' unit for blocks up to 2^emax: what they change by.
+    auto unit_for = [&](int32_t emax) {
+        float f = 1.0f;
         if (emax > exp_ref + kHeadroom) {
-            vrescale = exp_ref == kNoExp ? 0.0f : exp2_fast((float)(exp_ref - emax));
+            f = exp_ref == kNoExp ? 0.0f : exp2_fast((float)(exp_ref - emax));
             exp_ref = emax;
         }
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-            vsc[x] = e[x] == kNoExp || e[x] - exp_ref < -120 ? pow2_byte(7)
-                                                             : pow2_byte((uint32_t)(e[x] - exp_ref + 127));
-
-        f32x16_t s[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                s[x][i] = 0.f;
-#pragma unroll
-            for (int i = 0; i < QC; ++i) {
-                const uint32_t c = (2u * i + h) ^ kf;
-                const u32x4_t raw = *reinterpret_cast<const u32x4_t *>(lds + buf * (8 * BLK) + x * 2 * BLK + kbase + 16u * c);
-                s[x] = mfma32<Q>(Q::widen(raw.x, raw.y), q[i][0], s[x]);
-                s[x] = mfma32<Q>(Q::widen(raw.z, raw.w), q[i][1], s[x]);
-            }
-        }
-        if (MASKED) {
-#pragma unroll
-            for (int x = 0; x < 2; ++x)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int32_t key = tk + 32 * x + 16 * (int32_t)h + i;
-                    s[x][i] = key >= rlo && key < rhi ? s[x][i] : kNegInf;
-                }
-        }
-        float mx[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            mx[x] = s[x][0];
-#pragma unroll
-            for (int i = 1; i < 16; ++i)
-                mx[x] = fmaxf(mx[x], s[x][i]);
-            mx[x] *= ksc[x];
-        }
-        const float top = max_halves(fmaxf(mx[0], mx[1]));
-        if (__ballot(top > m + kLazy || vrescale != 1.0f)) {
+        return f;
+    };
+    // Moves a row's reference if `top`, the tile's largest score, passes it by
+    // too much, and the outputs to their new unit.
+    auto refer = [&](float top, float unit) {
+        if (__ballot(top > m + kLazy || unit != 1.0f)) {
             const float mn = top > m + kLazy ? top : m;
             const float grow = m == kNegInf ? 0.0f : exp2_fast(m - mn);
             l *= grow;
             m = mn;
-            const float f = grow * vrescale;
+            const float f = grow * unit;
 #pragma unroll
             for (int x = 0; x < VT; ++x)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     o[x][i] *= f;
         }
+    };
+    auto largest = [&](const f32x16_t &s) {
+        float mx = s[0];
+#pragma unroll
+        for (int i = 1; i < 16; ++i)
+            mx = fmaxf(mx, s[i]);
+        return mx;
+    };
+    auto pack = [&](const f32x16_t &s, u32x4_t (&p)[2]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            p[i >> 2][i & 3] = f16_pair(s[2 * i], s[2 * i + 1]);
+    };
+
+    // A tile that every row of the workgroup sees, its blocks all with scales.
+    auto whole = [&](uint32_t buf) {
+        Scale sc[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            sc[x] = scl[buf][2 * x + h];
+        const uint32_t vmax = sc[0].vs > sc[1].vs ? sc[0].vs : sc[1].vs;
+        const int32_t v0 = __builtin_amdgcn_readlane((int)vmax, 0), v1 = __builtin_amdgcn_readlane((int)vmax, 32);
+        const float unit = unit_for((v0 > v1 ? v0 : v1) - 127);
+        f32x16_t s[2];
+        float c[2], vsc[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            __builtin_amdgcn_s_setprio(1);
+            s[x] = products(buf, x);
+            __builtin_amdgcn_s_setprio(0);
+            c[x] = pow2_byte(sc[x].ks) * a.scale_log2;
+            const int32_t field = (int32_t)sc[x].vs - exp_ref;        // exponent field of 2^(e - E)
+            vsc[x] = pow2_byte((uint32_t)(field < 7 ? 7 : field));
+        }
+        refer(max_halves(fmaxf(largest(s[0]) * c[0], largest(s[1]) * c[1])), unit);
+        const float mu = m == kNegInf ? 0.0f : m;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            u32x4_t p[2];
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[x][i] = exp2_fast(fmaf(s[x][i], c[x], -mu));
+                sum += s[x][i];
+            }
+            l += sum;
+            pack(s[x], p);
+#pragma unroll
+            for (int d = 0; d < VT; ++d) {
+                const u32x4_t raw = v_frag(buf, x, d);
+                o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.x, raw.y, vsc[x]), p[0], o[d]);
+                o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.z, raw.w, vsc[x]), p[1], o[d]);
+            }
+        }
+    };
+
+    // Any tile: some rows may not see all of it, blocks may have no scale.
+    auto partly = [&](uint32_t tile, uint32_t buf) {
+        const int32_t tk = (int32_t)(tile * kKvTile), key0 = tk + 16 * (int32_t)h;   // of half x: + 32 x
+        float c[2], vsc[2];
+        int32_t e[2];
+        uint32_t poison[2];      // a block without a V scale reads as NaN codes
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const Scale sc = scl[buf][2 * x + h];
+            c[x] = sc.ks - 1u >= 254u ? __builtin_nanf("") : pow2_byte(sc.ks) * a.scale_log2;
+            poison[x] = sc.vs - 1u >= 254u ? 0x7f7f7f7fu : 0u;
+            e[x] = poison[x] || key0 + 32 * x >= w.hi ? kNoExp : (int32_t)sc.vs - 127;
+        }
+        const int32_t emax = e[0] > e[1] ? e[0] : e[1];
+        const int32_t e0 = __builtin_amdgcn_readlane(emax, 0), e1 = __builtin_amdgcn_readlane(emax, 32);
+        const float unit = unit_for(e0 > e1 ? e0 : e1);
+        f32x16_t s[2];
+        float top = kNegInf;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            vsc[x] = e[x] == kNoExp || e[x] - exp_ref < -120 ? pow2_byte(7)
+                                                             : pow2_byte((uint32_t)(e[x] - exp_ref + 127));
+            s[x] = products(buf, x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                s[x][i] = key0 + 32 * x + i >= rlo && key0 + 32 * x + i < rhi ? s[x][i] : kNegInf;
+            top = fmaxf(top, largest(s[x]) * c[x]);
+        }
+        refer(max_halves(top), unit);
         const float mu = m == kNegInf ? 0.0f : m;
         u32x4_t p[2][2];
 #pragma unroll
@@ -282,140 +353,143 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                float v = exp2_fast(fmaf(s[x][i], ksc[x], -mu));
-                if (MASKED)      // a NaN scale must not reach hidden keys
-                    v = s[x][i] == kNegInf ? 0.f : v;
-                s[x][i] = v;
-                sum += v;
+                // a NaN scale must not reach hidden keys
+                const float v = exp2_fast(fmaf(s[x][i], c[x], -mu));
+                s[x][i] = s[x][i] == kNegInf ? 0.f : v;
+                sum += s[x][i];
             }
             l += sum;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                p[x][u].x = f16_pair(s[x][8 * u + 0], s[x][8 * u + 1]);
-                p[x][u].y = f16_pair(s[x][8 * u + 2], s[x][8 * u + 3]);
-                p[x][u].z = f16_pair(s[x][8 * u + 4], s[x][8 * u + 5]);
-                p[x][u].w = f16_pair(s[x][8 * u + 6], s[x][8 * u + 7]);
-            }
+            pack(s[x], p[x]);
         }
-        if (MASKED) {
-            // Blocks without a V scale read as NaN codes; codes of keys no
-            // row sees are dropped; a NaN code is counted for the rows that
-            // see it by a product of its own, then dropped.
+        // Codes of half x that some row of the wave may see.
+        auto kept = [&](int x, int d) {
+            u32x4_t v = v_frag(buf, x, d) | (x ? poison[1] : poison[0]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t keep = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int32_t key = key0 + 32 * x + 4 * i + j;
+                    keep |= key >= w.lo && key < w.hi ? 0xffu << (8 * j) : 0u;
+                }
+                v[i] &= keep;
+            }
+            return v;
+        };
+        uint32_t any = 0;
+#pragma unroll
+        for (int d = 0; d < VT; ++d)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                const int32_t key0 = tk + 32 * x + 16 * (int32_t)h;
-                const uint32_t bad_scale = scl[buf][2 * x + h].vs - 1u >= 254u ? 0x7f7f7f7fu : 0u;
-                u32x4_t keep;
+                // 0 * NaN must not reach rows that do not see the key
+                u32x4_t raw = kept(x, d);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    keep[i] = 0u;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int32_t key = key0 + 4 * i + j;
-                        keep[i] |= key >= w.lo && key < w.hi ? 0xffu << (8 * j) : 0u;
-                    }
+                    const uint32_t nan = nan_bytes(raw[i]);
+                    any |= nan;
+                    raw[i] &= ~((nan >> 7) * 0xffu);
                 }
-#pragma unroll
-                for (int d = 0; d < VT; ++d) {
-                    u32x4_t raw = *reinterpret_cast<const u32x4_t *>(
-                        lds + buf * (8 * BLK) + (4u + 2u * x + h) * BLK + (32u * d + col) * 16u);
-                    raw = (raw | bad_scale) & keep;
-                    uint32_t any = 0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        any |= nan_bytes(raw[i]);
-                    if (__ballot(any != 0)) {
-                        u32x4_t bad[2], seen[2];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint32_t nb = nan_bytes(raw[i]) >> 7;
-                            raw[i] &= ~(nb * 0xffu);
-                            bad[i >> 1][2 * (i & 1)] = ((nb & 1u) | ((nb & 0x100u) << 8)) * 0x3c00u;
-                            bad[i >> 1][2 * (i & 1) + 1] =
-                                (((nb >> 16) & 1u) | ((nb >> 8) & 0x10000u)) * 0x3c00u;
-                        }
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int32_t key = key0 + 2 * i;
-                            seen[i >> 2][i & 3] = (key >= rlo && key < rhi ? 0x3c00u : 0u) |
-                                                  (key + 1 >= rlo && key + 1 < rhi ? 0x3c000000u : 0u);
-                        }
-                        f32x16_t n;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            n[i] = 0.f;
-                        n = mfma32<QueryF16>(bad[0], seen[0], n);
-                        n = mfma32<QueryF16>(bad[1], seen[1], n);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            o[d][i] = n[i] > 0.f ? __builtin_nanf("") : o[d][i];
-                    }
-                    o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.x, raw.y, vsc[x]), p[x][0], o[d]);
-                    o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.z, raw.w, vsc[x]), p[x][1], o[d]);
-                }
+                o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.x, raw.y, vsc[x]), p[x][0], o[d]);
+                o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.z, raw.w, vsc[x]), p[x][1], o[d]);
             }
-        } else {
+        if (__ballot(any != 0)) {
+            // NaN for the rows that do see one: a product that counts them
 #pragma unroll
-            for (int d = 0; d < VT; ++d)
+            for (int d = 0; d < VT; ++d) {
+                f32x16_t n;
 #pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    n[i] = 0.f;
+#pragma unroll 1
                 for (int x = 0; x < 2; ++x) {
-                    const u32x4_t raw = *reinterpret_cast<const u32x4_t *>(
-                        lds + buf * (8 * BLK) + (4u + 2u * x + h) * BLK + (32u * d + col) * 16u);
-                    o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.x, raw.y, vsc[x]), p[x][0], o[d]);
-                    o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.z, raw.w, vsc[x]), p[x][1], o[d]);
+                    const u32x4_t raw = kept(x, d);
+                    u32x4_t bad[2], seen[2];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t nb = nan_bytes(raw[i]) >> 7;
+                        bad[i >> 1][2 * (i & 1)] = ((nb & 1u) | ((nb & 0x100u) << 8)) * 0x3c00u;
+                        bad[i >> 1][2 * (i & 1) + 1] = (((nb >> 16) & 1u) | ((nb >> 8) & 0x10000u)) * 0x3c00u;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int32_t key = key0 + 32 * x + 2 * i;
+                        seen[i >> 2][i & 3] = (key >= rlo && key < rhi ? 0x3c00u : 0u) |
+                                              (key + 1 >= rlo && key + 1 < rhi ? 0x3c000000u : 0u);
+                    }
+                    n = mfma32<QueryF16>(bad[0], seen[0], n);
+                    n = mfma32<QueryF16>(bad[1], seen[1], n);
                 }
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    o[d][i] = n[i] > 0.f ? __builtin_nanf("") : o[d][i];
+            }
         }
     };
 
     if (begin < end) {
-        // Tiles every row of the workgroup sees run in a loop of their own,
-        // without the handling of hidden keys; it ends early at a block
-        // without a V scale.
+        // Tiles every row of the workgroup sees run in a loop of their own; it
+        // ends early at a block without a scale.
         uint32_t whole0 = ((uint32_t)t.all_lo + kKvTile - 1) / kKvTile, whole1 = (uint32_t)t.all_hi / kKvTile;
         whole0 = whole0 > tile0 + begin ? whole0 - tile0 : begin;
         whole1 = whole1 > tile0 + end ? end : (whole1 > tile0 ? whole1 - tile0 : 0u);
+        // Scale bytes pass through registers and go to LDS a tile after their
+        // load, two tiles before their use, 255 for a block without a scale.
+        Scale sc, was;
+        uint32_t ok, was_ok;
+        auto put = [&](uint32_t in, const Scale &v, uint32_t good) {
+            if (lane == 0)
+                scl[in][wave] = Scale{good && v.ks ? v.ks : 255u, good && v.vs ? v.vs : 255u};
+        };
         Where at = locate(tile0 + begin);
-        stage(at, 0);
-        Scale sc = scales(at);
-        uint32_t ok = at.ok;
-        if (lane == 0)
-            scl[0][wave] = Scale{ok ? sc.ks : 0u, ok ? sc.vs : 0u};
-        at = locate(tile0 + begin + 1);
+#pragma unroll
+        for (uint32_t k = 0; k + 1 < kBuffers; ++k) {
+            stage(at, k);
+            sc = scales(at);
+            ok = at.ok;
+            put(k, sc, ok);
+            at = locate(tile0 + begin + k + 1);
+        }
         wait_vm<0>();
         __syncthreads();
         uint32_t tile = begin, buf = 0;
-        // every wave has left the other buffer: fill it while this one is
-        // computed (after the last tile with one that is not used)
         auto ahead = [&]() {
-            stage(at, buf ^ 1u);
+            was = sc;
+            was_ok = ok;
             sc = scales(at);
             ok = at.ok;
-            at = locate(tile0 + tile + 2);
+            stage(at, (buf + 3u) & 3u);
+            at = locate(tile0 + tile + kBuffers);
         };
+        // The next tile has arrived when no more loads are open than the two
+        // tiles after it take: K and V pieces and two scale bytes each.
         auto turn = [&]() {
-            if (lane == 0)
-                scl[buf ^ 1u][wave] = Scale{ok ? sc.ks : 0u, ok ? sc.vs : 0u};
-            wait_vm<0>();
-            __syncthreads();
+            put((buf + 2u) & 3u, was, was_ok);
+            wait_vm<2 * (2 * (DP / 64) + 2)>();
+            barrier_lds();
             ++tile;
-            buf ^= 1u;
+            buf = (buf + 1u) & 3u;
+        };
+        auto scaled = [&](uint32_t in) {
+            const Scale s = scl[in][lane & 3u];
+            return !__ballot(s.ks == 255u || s.vs == 255u);
         };
         auto general = [&](uint32_t stop) {
             while (tile < stop) {
                 ahead();
                 const int32_t tk = (int32_t)((tile0 + tile) * kKvTile);
                 if (tk < w.hi && tk + (int32_t)kKvTile > w.lo)    // some key of it is for this wave
-                    compute(tile0 + tile, buf, Constant<true>());
+                    partly(tile0 + tile, buf);
                 turn();
             }
         };
         general(whole0 < end ? whole0 : end);
-        while (tile < whole1 && !__ballot(scl[buf][lane & 3u].vs - 1u >= 254u)) {
+        while (tile < whole1 && scaled(buf)) {
             ahead();
-            compute(tile0 + tile, buf, Constant<false>());
+            whole(buf);
             turn();
         }
         general(end);
+        wait_vm<0>();
     }
 
     // a row's sum is in two lanes; its output in both, 4 channels at a time
@@ -487,7 +561,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void w8a16_kv_tile_kernel(A
 template <class Q, int DP>
 hipError_t launch_dim(const AttnArgs &a, const w8a16_kv_plan_t &p, hipStream_t stream)
 {
-    const uint32_t bytes = 16 * 16 * DP + 64;
+    const uint32_t bytes = kBuffers * (8 * 16 * DP + 4 * 8);     // codes and scale bytes
     static std::atomic<uint64_t> lds_set{0};
     auto kern = w8a16_kv_tile_kernel<Q, DP>;
     hipError_t e = allow_lds(reinterpret_cast<const void *>(kern), bytes, bytes, lds_set);
