@@ -451,13 +451,18 @@ int kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
 
 // No C++ exception (an allocation in the maps and strings behind the
 // helpers) leaves a C entry.
-template <class F> int guarded(F f)
+template <class F> int guarded(const char *entry, F f)
 {
     try {
         return f();
+    } catch (const std::exception &e) {
+        try {
+            return refuse(W8A16_ERR_HIP, "%s: %s", entry, e.what());
+        } catch (...) {
+        }
     } catch (...) {
-        return W8A16_ERR_HIP;
     }
+    return W8A16_ERR_HIP;
 }
 
 }  // namespace
@@ -469,7 +474,7 @@ extern "C" {
 int w8a16_rope_table(const w8a16_rope_config_t *config, float *table, uint32_t positions,
                      uint32_t rot_dim, void *stream)
 {
-    return w8a16::guarded([&] {
+    return w8a16::guarded("w8a16_rope_table", [&] {
         return w8a16::rope_table(config, table, positions, rot_dim, static_cast<hipStream_t>(stream));
     });
 }
@@ -481,7 +486,7 @@ int w8a16_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, voi
                void *stream)
 {
     const int64_t strides[4] = {x_token_stride, x_head_stride, y_token_stride, y_head_stride};
-    return w8a16::guarded([&] {
+    return w8a16::guarded("w8a16_rope", [&] {
         return w8a16::rope(x, strides, y, dtype, tokens, heads, head_dim, table, table_positions, rot_dim,
                            positions, layout, inverse, static_cast<hipStream_t>(stream));
     });
@@ -490,7 +495,7 @@ int w8a16_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, voi
 int w8a16_kv_append(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
                     const w8a16_kv_append_args_t *args, void *stream)
 {
-    return w8a16::guarded([&] {
+    return w8a16::guarded("w8a16_kv_append", [&] {
         return w8a16::kv_append(cache, seqs, args, static_cast<hipStream_t>(stream));
     });
 }
@@ -498,7 +503,7 @@ int w8a16_kv_append(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
 int w8a16_kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
                        const w8a16_kv_attention_args_t *args, void *stream)
 {
-    return w8a16::guarded([&] {
+    return w8a16::guarded("w8a16_kv_attention", [&] {
         return w8a16::kv_attention(cache, seqs, args, static_cast<hipStream_t>(stream));
     });
 }
