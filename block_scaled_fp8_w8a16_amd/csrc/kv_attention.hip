@@ -570,18 +570,19 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
     }
 }
 
-// Adds the chunks' partial results of the tile kernel: one workgroup per (row, KV head).  Its
-// threads are groups of dim / 4, four channels each, that take the chunks in
-// turn; the groups' sums are added in group order.
+// Adds the chunks' partial results of the tile kernel: one wave per (row, KV
+// head).  Its lanes are groups of dim / 4, four channels each, that take the
+// chunks in turn; the groups' sums are added in group order.
 template <class E>
 __global__ __launch_bounds__(256) void w8a16_kv_join_kernel(AttnArgs a, uint32_t tile_rows,
-                                                            uint32_t rows_used, uint32_t grid_rows)
+                                                            uint32_t rows_used, uint32_t rows_all,
+                                                            uint32_t grid_rows)
 {
-    __shared__ float fac[256];
-    __shared__ float red[8];
-    __shared__ f32x4_t part[256];
-    const uint32_t tid = threadIdx.x;
-    const uint32_t r = blockIdx.x % rows_used, id = blockIdx.x / rows_used;   // id: ((b, head), rtile)
+    const uint32_t lane = threadIdx.x & 63u;
+    const uint32_t idx = 4u * blockIdx.x + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (idx >= rows_all)
+        return;
+    const uint32_t r = idx % rows_used, id = idx / rows_used;   // id: ((b, head), rtile)
     const uint32_t rtile = id % a.row_tiles;
     const uint32_t head = id / a.row_tiles % a.pool.heads, b = id / a.row_tiles / a.pool.heads;
     RowTile t;
@@ -598,14 +599,14 @@ __global__ __launch_bounds__(256) void w8a16_kv_join_kernel(AttnArgs a, uint32_t
         return;      // one chunk: its workgroup has stored the row
     uint32_t n = (tiles + a.chunk_tiles - 1) / a.chunk_tiles;
     n = n < a.chunks ? n : a.chunks;
-    const uint32_t dim = a.pool.dim, per = dim / 4, groups = 256u / per;
+    const uint32_t dim = a.pool.dim, per = dim / 4, groups = 64u / per;
     const size_t first = (size_t)id * a.chunks * tile_rows + r;
     const float *wo = a.ws + first * dim;
     const float *wst = a.ws + (size_t)grid_rows * dim + first * 4u;
 
     // the row's largest reference and exponent over all chunks
     float m = kNegInf, ex = (float)kNoExp;
-    for (uint32_t c = tid; c < n; c += 256u) {
+    for (uint32_t c = lane; c < n; c += 64u) {
         const f32x4_t st = *reinterpret_cast<const f32x4_t *>(wst + (size_t)c * tile_rows * 4u);
         m = fmaxf(m, st.x);
         ex = fmaxf(ex, st.z);
@@ -615,56 +616,50 @@ __global__ __launch_bounds__(256) void w8a16_kv_join_kernel(AttnArgs a, uint32_t
         m = fmaxf(m, __shfl_xor(m, off, 64));
         ex = fmaxf(ex, __shfl_xor(ex, off, 64));
     }
-    if ((tid & 63u) == 0) {
-        red[tid >> 6] = m;
-        red[4 + (tid >> 6)] = ex;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        m = fmaxf(m, red[w]);
-        ex = fmaxf(ex, red[4 + w]);
-    }
-    const uint32_t grp = tid / per, d = tid % per * 4u;
-    f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-    float l = 0.f;       // this thread's chunks c = tid, tid + 256, ...
-    for (uint32_t c0 = 0; c0 < n; c0 += 256u) {
-        __syncthreads();
-        if (c0 + tid < n) {
-            const f32x4_t st = *reinterpret_cast<const f32x4_t *>(wst + (size_t)(c0 + tid) * tile_rows * 4u);
+    const uint32_t grp = lane / per, d = lane % per * 4u;
+    f32x4_t own = {0.f, 0.f, 0.f, 0.f};
+    float l = 0.f;       // this lane's chunks c = lane, lane + 64, ...
+    for (uint32_t c0 = 0; c0 < n; c0 += 64u) {
+        float fac = 0.f;
+        if (c0 + lane < n) {
+            const f32x4_t st = *reinterpret_cast<const f32x4_t *>(wst + (size_t)(c0 + lane) * tile_rows * 4u);
             const float f = st.x == kNegInf ? 1.f : exp2_fast(st.x - m);   // -inf: l is 0, or NaN
             l += f * st.y;
-            fac[tid] = f * exp2_fast(st.z - ex);
+            fac = f * exp2_fast(st.z - ex);
         }
-        __syncthreads();
-        const uint32_t stop = n - c0 < 256u ? n - c0 : 256u;
-        if (grp < groups)
-#pragma unroll 4
-            for (uint32_t c = grp; c < stop; c += groups)
-                acc += fac[c] * *reinterpret_cast<const f32x4_t *>(wo + (size_t)(c0 + c) * tile_rows * dim + d);
+        const uint32_t stop = n - c0 < 64u ? n - c0 : 64u;
+        for (uint32_t base = 0; base < stop; base += 4u * groups) {    // all lanes: each lends its factor
+            f32x4_t v[4];
+            float f[4];
+#pragma unroll
+            for (uint32_t u = 0; u < 4; ++u) {
+                const uint32_t c = base + u * groups + grp;
+                v[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                if (c < stop && grp < groups)
+                    v[u] = *reinterpret_cast<const f32x4_t *>(wo + (size_t)(c0 + c) * tile_rows * dim + d);
+                f[u] = __shfl(fac, (int)(c & 63u), 64);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                own += f[u] * v[u];
+        }
     }
-    // sum of l: over the lanes, then over the waves
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1)
         l += __shfl_xor(l, off, 64);
-    __syncthreads();
-    if ((tid & 63u) == 0)
-        red[tid >> 6] = l;
-    part[tid] = acc;
-    __syncthreads();
-    if (tid >= per)
-        return;
-    l = red[0] + red[1] + red[2] + red[3];
+    f32x4_t acc = own;
     for (uint32_t k = 1; k < groups; ++k)
-        acc += part[k * per + tid];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            acc[i] += __shfl(own[i], (int)((lane + k * per) & 63u), 64);
+    if (lane >= per)
+        return;
     const uint32_t tok = a.by_group.div(row), hq = head * a.group + row - tok * a.group;
     const bool none = m == kNegInf && l == 0.f;
     const float inv = none ? 0.f : 1.0f / l, unit_e = none ? 0.f : ldexpf(1.0f, (int)ex);
-    E *dst = reinterpret_cast<E *>(a.out) + (int64_t)(t.first + tok) * a.out_token + (int64_t)hq * a.out_head;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        dst[d + i] = static_cast<E>(acc[i] * inv * unit_e);
-    if (tid == 0 && a.lse)
+    store_row4(reinterpret_cast<E *>(a.out) + (int64_t)(t.first + tok) * a.out_token +
+                   (int64_t)hq * a.out_head + d, acc * inv * unit_e);
+    if (lane == 0 && a.lse)
         a.lse[(size_t)(t.first + tok) * a.q_heads + hq] =
             none ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
 }
@@ -707,11 +702,12 @@ hipError_t launch_kv_join(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t 
 {
     const uint32_t rows = 16u * p.row_blocks;
     const uint32_t used = max_rows < rows ? max_rows : rows;     // rows of a tile that exist
-    const dim3 grid(p.grid / p.chunks * used), block(256);
+    const uint32_t all = p.grid / p.chunks * used;
+    const dim3 grid((all + 3u) / 4u), block(256);
     if (dtype == W8A16_BF16)
-        hipLaunchKernelGGL(w8a16_kv_join_kernel<__bf16>, grid, block, 0, stream, a, rows, used, p.grid * rows);
+        hipLaunchKernelGGL(w8a16_kv_join_kernel<__bf16>, grid, block, 0, stream, a, rows, used, all, p.grid * rows);
     else
-        hipLaunchKernelGGL(w8a16_kv_join_kernel<_Float16>, grid, block, 0, stream, a, rows, used, p.grid * rows);
+        hipLaunchKernelGGL(w8a16_kv_join_kernel<_Float16>, grid, block, 0, stream, a, rows, used, all, p.grid * rows);
     return hipGetLastError();
 }
 

@@ -11,7 +11,8 @@ namespace w8a16 {
 namespace {
 
 constexpr uint64_t kKeysPerTile = 64;
-constexpr uint64_t kCutTiles = 16;
+constexpr uint64_t kMinTiles = 4;      // of a chunk
+constexpr uint64_t kCutTiles = 12;     // that a cut has to spare, and one more
 
 uint64_t div_up(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
@@ -75,7 +76,21 @@ int make_kv_plan(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_he
     w8a16_kv_plan_t p;
     std::memset(&p, 0, sizeof p);
     const uint64_t rows = (uint64_t)max_new * (q_heads / kv_heads);
-    p.kernel = rows <= 32 ? W8A16_KV_ROWS : W8A16_KV_TILE;
+    // Up to 32 rows the row kernel, whose work grows with the rows; beyond,
+    // the tile kernel takes as long for 33 rows as for 128, which pays where
+    // the row tiles would wait for CUs.  8 KV heads of 128 channels, row
+    // kernel and tile kernel, us:
+    //   32 rows  64 sequences of 1000 tokens (1024 row tiles)  48  54
+    //   48 rows  64 of 1000 (1536) 64  56;  32 of 2000 (768)  62  74
+    //   64 rows  64 of 1000 (2048) 83  55;  32 of 2000 (1024) 79  73
+    //            16 of 1000 (512)  21  36;  1 of 500 (32)      9  19
+    //  128 rows  16 of 1000 (1024) 35  37;  8 of 4000 (512)   51  51
+    // so up to 128 rows where there are at most 4 row tiles per CU.  Of 256
+    // channels a CU holds one workgroup: 32 rows of one sequence of 16000
+    // 36 and 41, 48 rows 44 and 43, 64 rows 49 and 44.
+    const bool narrow = head_dim <= 128;
+    const uint64_t row_grid = (uint64_t)seqs * kv_heads * div_up(rows, 16);
+    p.kernel = rows <= 32 || (narrow && rows <= 128 && row_grid <= 4 * cus) ? W8A16_KV_ROWS : W8A16_KV_TILE;
     p.row_blocks = p.kernel == W8A16_KV_ROWS ? 1 : 8;
     p.waves = 4;
     p.chunk_tiles = 1u << 30;
@@ -89,19 +104,22 @@ int make_kv_plan(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_he
     // Cut the keys while that leaves no more workgroups than run at once: two
     // per CU, one of 8 waves or of heads above 128 channels.  Eight waves
     // where the row tiles alone do not give every CU a workgroup: half as
-    // many chunks to join (131072 tokens of 8 KV heads 66 -> 57 us, 3
-    // sequences of 9000 15.4 -> 14.6), but slower where several rounds of
-    // short workgroups run (256 sequences of 500 46 -> 74 us).  A cut has to
-    // spare more than kCutTiles tiles of a workgroup's time, about what the
-    // join costs, and a chunk has at least 8 tiles.
-    const bool narrow = head_dim <= 128;
+    // many chunks to join (32 sequences of 2000 tokens 30 us against 31 with
+    // four waves, 4 new tokens over 16000 20 against 23), but slower where
+    // more workgroups wait (48 sequences 52 against 45, 256 of 500 74 against
+    // 46).  A cut has to spare more tiles of a workgroup's time than the join
+    // costs (one sequence, 8 KV heads of 128 channels: 900 tokens 11.8 us
+    // uncut, 10.8 cut; 1200 12.8 and 10.8; 1500 15.6 and 11.0; 16 sequences,
+    // which can be cut in two: 1200 15.1 and 16.2, 2000 20.6 and 20.0), and a
+    // chunk has at least 4 tiles (8 of them: 2000 tokens 12.2 us, 4 of them
+    // 11.1; of 256 channels 17.5 and 13.1).
     if (p.kernel == W8A16_KV_ROWS && narrow && p.grid <= cus)
         p.waves = 8;
     const uint64_t slots = narrow && p.waves == 4 ? 2 * cus : cus;
     const uint64_t cuts = slots > p.grid ? slots / p.grid : 1;
     uint64_t per = div_up(tiles, cuts);
-    if (per < 8)
-        per = 8;
+    if (per < kMinTiles)
+        per = kMinTiles;
     if (p.kernel == W8A16_KV_ROWS && per < div_up(tiles, kKvMaxChunks))
         per = div_up(tiles, kKvMaxChunks);
     if (per + kCutTiles >= tiles)
