@@ -74,6 +74,8 @@ void fill_rope(RopeRows &r, const void *x, void *y, const int64_t strides[4], co
     r.by_items = FastDiv(r.items);
 }
 
+// Several heads per thread where that still leaves every CU 512 threads
+// (figures in rope_kernel.hip).
 uint32_t rope_heads_per_thread(uint64_t items)
 {
     return items >= 512ull * kDefaultCUs * kRopeHeads ? kRopeHeads : 1;
@@ -231,7 +233,6 @@ int rope(const void *x, const int64_t strides[4], void *y, uint32_t dtype, uint3
     RopeArgs a;
     std::memset(static_cast<void *>(&a), 0, sizeof a);
     fill_rope(a.r, x, y, strides, table, table_positions, rot, head_dim, layout, heads, dtype);
-    // several heads per thread where that leaves every CU 512 threads
     a.heads_per_thread = rope_heads_per_thread((uint64_t)heads * a.r.items * tokens);
     const uint64_t row = (uint64_t)((heads + a.heads_per_thread - 1) / a.heads_per_thread) * a.r.items;
     const uint64_t total = row * tokens;
@@ -294,6 +295,8 @@ int kv_append(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
     const uint32_t size = elem_size(g->dtype), dim = cache->head_dim, rot = g->table ? g->rot_dim : 0;
     const int64_t ks[4] = {a.k_token, a.k_head, a.v_token, a.v_head};
     // widest whole pieces: of the rows' alignment, and of the rotated halves
+    // (4 x 2048 tokens of 8 KV heads: pieces of 8 elements 13.7 us, of 4 15.1,
+    // of 1 30.1)
     a.vec = 1;
     for (uint32_t n = 8; n >= 4 && a.vec == 1; n /= 2) {
         const uint32_t bytes = n * size < 16 ? n * size : 16;

@@ -3,19 +3,27 @@
 //
 // One wave owns one block of 16 slots of one KV head, keys or values, so
 // that the block's scale needs no atomics: its lanes hold the new tokens'
-// elements in registers (8 consecutive elements of a token each), rotate
-// them, reduce the largest magnitude over the wave, and quantise.  Scales
-// are powers of two (E8M0), so quantising is one exact multiplication and
-// one rounding, and a block whose scale grows keeps its older codes exactly
-// unless they fall into E4M3's subnormals.
+// elements in registers (all loads in flight at once), rotate them, reduce
+// the largest magnitude over the wave, and quantise.  Scales are powers of
+// two (E8M0), so quantising is one exact multiplication and one rounding,
+// and a block whose scale grows keeps its older codes exactly unless they
+// fall into E4M3's subnormals.  Keys lie in lanes as pairs, as in the
+// rotation.
 //
 // Values are stored with a block's 16 tokens adjacent for each channel: the
 // attention's P V product then takes 16 keys of a channel in one 16-byte
-// load.  A wave transposes through LDS and merges the new bytes into the
-// 16-byte rows that hold them.
+// load.  A wave transposes through LDS, where a lane's four tokens of a
+// channel make one word, and merges the new bytes into the 16-byte rows that
+// hold them.
 //
 // The queries' rotation runs in further workgroups of the same launch: for
 // a decode step all of it is launch latency, and one launch does.
+//
+// HBM bounds long appends: 6 prompts of about 4100 tokens with 32 query and
+// 8 KV heads of 128 channels, about 460 MB, take 89 us, 5.2 TB/s (a large
+// copy moves 4.9).  A decode step of 256 sequences takes 7.7 us of the GPU,
+// of 4 sequences 4.4: the chain of loads from the lengths through the page
+// to the block's scale and rows.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -17,11 +17,22 @@
 // consecutive keys, one block of the cache: one K scale and one V scale for
 // all its scores, and its p are in place as the second product's operand,
 // whose other side is one 16-byte load of V (16 keys of one channel).
-// Nothing passes through LDS before the four waves' results are joined.
+// Nothing passes through LDS before the waves' results are joined.
 //
 // V codes are widened to FP16 by 2^(e - E), e the block's scale exponent
 // and E the largest seen by the wave, at most 2^7 above it: exact for blocks
 // within 2^22 of the largest; O counts in units of 2^E.
+//
+// What bounds it: reading the cache.  64 sequences of 8192 tokens (8 KV heads
+// of 128 channels, 673 MB) take 139 us, 4.8 TB/s; one of 131072 tokens, cut
+// into 32 chunks per head, 58 us, 4.7 TB/s, where a large copy moves 4.9.
+// Each wave has one 64-key tile of loads in flight (16 KB) while it computes
+// another, 4 waves to a workgroup and two workgroups to a CU up to 128
+// channels; 8 waves where there are few row tiles (figures in kv_plan.cpp).
+// Short caches are bound by the chain of loads (length, page, block): 300
+// tokens take 8.3 us, 24 windows of about 1000 keys with 20 rows each 15.8,
+// twice what their bytes and about what their widening and exponentials
+// take on a half-filled chip.
 //
 // Hidden keys: their p is set to zero, and V codes that no row sees are
 // replaced by zero, since 0 * NaN would reach the sums.  Where a NaN code is
