@@ -29,6 +29,9 @@
 // Each wave has one 64-key tile of loads in flight (16 KB) while it computes
 // another, 4 waves to a workgroup and two workgroups to a CU up to 128
 // channels; 8 waves where there are few row tiles (figures in kv_plan.cpp).
+// (Refilling two sets of tile registers as they are consumed, so that loads
+// stay in flight longer, gained nothing at 64 channels, 15.3 us for 24
+// windows of 1024 keys either way, and spilled at 128.)
 // Short caches are bound by the chain of loads (length, page, block): 300
 // tokens take 8.3 us, 24 windows of about 1000 keys with 20 rows each 15.8,
 // twice what their bytes and about what their widening and exponentials
