@@ -3,9 +3,10 @@
 // The mathematics is that of the row kernel (kv_attention.hip): S^T = K Q^T,
 // p = 2^(S k_scale scale log2(e) - m) with a reference m that moves only by
 // more than 2^8, O^T += V^T p^T with p in FP16 and V widened by 2^(e - E).
-// The issue of vector instructions bounds the time: a wave needs about 330
-// of them (exponentials, conversions of codes and p, sums, LDS reads) beside
-// the 64 matrix instructions of 64 keys and 128 channels.  So a workgroup
+// The issue of vector instructions bounds the time: a wave needs about 320
+// of them (128 conversions of codes, 32 exponentials, the rest sums, maxima
+// and conversions of p) beside the 32 matrix instructions of 64 keys and 128
+// channels.  So a workgroup
 // takes 128 rows, its four waves 32 each with 32x32x16 matrix instructions,
 // two workgroups share a CU where registers allow (up to 128 channels), and:
 //   * 64 keys at a time, K and V as codes (half of what 16-bit operands
