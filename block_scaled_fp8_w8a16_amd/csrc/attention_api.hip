@@ -199,6 +199,9 @@ int rope_table(const w8a16_rope_config_t *c, float *table, uint32_t positions, u
                       entry, c->original, c->low_turns, c->high_turns);
     if (positions > 0x7fffffffu)
         return refuse(W8A16_ERR_SHAPE, "%s: positions=%u must be below 2^31", entry, positions);
+    if ((uint64_t)positions * (rot / 2) > kMaxThreads - 255)
+        return refuse(W8A16_ERR_SHAPE, "%s: %u positions of %u pairs are too many for one call", entry,
+                      positions, rot / 2);
     if (positions == 0)
         return W8A16_OK;
     hipError_t e = launch_rope_table(*c, table, positions, rot, stream);
@@ -327,7 +330,7 @@ int kv_append(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
         a.by_q_groups = FastDiv(a.q_groups);
         groups += per * seqs->tokens;
     }
-    if (units >= (1ull << 31) || groups >= (1ull << 31))
+    if (units >= (1ull << 31) || groups * 256ull > kMaxThreads)
         return refuse(W8A16_ERR_SHAPE, "%s: %u tokens of %u sequences (max_new=%u) are too many for one "
                       "call", entry, seqs->tokens, seqs->seqs, seqs->max_new);
     hipError_t e = launch_kv_append(a, g->dtype, stream);

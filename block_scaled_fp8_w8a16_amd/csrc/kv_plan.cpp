@@ -42,8 +42,8 @@ int kv_plan_finalize(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t 
         tiles = 1;
     const uint64_t row_tiles = div_up(rows, tile_rows), chunks = div_up(tiles, p->chunk_tiles);
     const uint64_t grid = (uint64_t)seqs * kv_heads * row_tiles * chunks;
-    if (grid >= (1ull << 31))
-        return fail(W8A16_ERR_SHAPE, "w8a16_kv_attention: too many workgroups (2^31) for one call");
+    if (grid * 64ull * p->waves > kMaxThreads)
+        return fail(W8A16_ERR_SHAPE, "w8a16_kv_attention: too many workgroups (2^32 threads) for one call");
     p->row_tiles = (uint32_t)row_tiles;
     p->chunks = (uint32_t)chunks;
     p->grid = (uint32_t)grid;

@@ -169,6 +169,8 @@ int plan_batched(const w8a16_gemm_desc_t *descs, uint32_t count, uint32_t cu_cou
 // Cache attention (kv_plan.cpp).  The row kernel joins a row tile's chunks in
 // the last workgroup to arrive, which holds a factor per chunk and row in
 // LDS; arrival counters sit 64 bytes apart.
+// Threads of one launch (a grid's size is held in 32 bits).
+constexpr uint64_t kMaxThreads = (1ull << 32) - 1;
 constexpr uint32_t kKvMaxChunks = 128;
 constexpr uint32_t kKvCounterStride = 16;
 int kv_plan_finalize(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_heads,

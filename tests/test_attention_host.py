@@ -49,6 +49,22 @@ def test_bad_setting_fails_every_call(var):
     assert lines[5] == str(w8.KV_KERNEL_ROWS)
 
 
+def test_launches_of_too_many_threads_are_refused():
+    from test_attention import _descs
+    from block_scaled_fp8_w8a16_amd.attention import RopeConfig
+    lib = w8.library()
+    assert lib.w8a16_rope_table(RopeConfig(1e4, 1, 0, 1, 4, 1, 0), 16, 1 << 26, 128, 0) == w8.ERR_SHAPE
+    many = dict(s__seqs=1 << 22, s__tokens=1 << 22, s__max_new=1, c__kv_heads=8, ap__q_heads=8,
+                at__q_heads=8, c__k_page_stride=1 << 20, c__v_page_stride=1 << 20,
+                c__k_scale_page_stride=64, c__v_scale_page_stride=64)
+    c, s, ap, at = _descs(**many)
+    assert lib.w8a16_kv_append(c, s, ap, 0) == w8.ERR_SHAPE
+    assert "too many" in w8.last_error()
+    with pytest.raises(w8.W8A16Error) as e:
+        w8.plan_kv_attention(1 << 22, 1, 64, 8, 8, 64)
+    assert e.value.status == w8.ERR_SHAPE and "too many" in str(e.value)
+
+
 LOGGED = """
 import torch
 import block_scaled_fp8_w8a16_amd as w8
