@@ -33,7 +33,7 @@
 // stay in flight longer, gained nothing at 64 channels, 15.3 us for 24
 // windows of 1024 keys either way, and spilled at 128.)
 // Short caches are bound by the chain of loads (length, page, block): 300
-// tokens take 8.3 us, 24 windows of about 1000 keys with 20 rows each 15.8,
+// tokens take 7.8 us, 24 windows of about 1000 keys with 25 rows each 14.3,
 // twice what their bytes and about what their widening and exponentials
 // take on a half-filled chip.
 //
@@ -231,11 +231,10 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
 
     auto compute = [&](uint32_t tile) {
         const int32_t key0 = (int32_t)(tile * kKvTile + 16u * g);   // the lane's first key
-        const float ksc = at.ok && at.ks - 1u < 254u ? pow2_byte(at.ks) * a.scale_log2
-                                                     : __builtin_nanf("");
-        int32_t e = at.vs - 1u < 254u ? (int32_t)at.vs - 127 : kNoExp;
-        if (key0 >= t.hi)
-            e = kNoExp;     // no visible key in the block
+        const bool seen = key0 < t.hi && key0 + 16 > t.lo;      // some key of the block, by some row
+        const float ksc = !seen ? 1.0f : (at.ok && at.ks - 1u < 254u ? pow2_byte(at.ks) * a.scale_log2
+                                                                      : __builtin_nanf(""));
+        int32_t e = seen && at.vs - 1u < 254u ? (int32_t)at.vs - 127 : kNoExp;
         int32_t emax = e;
 #pragma unroll
         for (int off = 16; off <= 32; off <<= 1) {
@@ -264,15 +263,26 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
                 s[x] = Q::mfma16(Q::widen(k[i][x].z, k[i][x].w), q[i][1], s[x]);
             }
 
-        if (__ballot(!at.ok || at.vs - 1u >= 254u)) {
+        const bool bad = seen && (!at.ok || at.vs - 1u >= 254u);
+        if (__ballot(bad)) {
             // a block without a V scale reads as NaN codes
-            const uint32_t poison = !at.ok || at.vs - 1u >= 254u ? 0x7f7f7f7fu : 0u;
+            const uint32_t poison = bad ? 0x7f7f7f7fu : 0u;
 #pragma unroll
             for (int x = 0; x < VT; ++x)
                 v[x] |= poison;
         }
         uint32_t hit = 0;
         if (masked) {
+            // (hidden numbers meet p of 0; only NaN would not vanish)
+            uint32_t odd = 0;
+#pragma unroll
+            for (int x = 0; x < VT; ++x)
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    odd |= (v[x][w] & 0x7f7f7f7fu) + 0x01010101u;
+            hit = __ballot((odd & 0x80808080u) != 0) != 0 ? 1u : 0u;
+        }
+        if (hit) {
             // codes of keys no row of the tile sees
             uint32_t any = 0;
 #pragma unroll
@@ -293,13 +303,18 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
         }
 
         if (masked) {
+            const int32_t up = rhi - key0, low = rlo - key0;
 #pragma unroll
             for (int x = 0; x < 4; ++x)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int32_t key = key0 + 4 * x + i;
-                    s[x][i] = key >= rlo && key < rhi ? s[x][i] : kNegInf;
-                }
+                for (int i = 0; i < 4; ++i)
+                    s[x][i] = 4 * x + i < up ? s[x][i] : kNegInf;
+            if (a.window)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        s[x][i] = 4 * x + i >= low ? s[x][i] : kNegInf;
         }
         float mx = kNegInf;
 #pragma unroll
@@ -321,17 +336,26 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
         }
         const float mu = m == kNegInf ? 0.0f : m;
         u32x4_t p[2];
+        if (masked && __ballot(!(ksc > 0.f))) {
+            // a NaN scale must not reach hidden keys, nor a factor of 0 their -inf
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s[x][i] = s[x][i] == kNegInf ? 0.f : exp2_fast(fmaf(s[x][i], ksc, -mu));
+        } else {
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    s[x][i] = exp2_fast(fmaf(s[x][i], ksc, -mu));
+        }
         float sum = 0.f;
 #pragma unroll
         for (int x = 0; x < 4; ++x)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float e2 = exp2_fast(fmaf(s[x][i], ksc, -mu));
-                if (masked)   // a NaN scale must not reach hidden keys
-                    e2 = s[x][i] == kNegInf ? 0.f : e2;
-                s[x][i] = e2;
-                sum += e2;
-            }
+            for (int i = 0; i < 4; ++i)
+                sum += s[x][i];
         l += sum;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
