@@ -19,7 +19,7 @@
 // The queries' rotation runs in further workgroups of the same launch: for
 // a decode step all of it is launch latency, and one launch does.
 //
-// HBM bounds long appends: 6 prompts of about 4100 tokens with 32 query and
+// HBM bounds long appends: 6 prompts of up to 4099 tokens with 32 query and
 // 8 KV heads of 128 channels, about 460 MB, take 89 us, 5.2 TB/s (a large
 // copy moves 4.9).  A decode step of 256 sequences takes 7.7 us of the GPU,
 // of 4 sequences 4.4: the chain of loads from the lengths through the page

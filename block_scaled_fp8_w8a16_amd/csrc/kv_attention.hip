@@ -23,8 +23,8 @@
 // and E the largest seen by the wave, at most 2^7 above it: exact for blocks
 // within 2^22 of the largest; O counts in units of 2^E.
 //
-// What bounds it: reading the cache.  64 sequences of 8192 tokens (8 KV heads
-// of 128 channels, 673 MB) take 139 us, 4.8 TB/s; one of 131072 tokens, cut
+// What bounds it: reading the cache.  64 sequences of up to 8192 tokens (8 KV
+// heads of 128 channels, 673 MB) take 139 us, 4.8 TB/s; one of 131072 tokens, cut
 // into 32 chunks per head, 58 us, 4.7 TB/s, where a large copy moves 4.9.
 // Each wave has one 64-key tile of loads in flight (16 KB) while it computes
 // another, 4 waves to a workgroup and two workgroups to a CU up to 128
@@ -37,10 +37,10 @@
 // twice what their bytes and about what their widening and exponentials
 // take on a half-filled chip.
 //
-// Hidden keys: their p is set to zero, and V codes that no row sees are
-// replaced by zero, since 0 * NaN would reach the sums.  Where a NaN code is
-// seen by some rows and hidden from others, a second product counts it for
-// the rows that see it.
+// Hidden keys: their scores are -inf, so their p are zero.  0 * NaN would
+// still reach the sums, so where a partly hidden tile has NaN among its V
+// codes, those that no row sees are replaced by zero, and a second product
+// counts the others for the rows that see them.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -517,7 +517,7 @@ typedef struct w8a16_kv_plan {
  * q_heads, head_dim] of `dtype` (BF16 or FP16); lse: FP32 [tokens, q_heads]
  * contiguous, or null.  max_kv: at least the largest kv_lens (0: the block
  * table's width); it shapes the launch only, longer sequences stay right.
- * plan: null for the default. */
+ * scale: finite, not negative.  plan: null for the default. */
 typedef struct w8a16_kv_attention_args {
     const void *q;
     void *out;
