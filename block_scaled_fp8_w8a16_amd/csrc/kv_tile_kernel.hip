@@ -441,25 +441,33 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
             if (lane == 0)
                 scl[in][wave] = Scale{good && v.ks ? v.ks : 255u, good && v.vs ? v.vs : 255u};
         };
-        Where at = locate(tile0 + begin);
+        // (all of the first tiles' loads before the first wait for one)
+        Where at[kBuffers - 1];
+        Scale first[kBuffers - 1];
+#pragma unroll
+        for (uint32_t k = 0; k + 1 < kBuffers; ++k)
+            at[k] = locate(tile0 + begin + k);
 #pragma unroll
         for (uint32_t k = 0; k + 1 < kBuffers; ++k) {
-            stage(at, k);
-            sc = scales(at);
-            ok = at.ok;
-            put(k, sc, ok);
-            at = locate(tile0 + begin + k + 1);
+            first[k] = scales(at[k]);
+            stage(at[k], k);
         }
+        Where next = locate(tile0 + begin + kBuffers - 1);
+#pragma unroll
+        for (uint32_t k = 0; k + 1 < kBuffers; ++k)
+            put(k, first[k], at[k].ok);
+        sc = first[kBuffers - 2];
+        ok = at[kBuffers - 2].ok;
         wait_vm<0>();
         __syncthreads();
         uint32_t tile = begin, buf = 0;
         auto ahead = [&]() {
             was = sc;
             was_ok = ok;
-            sc = scales(at);
-            ok = at.ok;
-            stage(at, (buf + 3u) & 3u);
-            at = locate(tile0 + tile + kBuffers);
+            sc = scales(next);
+            ok = next.ok;
+            stage(next, (buf + 3u) & 3u);
+            next = locate(tile0 + tile + kBuffers);
         };
         // The next tile has arrived when no more loads are open than the two
         // tiles after it take: K and V pieces and two scale bytes each.
