@@ -11,8 +11,8 @@ namespace w8a16 {
 namespace {
 
 constexpr uint64_t kKeysPerTile = 64;
-constexpr uint64_t kMinTiles = 4;      // of a chunk
-constexpr uint64_t kCutTiles = 12;     // that a cut has to spare, and one more
+constexpr uint64_t kMinTiles = 4;      // of a chunk; 8 where a CU has one already
+constexpr uint64_t kCutTiles = 10;     // that a cut has to spare, and one more
 
 uint64_t div_up(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
@@ -104,25 +104,37 @@ int make_kv_plan(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_he
     // Cut the keys while that leaves no more workgroups than run at once: two
     // per CU, one of 8 waves or of heads above 128 channels.  Eight waves
     // where the row tiles alone do not give every CU a workgroup: half as
-    // many chunks to join (32 sequences of 2000 tokens 30 us against 31 with
+    // many chunks to join (32 sequences of 2000 tokens 29 us against 31 with
     // four waves, 4 new tokens over 16000 20 against 23), but slower where
-    // more workgroups wait (48 sequences 52 against 45, 256 of 500 74 against
-    // 46).  A cut has to spare more tiles of a workgroup's time than the join
-    // costs (one sequence, 8 KV heads of 128 channels: 900 tokens 11.8 us
-    // uncut, 10.8 cut; 1200 12.8 and 10.8; 1500 15.6 and 11.0; 16 sequences,
-    // which can be cut in two: 1200 15.1 and 16.2, 2000 20.6 and 20.0), and a
-    // chunk has at least 4 tiles (8 of them: 2000 tokens 12.2 us, 4 of them
-    // 11.1; of 256 channels 17.5 and 13.1).
+    // more workgroups wait (48 sequences 51 against 46, 256 of 500 79 against
+    // 53).
+    //
+    // A cut has to spare more tiles of a workgroup's time than the join
+    // costs.  Row kernel, us: 4 sequences of 768 tokens 9.3 uncut, 10.7 cut;
+    // one of 900 11.8 and 10.8, of 1500 15.6 and 11.0; 16 sequences, which
+    // can be cut in two, of 1200 15.1 and 16.2, of 2000 20.6 and 20.0.  Tile
+    // kernel, whose partial rows grow with the workgroups: 128 new tokens
+    // over 1500 45 and 29 (96 workgroups); 2 x 256 over 1024 32 and 37, over
+    // 2048 60 and 44, 4 x 256 over 2048 of 64 channels 47 and 55, 2 x 512
+    // over 4096 115 and 95 (512 workgroups).
+    // A chunk has at least 4 tiles (2000 tokens: 8 tiles 12.2 us, 4 11.1; of
+    // 256 channels 17.5 and 13.1; 64 new tokens 27 and 24), or 8 where it
+    // would be a CU's second (128 new tokens over 4096: 34 and 37).
     if (p.kernel == W8A16_KV_ROWS && narrow && p.grid <= cus)
         p.waves = 8;
     const uint64_t slots = narrow && p.waves == 4 ? 2 * cus : cus;
     const uint64_t cuts = slots > p.grid ? slots / p.grid : 1;
     uint64_t per = div_up(tiles, cuts);
+    const uint64_t once = cus > p.grid ? div_up(tiles, cus / p.grid) : tiles;    // a workgroup per CU
+    const uint64_t least = once < 2 * kMinTiles ? once : 2 * kMinTiles;
+    if (per < least)
+        per = least;
     if (per < kMinTiles)
         per = kMinTiles;
     if (p.kernel == W8A16_KV_ROWS && per < div_up(tiles, kKvMaxChunks))
         per = div_up(tiles, kKvMaxChunks);
-    if (per + kCutTiles >= tiles)
+    const uint64_t join = p.kernel == W8A16_KV_ROWS ? kCutTiles : 4 + 12 * p.grid * div_up(tiles, per) / slots;
+    if (per + join >= tiles)
         per = tiles;
     p.chunk_tiles = (uint32_t)per;
     st = kv_plan_finalize(seqs, max_new, max_kv, q_heads, kv_heads, head_dim, window, &p);
