@@ -107,7 +107,7 @@ hipError_t launch_kv_rows(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t 
                           hipStream_t stream);
 hipError_t launch_kv_tile(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t dtype,
                           hipStream_t stream);
-// Adds the chunks' partial results of either kernel; max_rows: rows of the
+// Adds the chunks' partial results of the tile kernel; max_rows: rows of the
 // longest sequence.
 hipError_t launch_kv_join(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t max_rows,
                           uint32_t dtype, hipStream_t stream);

@@ -6,9 +6,9 @@
 // The issue of vector instructions bounds the time: a wave needs about 320
 // of them (128 conversions of codes, 32 exponentials, the rest sums, maxima
 // and conversions of p) beside the 32 matrix instructions of 64 keys and 128
-// channels.  So a workgroup
-// takes 128 rows, its four waves 32 each with 32x32x16 matrix instructions,
-// two workgroups share a CU where registers allow (up to 128 channels), and:
+// channels.  So a workgroup takes 128 rows, its four waves 32 each with
+// 32x32x16 matrix instructions, two workgroups share a CU where registers
+// allow (up to 128 channels), and:
 //   * 64 keys at a time, K and V as codes (half of what 16-bit operands
 //     would read from LDS), brought to LDS by DMA three tiles ahead: four
 //     buffers, one barrier per tile.  Each wave brings one block of 16 keys;
@@ -24,9 +24,9 @@
 //     fall out of step and one's exponentials run under another's matrix
 //     instructions; the second product follows each half's exponentials at
 //     once.
-// Measured, 2 x 2048 rows of 8 heads over 8192 keys of 128 channels: 488 to
-// 498 us by run, 965 to 986 TFLOP/s (a plain FP16 matrix product of 8192^3
-// reaches 1151 here).  Before the priority 512, with two buffers and one
+// Measured, 2 x 2048 tokens of 32 query and 8 KV heads over 8192 keys of 128
+// channels: 488 to 508 us by run and card, 947 to 986 TFLOP/s (a plain FP16
+// matrix product of 8192^3 reaches 1151 here).  Before the priority 512, with two buffers and one
 // loop for all tiles 530.  Slower: widening once per workgroup into LDS as
 // 16-bit operands 584, the next tile's scores under this one's exponentials
 // 602, the raised priority for the second product as well 503 or for the
