@@ -15,6 +15,12 @@ typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr float kNegInf = -__builtin_inff();
 
+// Softmax weights are held as 2^(x - m + kTop) with a reference m that is
+// left alone until a row's maximum passes it by kLazy: at most 2^15, inside
+// FP16, and a row's largest at least 2^(kTop - 1).
+constexpr float kLazy = 4.0f;
+constexpr float kTop = 11.0f;
+
 // Query types: K codes are widened to the query's type with scale 1, which
 // is exact for both (E4M3 spans 2^-9 .. 448), so the products see the query
 // unrounded; the block's scale multiplies the FP32 sums.

@@ -3,12 +3,14 @@
 // Mathematics.  For one KV head, the rows r = (new token, query head of the
 // group) are the columns of S^T = K Q^T, computed 64 keys at a time with
 // 16x16x32 matrix instructions.  With m the row's running reference,
-//     p = 2^(S k_scale scale log2(e) - m),  l += p,  O^T += V^T p^T,
+//     p = 2^(S k_scale scale log2(e) - m + 11),  l += p,  O^T += V^T p^T,
 // and out = O / l.  m moves only when a row's maximum passes it by more than
-// 2^8 (p stays below 256, in range of FP16), so the accumulators are
-// rarely multiplied.  l and O are FP32; p is rounded to FP16 (11 bits, an
-// order finer than a BF16 output) for the second product, and l sums the
-// unrounded p.
+// 2^4, so the accumulators are rarely multiplied.  l and O are FP32; p is
+// rounded to FP16 for the second product, and l sums the unrounded p.  The
+// largest p of a row is at least 2^10 (m is a maximum rounded up to a whole
+// number) and at most 2^15, inside FP16, which holds 11 bits of those down to
+// 2^-24 of the largest (an order finer than a BF16 output) and fewer down to
+// 2^-35 of it.
 //
 // Layout.  S^T keeps a row's statistics in one column: 16 of a row's 64
 // scores in one lane, the others in the lanes 16, 32 and 48 further.  The
@@ -55,7 +57,6 @@ namespace {
 
 using namespace dev;
 
-constexpr float kLazy = 8.0f;       // log2 growth of a row's maximum that is left alone
 constexpr int32_t kHeadroom = 7;    // V operands reach 448 * 2^7 < 65504
 constexpr int32_t kNoExp = -100000;
 constexpr uint32_t kInFlight = 16;  // partial loads of a thread at a time in the join: each is a
@@ -326,7 +327,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
         mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
         mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
         if (__ballot(mx > m + kLazy || vrescale != 1.0f)) {
-            const float mn = mx > m + kLazy ? mx : m;
+            const float mn = mx > m + kLazy ? ceilf(mx) : m;
             const float grow = m == kNegInf ? 0.0f : exp2_fast(m - mn);
             l *= grow;
             m = mn;
@@ -334,7 +335,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
             for (int x = 0; x < VT; ++x)
                 o[x] *= grow * vrescale;
         }
-        const float mu = m == kNegInf ? 0.0f : m;
+        const float mu = (m == kNegInf ? 0.0f : m) - kTop;
         u32x4_t p[2];
         if (masked && __ballot(!(ksc > 0.f))) {
             // a NaN scale must not reach hidden keys, nor a factor of 0 their -inf
@@ -498,7 +499,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
             store_agent(wst + (size_t)chunk * NR + tr, f32x4_t{mr, lr, (float)exp_all, 0.f});
         else if (a.lse)
             a.lse[(size_t)(t.first + tok) * a.q_heads + hq] =
-                none ? kNegInf : (mr + log2f(lr)) * 0.69314718055994531f;
+                none ? kNegInf : (mr - kTop + log2f(lr)) * 0.69314718055994531f;
     }
     if (alone)
         return;
@@ -604,7 +605,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
                        (int64_t)jh * a.out_head + 4 * c4, acc * scale);
         if (c4 == 0 && a.lse)
             a.lse[(size_t)(t.first + jtok) * a.q_heads + jh] =
-                empty ? kNegInf : (mg + log2f(lg)) * 0.69314718055994531f;
+                empty ? kNegInf : (mg - kTop + log2f(lg)) * 0.69314718055994531f;
     }
 }
 
@@ -699,7 +700,7 @@ __global__ __launch_bounds__(256) void w8a16_kv_join_kernel(AttnArgs a, uint32_t
                    (int64_t)hq * a.out_head + d, acc * inv * unit_e);
     if (lane == 0 && a.lse)
         a.lse[(size_t)(t.first + tok) * a.q_heads + hq] =
-            none ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
+            none ? kNegInf : (m - kTop + log2f(l)) * 0.69314718055994531f;
 }
 
 template <class Q, int DP>

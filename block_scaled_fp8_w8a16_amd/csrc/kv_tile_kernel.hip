@@ -1,8 +1,8 @@
 // Attention of many rows (prompts, prompt chunks) over the paged FP8 cache.
 //
 // The mathematics is that of the row kernel (kv_attention.hip): S^T = K Q^T,
-// p = 2^(S k_scale scale log2(e) - m) with a reference m that moves only by
-// more than 2^8, O^T += V^T p^T with p in FP16 and V widened by 2^(e - E).
+// p = 2^(S k_scale scale log2(e) - m + 11) with a reference m that moves only
+// by more than 2^4, O^T += V^T p^T with p in FP16 and V widened by 2^(e - E).
 // The issue of vector instructions bounds the time: a wave needs about 320
 // of them (128 conversions of codes, 32 exponentials, the rest sums, maxima
 // and conversions of p) beside the 32 matrix instructions of 64 keys and 128
@@ -50,7 +50,6 @@ using namespace dev;
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 constexpr uint32_t kRows = 128;      // rows per workgroup
-constexpr float kLazy = 8.0f;
 constexpr int32_t kHeadroom = 7;
 constexpr int32_t kNoExp = -100000;
 constexpr uint32_t kBuffers = 4;     // tiles in LDS: one in use, three on their way
@@ -251,7 +250,7 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
     // too much, and the outputs to their new unit.
     auto refer = [&](float top, float unit) {
         if (__ballot(top > m + kLazy || unit != 1.0f)) {
-            const float mn = top > m + kLazy ? top : m;
+            const float mn = top > m + kLazy ? ceilf(top) : m;
             const float grow = m == kNegInf ? 0.0f : exp2_fast(m - mn);
             l *= grow;
             m = mn;
@@ -297,7 +296,7 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
             vsc[x] = pow2_byte((uint32_t)(field < 7 ? 7 : field));
         }
         refer(max_halves(fmaxf(largest(s[0]) * c[0], largest(s[1]) * c[1])), unit);
-        const float mu = m == kNegInf ? 0.0f : m;
+        const float mu = (m == kNegInf ? 0.0f : m) - kTop;
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             u32x4_t p[2];
@@ -347,7 +346,7 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
             top = fmaxf(top, largest(s[x]) * c[x]);
         }
         refer(max_halves(top), unit);
-        const float mu = m == kNegInf ? 0.0f : m;
+        const float mu = (m == kNegInf ? 0.0f : m) - kTop;
         u32x4_t p[2][2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
@@ -538,7 +537,7 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
             }
         if (a.lse && h == 0)
             a.lse[(size_t)(t.first + tok) * a.q_heads + hq] =
-                none ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
+                none ? kNegInf : (m - kTop + log2f(l)) * 0.69314718055994531f;
         return;
     }
     // partial rows in the join kernel's order: ((b, head), rtile, chunk)

@@ -528,8 +528,10 @@ typedef struct w8a16_kv_attention_args {
     uint32_t q_heads, dtype, causal, window, max_kv;
 } w8a16_kv_attention_args_t;
 
-/* Sums and softmax statistics are FP32 and every order of addition is fixed
- * by the plan, so a plan gives the same bits on every run.  A plan with
+/* Sums and softmax statistics are FP32; in the sum of the values a weight is
+ * rounded to 11 bits, fewer below 2^-24 of the row's largest and none from
+ * 2^-35 on.  Every order of addition is fixed by the plan, so a plan gives
+ * the same bits on every run.  A plan with
  * chunks uses the (device, stream) workspace under the rules at the top of
  * this file (growth is refused during capture). */
 int w8a16_kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
