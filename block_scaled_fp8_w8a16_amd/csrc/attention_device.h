@@ -15,11 +15,38 @@ typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr float kNegInf = -__builtin_inff();
 
-// Softmax weights are held as 2^(x - m + kTop) with a reference m that is
-// left alone until a row's maximum passes it by kLazy: at most 2^15, inside
-// FP16, and a row's largest at least 2^(kTop - 1).
-constexpr float kLazy = 4.0f;
+// A row's running references.  With x the base-2 logarithm of a key's weight
+// before the softmax's division, and e the exponent of its block's V scale,
+//     l sums 2^(x - sum),   the outputs sum 2^(x + e - out) times V's codes:
+// the V scales ride on the weights, so a block enters only the rows that see
+// it, and V's codes are exact in FP16.  Both references are whole numbers
+// (moving them rounds nothing) and left alone until a maximum passes them by
+// too much: the operand, rounded to FP16, is at most 2^15, and a row's
+// largest at least 2^(kTop - 1).
 constexpr float kTop = 11.0f;
+constexpr float kLazy = 4.0f;
+constexpr float kUnset = -3.0e38f;     // of a row that has seen no key: below any, and
+                                       // finite, so that references can be subtracted
+constexpr float kFar = 60.0f;
+struct RowRef {
+    float sum = kUnset, out = kUnset;
+    // Whether `top`, the largest x of a block of exponent e, is too far above.
+    __device__ __forceinline__ bool passed(float top, float e) const
+    {
+        return top > sum + kLazy || top + e > out + (kTop + kLazy);
+    }
+    __device__ __forceinline__ void move(float top, float top_out)
+    {
+        sum = top > sum + kLazy ? ceilf(top) : sum;
+        out = top_out > out + (kTop + kLazy) ? ceilf(top_out) - kTop : out;
+    }
+    // What turns the operands of a block into the weights that l sums, as an
+    // exponent: one multiplication per block in place of an exponential per
+    // key.  Past kFar (a V scale far from the row's others) the operands may
+    // have left FP32's range where the weights have not: those blocks'
+    // weights are computed by themselves and the operands' sum is dropped.
+    __device__ __forceinline__ float shift(float e) const { return out - sum - e; }
+};
 
 // Query types: K codes are widened to the query's type with scale 1, which
 // is exact for both (E4M3 spans 2^-9 .. 448), so the products see the query
@@ -86,6 +113,12 @@ __device__ __forceinline__ uint32_t f16_pair(float a, float b)
 
 // 2^x of the hardware (within 1 ulp); 2^-inf is 0.
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// x * 2^n of a whole number n, subnormal results included.
+__device__ __forceinline__ float scale2(float x, float n)
+{
+    return ldexpf(x, (int)fminf(fmaxf(n, -400.0f), 400.0f));
+}
 
 __device__ __forceinline__ float pow2_byte(uint32_t byte)     // 2^(byte - 127), bytes 1..254
 {

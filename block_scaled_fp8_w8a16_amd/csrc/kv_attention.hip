@@ -3,14 +3,16 @@
 // Mathematics.  For one KV head, the rows r = (new token, query head of the
 // group) are the columns of S^T = K Q^T, computed 64 keys at a time with
 // 16x16x32 matrix instructions.  With m the row's running reference,
-//     p = 2^(S k_scale scale log2(e) - m + 11),  l += p,  O^T += V^T p^T,
-// and out = O / l.  m moves only when a row's maximum passes it by more than
-// 2^4, so the accumulators are rarely multiplied.  l and O are FP32; p is
-// rounded to FP16 for the second product, and l sums the unrounded p.  The
-// largest p of a row is at least 2^10 (m is a maximum rounded up to a whole
-// number) and at most 2^15, inside FP16, which holds 11 bits of those down to
-// 2^-24 of the largest (an order finer than a BF16 output) and fewer down to
-// 2^-35 of it.
+//     x = S k_scale scale log2(e),  l += 2^(x - m),  O^T += V^T p^T,  p = 2^(x + e - M + 11)
+// and out = O 2^(M - 11 - m) / l, where e is the exponent of the key's V
+// scale: V enters as its codes, exact in FP16, and its scales ride on p, so
+// that a block's scale is nothing to the rows that do not see the block.  m
+// and M move only when a row's maximum (of x and of x + e) passes them by
+// more than 4, so the accumulators are rarely multiplied.  l and O are FP32;
+// p is rounded to FP16 for the second product, and l sums FP32 weights.  The
+// largest p of a row is between 2^10 (M is a maximum rounded up to a whole
+// number) and 2^15; FP16 holds 11 bits of those down to 2^-24 of the largest
+// (an order finer than a BF16 output) and fewer down to 2^-35 of it.
 //
 // Layout.  S^T keeps a row's statistics in one column: 16 of a row's 64
 // scores in one lane, the others in the lanes 16, 32 and 48 further.  The
@@ -20,10 +22,6 @@
 // all its scores, and its p are in place as the second product's operand,
 // whose other side is one 16-byte load of V (16 keys of one channel).
 // Nothing passes through LDS before the waves' results are joined.
-//
-// V codes are widened to FP16 by 2^(e - E), e the block's scale exponent
-// and E the largest seen by the wave, at most 2^7 above it: exact for blocks
-// within 2^22 of the largest; O counts in units of 2^E.
 //
 // What bounds it: reading the cache.  64 sequences of up to 8192 tokens (8 KV
 // heads of 128 channels, 673 MB) take 139 us, 4.8 TB/s; one of 131072 tokens, cut
@@ -57,15 +55,14 @@ namespace {
 
 using namespace dev;
 
-constexpr int32_t kHeadroom = 7;    // V operands reach 448 * 2^7 < 65504
-constexpr int32_t kNoExp = -100000;
 constexpr uint32_t kInFlight = 16;  // partial loads of a thread at a time in the join: each is a
                                     // round trip past the L2
 
-// Four outputs of a row, rounded to its type.
-template <class E> __device__ __forceinline__ void store_row4(E *dst, f32x4_t v)
+// Four outputs of a row, v * 2^n, rounded to its type.
+template <class E> __device__ __forceinline__ void store_row4(E *dst, f32x4_t v, float n)
 {
-    const E e[4] = {static_cast<E>(v.x), static_cast<E>(v.y), static_cast<E>(v.z), static_cast<E>(v.w)};
+    const E e[4] = {static_cast<E>(scale2(v.x, n)), static_cast<E>(scale2(v.y, n)),
+                    static_cast<E>(scale2(v.z, n)), static_cast<E>(scale2(v.w, n))};
     if ((reinterpret_cast<uintptr_t>(dst) & 7u) == 0) {
         u32x2_t p;
         p.x = (uint32_t)__builtin_bit_cast(uint16_t, e[0]) | ((uint32_t)__builtin_bit_cast(uint16_t, e[1]) << 16);
@@ -96,9 +93,8 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
     constexpr int PART = 16 * (SEG + 4);
     static_assert(WAVES * PART >= (int)kKvMaxChunks * NR && WAVES * PART >= 4 * (int)THREADS, "LDS of the join");
     __shared__ __attribute__((aligned(16))) float part[WAVES * PART];   // [wave][16][SEG + 4]
-    __shared__ float stat[WAVES][NR][2];
+    __shared__ f32x4_t stat[WAVES][NR];      // sum reference, l, output reference
     __shared__ float red[2 * THREADS];
-    __shared__ int32_t exps[WAVES];
     __shared__ uint32_t last;
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -224,31 +220,18 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
     }
 
     f32x4_t o[VT];
-    float m = kNegInf, l = 0.f;
+    RowRef m;
+    float l = 0.f;
 #pragma unroll
     for (int v = 0; v < VT; ++v)
         o[v] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    int32_t exp_ref = kNoExp;
 
     auto compute = [&](uint32_t tile) {
         const int32_t key0 = (int32_t)(tile * kKvTile + 16u * g);   // the lane's first key
         const bool seen = key0 < t.hi && key0 + 16 > t.lo;      // some key of the block, by some row
         const float ksc = !seen ? 1.0f : (at.ok && at.ks - 1u < 254u ? pow2_byte(at.ks) * a.scale_log2
                                                                       : __builtin_nanf(""));
-        int32_t e = seen && at.vs - 1u < 254u ? (int32_t)at.vs - 127 : kNoExp;
-        int32_t emax = e;
-#pragma unroll
-        for (int off = 16; off <= 32; off <<= 1) {
-            const int32_t other = __shfl_xor(emax, off, 64);
-            emax = emax > other ? emax : other;
-        }
-        emax = __builtin_amdgcn_readfirstlane(emax);
-        float vrescale = 1.0f;
-        if (emax > exp_ref + kHeadroom) {
-            vrescale = exp_ref == kNoExp ? 0.0f : exp2_fast((float)(exp_ref - emax));
-            exp_ref = emax;
-        }
-        const float vsc = e == kNoExp || e - exp_ref < -120 ? pow2_byte(7) : pow2_byte((uint32_t)(e - exp_ref + 127));
+        const float e = (float)at.vs - 127.0f;     // (255 and 0, no scale: the codes become NaN)
 
         const bool masked = (int32_t)(tile * kKvTile) < t.all_lo ||
                             (int32_t)(tile * kKvTile + kKvTile) > t.all_hi;
@@ -324,18 +307,31 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
             for (int i = 0; i < 4; ++i)
                 mx = fmaxf(mx, s[x][i]);
         mx *= ksc;
-        mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-        mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-        if (__ballot(mx > m + kLazy || vrescale != 1.0f)) {
-            const float mn = mx > m + kLazy ? ceilf(mx) : m;
-            const float grow = m == kNegInf ? 0.0f : exp2_fast(m - mn);
-            l *= grow;
-            m = mn;
+        if (__ballot(m.passed(mx, e))) {
+            const RowRef was = m;
+            float top = mx, top_out = mx + e;
+#pragma unroll
+            for (int off = 16; off <= 32; off <<= 1) {
+                top = fmaxf(top, __shfl_xor(top, off, 64));
+                top_out = fmaxf(top_out, __shfl_xor(top_out, off, 64));
+            }
+            m.move(top, top_out);
+            l *= exp2_fast(was.sum - m.sum);
+            const float f = exp2_fast(was.out - m.out);
 #pragma unroll
             for (int x = 0; x < VT; ++x)
-                o[x] *= grow * vrescale;
+                o[x] *= f;
         }
-        const float mu = (m == kNegInf ? 0.0f : m) - kTop;
+        float shift = m.shift(e);
+        if (fabsf(shift) > kFar) {
+            shift = kNegInf;
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    l += s[x][i] == kNegInf ? 0.f : exp2_fast(fmaf(s[x][i], ksc, -m.sum));
+        }
+        const float mu = m.out - e;
         u32x4_t p[2];
         if (masked && __ballot(!(ksc > 0.f))) {
             // a NaN scale must not reach hidden keys, nor a factor of 0 their -inf
@@ -357,7 +353,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 sum += s[x][i];
-        l += sum;
+        l = fmaf(sum, exp2_fast(shift), l);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             p[u].x = f16_pair(s[2 * u][0], s[2 * u][1]);
@@ -390,8 +386,8 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
                 for (int i = 0; i < 4; ++i)
                     o[x][i] = n[i] > 0.f ? __builtin_nanf("") : o[x][i];
             }
-            o[x] = mfma16_f16(f16_from_fp8x8(v[x].x, v[x].y, vsc), p[0], o[x]);
-            o[x] = mfma16_f16(f16_from_fp8x8(v[x].z, v[x].w, vsc), p[1], o[x]);
+            o[x] = mfma16_f16(f16_from_fp8x8(v[x].x, v[x].y, 1.0f), p[0], o[x]);
+            o[x] = mfma16_f16(f16_from_fp8x8(v[x].z, v[x].w, 1.0f), p[1], o[x]);
         }
     };
 
@@ -423,49 +419,42 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
         compute(tile0 + tile);
     }
 
-    // join the waves: a common reference per row and a common exponent
+    // join the waves: common references per row
     l += __shfl_xor(l, 16, 64);
     l += __shfl_xor(l, 32, 64);
-    if (g == 0) {
-        stat[wave][col][0] = m;
-        stat[wave][col][1] = l;
-    }
-    if (lane == 0)
-        exps[wave] = exp_ref;
+    if (g == 0)
+        stat[wave][col] = f32x4_t{m.sum, l, m.out, 0.f};
     __syncthreads();
-    int32_t exp_all = exps[0];
-#pragma unroll
-    for (int w = 1; w < WAVES; ++w)
-        exp_all = exp_all > exps[w] ? exp_all : exps[w];
-    const float efac = exp_ref == kNoExp ? 0.f : exp2_fast((float)(exp_ref - exp_all));
     const uint32_t n_rows = t.rows - t.row0 < (uint32_t)NR ? t.rows - t.row0 : (uint32_t)NR;
     const uint32_t dim4 = pool.dim / 4;
-    // partial rows: [(b, head, rtile)][chunk][row][dim], then as many (m, l,
-    // exponent) quadruples
+    // partial rows: [(b, head, rtile)][chunk][row][dim], then as many (sum
+    // reference, l, output reference) quadruples
     const size_t tile_id = (size_t)grp * a.row_tiles + rtile;
     f32x4_t *const wo = reinterpret_cast<f32x4_t *>(a.ws) + tile_id * a.chunks * NR * dim4;
     f32x4_t *const wst = reinterpret_cast<f32x4_t *>(a.ws) + (size_t)gridDim.x * NR * dim4 +
                          tile_id * a.chunks * NR;
-    const float unit = exp_all == kNoExp ? 0.f : ldexpf(1.0f, exp_all);
-    float mall = kNegInf;
+    float out_all = kUnset;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w)
-        mall = fmaxf(mall, stat[w][col][0]);
-    // a wave that saw no key of the row (m = -inf) adds zeros
-    const float wave_fac = m == kNegInf ? 0.f : efac * exp2_fast(m - mall);
+        out_all = fmaxf(out_all, stat[w][col].z);
+    const float wave_fac = exp2_fast(m.out - out_all);
     constexpr uint32_t TPR = THREADS / NR;       // threads per row
     const uint32_t tr = threadIdx.x / TPR, row = t.row0 + tr;
-    float mr = kNegInf, lr = 0.f;
+    RowRef mr;
+    float lr = 0.f;
+    f32x4_t st_row[WAVES];
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+        st_row[w] = stat[w][tr];
+        mr.sum = fmaxf(mr.sum, st_row[w].x);
+        mr.out = fmaxf(mr.out, st_row[w].z);
+    }
 #pragma unroll
     for (int w = 0; w < WAVES; ++w)
-        mr = fmaxf(mr, stat[w][tr][0]);
-#pragma unroll
-    for (int w = 0; w < WAVES; ++w)
-        lr += stat[w][tr][1] *     // m = -inf: l is 0, or NaN
-              (stat[w][tr][0] == kNegInf ? 1.f : exp2_fast(stat[w][tr][0] - mr));
+        lr += st_row[w].y * exp2_fast(st_row[w].x - mr.sum);
     const uint32_t tok = a.by_group.div(row), hq = head * a.group + row - tok * a.group;
-    const bool none = mr == kNegInf && lr == 0.f;    // the row sees nothing
-    const float inv = (none ? 0.f : 1.0f / lr) * unit;
+    const bool none = mr.sum == kUnset && lr == 0.f;     // the row sees nothing
+    const float inv = none ? 0.f : 1.0f / lr, unit = mr.out - mr.sum;
     typename Q::elem *const dst = reinterpret_cast<typename Q::elem *>(a.out) +
                                   (int64_t)(t.first + tok) * a.out_token + (int64_t)hq * a.out_head;
 #pragma unroll
@@ -489,17 +478,17 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
             for (int w = 1; w < WAVES; ++w)
                 acc += *reinterpret_cast<const f32x4_t *>(&part[w * PART + tr * (SEG + 4) + c]);
             if (alone)
-                store_row4(dst + s0 + c, acc * inv);
+                store_row4(dst + s0 + c, acc * inv, unit);
             else
                 store_agent(wo + ((size_t)chunk * NR + tr) * dim4 + (s0 + c) / 4, acc);
         }
     }
     if (tr < n_rows && threadIdx.x % TPR == 0) {
         if (!alone)
-            store_agent(wst + (size_t)chunk * NR + tr, f32x4_t{mr, lr, (float)exp_all, 0.f});
+            store_agent(wst + (size_t)chunk * NR + tr, f32x4_t{mr.sum, lr, mr.out, 0.f});
         else if (a.lse)
             a.lse[(size_t)(t.first + tok) * a.q_heads + hq] =
-                none ? kNegInf : (mr - kTop + log2f(lr)) * 0.69314718055994531f;
+                none ? kNegInf : (mr.sum + log2f(lr)) * 0.69314718055994531f;
     }
     if (alone)
         return;
@@ -524,10 +513,10 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
     constexpr uint32_t SG = THREADS / NR, PER = kKvMaxChunks / SG;
     const uint32_t sr = tid % NR, sg = tid / NR;
     f32x4_t st[PER];
-    float mj = kNegInf, ex = (float)kNoExp;
+    float mj = kUnset, ex = kUnset;
 #pragma unroll
     for (uint32_t i = 0; i < PER; ++i) {
-        st[i] = f32x4_t{kNegInf, 0.f, (float)kNoExp, 0.f};
+        st[i] = f32x4_t{kUnset, 0.f, kUnset, 0.f};
         if (sr < n_rows && sg + i * SG < n)
             st[i] = load_agent(wst + (size_t)(sg + i * SG) * NR + sr);
     }
@@ -548,9 +537,8 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
 #pragma unroll
     for (uint32_t i = 0; i < PER; ++i)
         if (sg + i * SG < n) {
-            const float f = st[i].x == kNegInf ? 1.f : exp2_fast(st[i].x - mj);   // -inf: l is 0, or NaN
-            lj += f * st[i].y;
-            fac[(sg + i * SG) * NR + sr] = f * exp2_fast(st[i].z - ex);
+            lj += exp2_fast(st[i].x - mj) * st[i].y;
+            fac[(sg + i * SG) * NR + sr] = exp2_fast(st[i].z - ex);
         }
     __syncthreads();
     red[tid] = lj;
@@ -599,13 +587,13 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
             continue;
         const float mg = red[THREADS + jr], eg = red[THREADS + NR + jr], lg = red[THREADS + 2 * NR + jr];
         const uint32_t jtok = a.by_group.div(t.row0 + jr), jh = head * a.group + t.row0 + jr - jtok * a.group;
-        const bool empty = mg == kNegInf && lg == 0.f;
-        const float scale = empty ? 0.f : 1.0f / lg * ldexpf(1.0f, (int)eg);
+        const bool empty = mg == kUnset && lg == 0.f;
+        const float inv_all = empty ? 0.f : 1.0f / lg;
         store_row4(reinterpret_cast<typename Q::elem *>(a.out) + (int64_t)(t.first + jtok) * a.out_token +
-                       (int64_t)jh * a.out_head + 4 * c4, acc * scale);
+                       (int64_t)jh * a.out_head + 4 * c4, acc * inv_all, eg - mg);
         if (c4 == 0 && a.lse)
             a.lse[(size_t)(t.first + jtok) * a.q_heads + jh] =
-                empty ? kNegInf : (mg - kTop + log2f(lg)) * 0.69314718055994531f;
+                empty ? kNegInf : (mg + log2f(lg)) * 0.69314718055994531f;
     }
 }
 
@@ -643,8 +631,8 @@ __global__ __launch_bounds__(256) void w8a16_kv_join_kernel(AttnArgs a, uint32_t
     const float *wo = a.ws + first * dim;
     const float *wst = a.ws + (size_t)grid_rows * dim + first * 4u;
 
-    // the row's largest reference and exponent over all chunks
-    float m = kNegInf, ex = (float)kNoExp;
+    // the row's largest references over all chunks
+    float m = kUnset, ex = kUnset;
     for (uint32_t c = lane; c < n; c += 64u) {
         const f32x4_t st = *reinterpret_cast<const f32x4_t *>(wst + (size_t)c * tile_rows * 4u);
         m = fmaxf(m, st.x);
@@ -662,9 +650,8 @@ __global__ __launch_bounds__(256) void w8a16_kv_join_kernel(AttnArgs a, uint32_t
         float fac = 0.f;
         if (c0 + lane < n) {
             const f32x4_t st = *reinterpret_cast<const f32x4_t *>(wst + (size_t)(c0 + lane) * tile_rows * 4u);
-            const float f = st.x == kNegInf ? 1.f : exp2_fast(st.x - m);   // -inf: l is 0, or NaN
-            l += f * st.y;
-            fac = f * exp2_fast(st.z - ex);
+            l += exp2_fast(st.x - m) * st.y;
+            fac = exp2_fast(st.z - ex);
         }
         const uint32_t stop = n - c0 < 64u ? n - c0 : 64u;
         for (uint32_t base = 0; base < stop; base += 4u * groups) {    // all lanes: each lends its factor
@@ -694,13 +681,13 @@ __global__ __launch_bounds__(256) void w8a16_kv_join_kernel(AttnArgs a, uint32_t
     if (lane >= per)
         return;
     const uint32_t tok = a.by_group.div(row), hq = head * a.group + row - tok * a.group;
-    const bool none = m == kNegInf && l == 0.f;
-    const float inv = none ? 0.f : 1.0f / l, unit_e = none ? 0.f : ldexpf(1.0f, (int)ex);
+    const bool none = m == kUnset && l == 0.f;
+    const float inv = none ? 0.f : 1.0f / l;
     store_row4(reinterpret_cast<E *>(a.out) + (int64_t)(t.first + tok) * a.out_token +
-                   (int64_t)hq * a.out_head + d, acc * inv * unit_e);
+                   (int64_t)hq * a.out_head + d, acc * inv, ex - m);
     if (lane == 0 && a.lse)
         a.lse[(size_t)(t.first + tok) * a.q_heads + hq] =
-            none ? kNegInf : (m - kTop + log2f(l)) * 0.69314718055994531f;
+            none ? kNegInf : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 template <class Q, int DP>

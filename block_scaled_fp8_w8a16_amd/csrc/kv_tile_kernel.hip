@@ -1,8 +1,8 @@
 // Attention of many rows (prompts, prompt chunks) over the paged FP8 cache.
 //
 // The mathematics is that of the row kernel (kv_attention.hip): S^T = K Q^T,
-// p = 2^(S k_scale scale log2(e) - m + 11) with a reference m that moves only
-// by more than 2^4, O^T += V^T p^T with p in FP16 and V widened by 2^(e - E).
+// l += 2^(x - m), O^T += V^T p^T, p = 2^(x + e - M + 11) in FP16, V as its
+// codes.
 // The issue of vector instructions bounds the time: a wave needs about 320
 // of them (128 conversions of codes, 32 exponentials, the rest sums, maxima
 // and conversions of p) beside the 32 matrix instructions of 64 keys and 128
@@ -36,6 +36,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "attention.h"
 #include "attention_device.h"
 #include "device_common.h"
@@ -50,8 +52,6 @@ using namespace dev;
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 constexpr uint32_t kRows = 128;      // rows per workgroup
-constexpr int32_t kHeadroom = 7;
-constexpr int32_t kNoExp = -100000;
 constexpr uint32_t kBuffers = 4;     // tiles in LDS: one in use, three on their way
 
 template <class Q> __device__ __forceinline__ f32x16_t mfma32(u32x4_t a, u32x4_t b, f32x16_t c);
@@ -210,8 +210,8 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             o[x][i] = 0.f;
-    float m = kNegInf, l = 0.f;
-    int32_t exp_ref = kNoExp;
+    RowRef m;
+    float l = 0.f;
 
     // LDS offsets of the lane's K row for each chunk pair, and of its V row
     const uint32_t krow = 16u * ((col >> 2) & 1u) + 4u * (col >> 3) + (col & 3u);
@@ -237,30 +237,40 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
         return *reinterpret_cast<const u32x4_t *>(lds + buf * BUF + (4u + 2u * x + h) * BLK +
                                                   (32u * d + col) * 16u);
     };
-    // The outputs' unit for blocks up to 2^emax: what they change by.
-    auto unit_for = [&](int32_t emax) {
-        float f = 1.0f;
-        if (emax > exp_ref + kHeadroom) {
-            f = exp_ref == kNoExp ? 0.0f : exp2_fast((float)(exp_ref - emax));
-            exp_ref = emax;
-        }
-        return f;
-    };
-    // Moves a row's reference if `top`, the tile's largest score, passes it by
-    // too much, and the outputs to their new unit.
-    auto refer = [&](float top, float unit) {
-        if (__ballot(top > m + kLazy || unit != 1.0f)) {
-            const float mn = top > m + kLazy ? ceilf(top) : m;
-            const float grow = m == kNegInf ? 0.0f : exp2_fast(m - mn);
-            l *= grow;
-            m = mn;
-            const float f = grow * unit;
+    // Moves a row's references if the tile's largest score passes them by too
+    // much; mx: the largest of each half in this lane, e its V exponent.
+    auto refer = [&](const float (&mx)[2], const float (&e)[2]) {
+        if (__ballot(m.passed(mx[0], e[0]) || m.passed(mx[1], e[1]))) {
+            const RowRef was = m;
+            m.move(max_halves(fmaxf(mx[0], mx[1])), max_halves(fmaxf(mx[0] + e[0], mx[1] + e[1])));
+            l *= exp2_fast(was.sum - m.sum);
+            const float f = exp2_fast(was.out - m.out);
 #pragma unroll
             for (int x = 0; x < VT; ++x)
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
                     o[x][i] *= f;
         }
+    };
+    // Scores of one block to operands of the second product, and to l; hidden:
+    // some may be -inf under a scale of NaN or 0.
+    auto weigh = [&](f32x16_t &s, float c, float e, auto hidden) {
+        const float mu = m.out - e;
+        float shift = m.shift(e);
+        if (fabsf(shift) > kFar) {
+            shift = kNegInf;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                l += s[i] == kNegInf ? 0.f : exp2_fast(fmaf(s[i], c, -m.sum));
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float v = exp2_fast(fmaf(s[i], c, -mu));
+            s[i] = decltype(hidden)::value && s[i] == kNegInf ? 0.f : v;
+            sum += s[i];
+        }
+        l = fmaf(sum, exp2_fast(shift), l);
     };
     auto largest = [&](const f32x16_t &s) {
         float mx = s[0];
@@ -277,42 +287,29 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
 
     // A tile that every row of the workgroup sees, its blocks all with scales.
     auto whole = [&](uint32_t buf) {
-        Scale sc[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-            sc[x] = scl[buf][2 * x + h];
-        const uint32_t vmax = sc[0].vs > sc[1].vs ? sc[0].vs : sc[1].vs;
-        const int32_t v0 = __builtin_amdgcn_readlane((int)vmax, 0), v1 = __builtin_amdgcn_readlane((int)vmax, 32);
-        const float unit = unit_for((v0 > v1 ? v0 : v1) - 127);
         f32x16_t s[2];
-        float c[2], vsc[2];
+        float c[2], e[2], mx[2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
+            const Scale sc = scl[buf][2 * x + h];
             __builtin_amdgcn_s_setprio(1);
             s[x] = products(buf, x);
             __builtin_amdgcn_s_setprio(0);
-            c[x] = pow2_byte(sc[x].ks) * a.scale_log2;
-            const int32_t field = (int32_t)sc[x].vs - exp_ref;        // exponent field of 2^(e - E)
-            vsc[x] = pow2_byte((uint32_t)(field < 7 ? 7 : field));
+            c[x] = pow2_byte(sc.ks) * a.scale_log2;
+            e[x] = (float)sc.vs - 127.0f;
+            mx[x] = largest(s[x]) * c[x];
         }
-        refer(max_halves(fmaxf(largest(s[0]) * c[0], largest(s[1]) * c[1])), unit);
-        const float mu = (m == kNegInf ? 0.0f : m) - kTop;
+        refer(mx, e);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             u32x4_t p[2];
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                s[x][i] = exp2_fast(fmaf(s[x][i], c[x], -mu));
-                sum += s[x][i];
-            }
-            l += sum;
+            weigh(s[x], c[x], e[x], std::false_type{});
             pack(s[x], p);
 #pragma unroll
             for (int d = 0; d < VT; ++d) {
                 const u32x4_t raw = v_frag(buf, x, d);
-                o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.x, raw.y, vsc[x]), p[0], o[d]);
-                o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.z, raw.w, vsc[x]), p[1], o[d]);
+                o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.x, raw.y, 1.0f), p[0], o[d]);
+                o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.z, raw.w, 1.0f), p[1], o[d]);
             }
         }
     };
@@ -320,45 +317,26 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
     // Any tile: some rows may not see all of it, blocks may have no scale.
     auto partly = [&](uint32_t tile, uint32_t buf) {
         const int32_t tk = (int32_t)(tile * kKvTile), key0 = tk + 16 * (int32_t)h;   // of half x: + 32 x
-        float c[2], vsc[2];
-        int32_t e[2];
+        f32x16_t s[2];
+        float c[2], e[2], mx[2];
         uint32_t poison[2];      // a block without a V scale reads as NaN codes
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const Scale sc = scl[buf][2 * x + h];
             c[x] = sc.ks - 1u >= 254u ? __builtin_nanf("") : pow2_byte(sc.ks) * a.scale_log2;
+            e[x] = (float)sc.vs - 127.0f;
             poison[x] = sc.vs - 1u >= 254u ? 0x7f7f7f7fu : 0u;
-            e[x] = poison[x] || key0 + 32 * x >= w.hi ? kNoExp : (int32_t)sc.vs - 127;
-        }
-        const int32_t emax = e[0] > e[1] ? e[0] : e[1];
-        const int32_t e0 = __builtin_amdgcn_readlane(emax, 0), e1 = __builtin_amdgcn_readlane(emax, 32);
-        const float unit = unit_for(e0 > e1 ? e0 : e1);
-        f32x16_t s[2];
-        float top = kNegInf;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            vsc[x] = e[x] == kNoExp || e[x] - exp_ref < -120 ? pow2_byte(7)
-                                                             : pow2_byte((uint32_t)(e[x] - exp_ref + 127));
             s[x] = products(buf, x);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 s[x][i] = key0 + 32 * x + i >= rlo && key0 + 32 * x + i < rhi ? s[x][i] : kNegInf;
-            top = fmaxf(top, largest(s[x]) * c[x]);
+            mx[x] = largest(s[x]) * c[x];
         }
-        refer(max_halves(top), unit);
-        const float mu = (m == kNegInf ? 0.0f : m) - kTop;
+        refer(mx, e);
         u32x4_t p[2][2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                // a NaN scale must not reach hidden keys
-                const float v = exp2_fast(fmaf(s[x][i], c[x], -mu));
-                s[x][i] = s[x][i] == kNegInf ? 0.f : v;
-                sum += s[x][i];
-            }
-            l += sum;
+            weigh(s[x], c[x], e[x], std::true_type{});
             pack(s[x], p[x]);
         }
         // Codes of half x that some row of the wave may see.
@@ -389,8 +367,8 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
                     any |= nan;
                     raw[i] &= ~((nan >> 7) * 0xffu);
                 }
-                o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.x, raw.y, vsc[x]), p[x][0], o[d]);
-                o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.z, raw.w, vsc[x]), p[x][1], o[d]);
+                o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.x, raw.y, 1.0f), p[x][0], o[d]);
+                o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.z, raw.w, 1.0f), p[x][1], o[d]);
             }
         if (__ballot(any != 0)) {
             // NaN for the rows that do see one: a product that counts them
@@ -504,10 +482,10 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
     l += __shfl_xor(l, 32, 64);
     if (row >= t.rows)
         return;
-    const bool none = m == kNegInf && l == 0.f;
+    const bool none = m.sum == kUnset && l == 0.f;
     if (alone) {
         const float inv = none ? 0.f : 1.0f / l;
-        const float unit = exp_ref == kNoExp ? 0.f : ldexpf(1.0f, exp_ref);
+        const float unit = m.out - m.sum;
         typename Q::elem *dst = reinterpret_cast<typename Q::elem *>(a.out) +
                                 (int64_t)(t.first + tok) * a.out_token + (int64_t)hq * a.out_head;
         const bool wide = (reinterpret_cast<uintptr_t>(dst) & 7u) == 0;
@@ -521,7 +499,7 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
                 typename Q::elem v[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    v[i] = static_cast<typename Q::elem>(o[d][4 * g + i] * inv * unit);
+                    v[i] = static_cast<typename Q::elem>(scale2(o[d][4 * g + i] * inv, unit));
                 if (wide) {
                     u32x2_t pk;
                     pk.x = (uint32_t)__builtin_bit_cast(uint16_t, v[0]) |
@@ -537,7 +515,7 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
             }
         if (a.lse && h == 0)
             a.lse[(size_t)(t.first + tok) * a.q_heads + hq] =
-                none ? kNegInf : (m - kTop + log2f(l)) * 0.69314718055994531f;
+                none ? kNegInf : (m.sum + log2f(l)) * 0.69314718055994531f;
         return;
     }
     // partial rows in the join kernel's order: ((b, head), rtile, chunk)
@@ -554,9 +532,9 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
                     f32x4_t{o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
         }
     if (h == 0) {
-        wst[0] = m;
+        wst[0] = m.sum;
         wst[1] = l;
-        wst[2] = (float)exp_ref;
+        wst[2] = m.out;
     }
 }
 

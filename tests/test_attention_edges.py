@@ -90,3 +90,89 @@ def test_weights_far_below_the_largest(w8, gap, dtype):
     q = np.zeros(32, np.float32)
     q[0] = 1
     compare_row(w8, cache, table, 4096, q, gap, PLANS, dtype)
+
+
+def rows_of(w8, cache, table, total, new, q, p, window):
+    out, lse = w8.kv_attention(q, cache.to(w8), i32([list(map(int, table))]), i32([total]), window=window,
+                               return_lse=True, plan_=p, max_new=new)
+    return out.cpu(), lse.cpu()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("byte", [1, 160, 254])
+@pytest.mark.parametrize("p", PLANS, ids=name)
+@pytest.mark.parametrize("dim", [64, 128, 192])
+def test_scales_of_hidden_blocks_change_nothing(w8, byte, p, dim):
+    """A block's V scale of any size changes only the rows that see the
+    block: bit for bit in the others, whether it lies before every row's
+    window in the first tile they read, before some rows' windows, or on
+    tokens that only later rows see."""
+    if p.waves == 8 and dim > 128:
+        p = plan(ROWS, 1000)
+    rng = np.random.default_rng(2)
+    total, new, group = 200, 40, 2
+    cache, table = flat_cache(rng, total, 16, dim)
+    cache.k[:] = rng.integers(0x20, 0x38, cache.k.shape) + 0x80 * rng.integers(0, 2, cache.k.shape)
+    q = cuda(rng.normal(size=(new, group, dim)), torch.bfloat16)
+    pos = np.arange(total - new, total)
+    for window, block in ((70, 4), (70, 6), (0, 12), (0, 11), (70, 11)):
+        plain = rows_of(w8, cache, table, total, new, q, p, window)
+        other = ref.Cache(cache.pages, 1, 16, dim)
+        for a, b in zip((other.k, other.v, other.ks, other.vs), (cache.k, cache.v, cache.ks, cache.vs)):
+            a[:] = b
+        other.vs[table[block], 0, 0] = byte
+        got = rows_of(w8, other, table, total, new, q, p, window)
+        lo = np.maximum(0, pos - window + 1) if window else 0 * pos
+        sees = torch.from_numpy((pos >= 16 * block) & (lo < 16 * block + 16))
+        assert (~sees).any()
+        for a, b in zip(got, plain):
+            assert torch.equal(a[~sees], b[~sees]), (window, block)
+        if sees.any():
+            assert not torch.equal(got[0][sees], plain[0][sees])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("up", [18, 40, 100])
+def test_a_large_block_of_little_weight(w8, up):
+    """A block whose V scale is 2^up larger but whose keys weigh next to
+    nothing leaves the others their precision."""
+    cache, table = flat_cache(np.random.default_rng(3), 700, 32, 48)
+    cache.k[1, 0, 16:, 0] = 0xB8                # block 3: keys of -1
+    cache.vs[1, 0, 1] = 127 + up
+    q = np.zeros(48, np.float32)
+    q[0] = 1
+    compare_row(w8, cache, table, 700, q, up * math.log(2) + 12, PLANS, "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("up", [12, 15, 18, 22])
+def test_subnormal_codes_beside_a_larger_block(w8, up):
+    """Equal weights, one block 2^up larger with codes of zero in most
+    channels, the others of subnormal codes: these keep their precision."""
+    rng = np.random.default_rng(4)
+    cache, table = flat_cache(rng, 600, 16, 64)
+    cache.v[:] = rng.integers(1, 8, cache.v.shape)
+    cache.v[7] = 0
+    cache.v[7, 0, 0, ::8] = 0x38
+    cache.vs[7, 0, 0] = 127 + up
+    compare_row(w8, cache, table, 600, np.zeros(64, np.float32), 1.0, PLANS)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("bytes_", [(1, 127), (1, 240), (1, 254)])
+def test_blocks_of_every_scale(w8, bytes_):
+    """V scales at both ends of their range in one row, zero codes (what an
+    append of zeros stores: byte 1) among them; the sums see the keys of all
+    blocks."""
+    rng = np.random.default_rng(5)
+    cache, table = flat_cache(rng, 900, 16, 32)
+    small = rng.random(cache.vs.shape[0]) < 0.5
+    cache.v[small] = 0
+    cache.vs[small], cache.vs[~small] = bytes_
+    if bytes_[1] > 240:
+        cache.v[~small] = rng.integers(1, 8, cache.v[~small].shape)      # within the type's range
+    cache.k[:] = rng.integers(0x20, 0x38, cache.k.shape) + 0x80 * rng.integers(0, 2, cache.k.shape)
+    q = rounded(rng.normal(size=32), "bf16")
+    compare_row(w8, cache, table, 900, q, 0.4, PLANS, "bf16")
+    cache.vs[:], cache.v[:] = rng.integers(1, 240, cache.vs.shape), rng.integers(0, 0x7F, cache.v.shape)
+    compare_row(w8, cache, table, 900, q, 3.0, PLANS, "bf16")
