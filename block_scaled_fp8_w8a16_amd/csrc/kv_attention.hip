@@ -88,7 +88,8 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
     constexpr int QC = DP / 64;       // 64-channel groups of the first product
     constexpr int VT = DP / 16;       // 16-channel tiles of the second
     constexpr uint32_t THREADS = 64 * WAVES;
-    constexpr int SEG = DP < 128 || WAVES > 4 ? 64 : 128;    // channels joined at a time
+    constexpr int SEG = DP % 128 || WAVES > 4 ? 64 : 128;    // channels joined at a time
+    static_assert(DP % SEG == 0, "the join's passes take whole output tiles");
     constexpr int NR = 16;            // rows
     constexpr int PART = 16 * (SEG + 4);
     static_assert(WAVES * PART >= (int)kKvMaxChunks * NR && WAVES * PART >= 4 * (int)THREADS, "LDS of the join");
