@@ -95,6 +95,9 @@ struct AttnArgs {
     FastDiv by_group;
     uint32_t q_heads, causal, window;
     uint32_t row_tiles, chunks, chunk_tiles;
+    uint32_t grid;             // workgroups of the plan; the launch's others look at the token axis
+                               // for tokens that no sequence brings
+    uint32_t fill_tokens;      // that one of their waves takes (at most 64)
 };
 
 constexpr uint32_t kKvTile = 64;                // keys per tile
@@ -103,10 +106,16 @@ hipError_t launch_rope_table(const w8a16_rope_config_t &c, float *table, uint32_
                              uint32_t rot_dim, hipStream_t stream);
 hipError_t launch_rope(const RopeArgs &a, uint32_t dtype, hipStream_t stream);
 hipError_t launch_kv_append(const AppendArgs &a, uint32_t dtype, hipStream_t stream);
+// Workgroups of the attention's launch: the plan's and, where offsets are
+// given, those of the tokens outside them.
+inline uint64_t kv_launch_groups(const AttnArgs &a, uint32_t waves)
+{
+    const uint32_t tokens = a.fill_tokens * waves;
+    return (uint64_t)a.grid + (a.seqs.cu ? (a.seqs.tokens + tokens - 1) / tokens : 0u);
+}
 hipError_t launch_kv_rows(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t dtype,
                           hipStream_t stream);
-hipError_t launch_kv_tile(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t dtype,
-                          hipStream_t stream);
+hipError_t launch_kv_tile(const AttnArgs &a, uint32_t dtype, hipStream_t stream);
 // Adds the chunks' partial results of the tile kernel; max_rows: rows of the
 // longest sequence.
 hipError_t launch_kv_join(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t max_rows,

@@ -403,6 +403,14 @@ int kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
         return st;
     AttnArgs a;
     std::memset(static_cast<void *>(&a), 0, sizeof a);
+    a.seqs = seqs_of(*seqs);
+    a.grid = p.grid;
+    // (a long token axis by some 512 workgroups)
+    const uint32_t fill = seqs->tokens / (512u * p.waves) + 1;
+    a.fill_tokens = fill < 64u ? fill : 64u;
+    if (kv_launch_groups(a, p.waves) * 64ull * p.waves > kMaxThreads)
+        return refuse(W8A16_ERR_SHAPE, "%s: %u tokens of %u sequences are too many for one call", entry,
+                      seqs->tokens, seqs->seqs);
     if (p.workspace_bytes) {
         w8a16_plan_t need;
         std::memset(&need, 0, sizeof need);
@@ -417,7 +425,6 @@ int kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
         a.counters = ws.counters;
     }
     a.pool = pool_of(*cache);
-    a.seqs = seqs_of(*seqs);
     a.q = static_cast<const uint8_t *>(g->q);
     a.out = static_cast<uint8_t *>(g->out);
     a.lse = g->lse;
@@ -435,7 +442,7 @@ int kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
     a.chunks = p.chunks;
     a.chunk_tiles = p.chunk_tiles;
     e = p.kernel == W8A16_KV_ROWS ? launch_kv_rows(a, p, g->dtype, stream)
-                                  : launch_kv_tile(a, p, g->dtype, stream);
+                                  : launch_kv_tile(a, g->dtype, stream);
     if (e == hipSuccess && p.kernel == W8A16_KV_TILE && p.chunks > 1)
         e = launch_kv_join(a, p, seqs->max_new * group, g->dtype, stream);
     if (e != hipSuccess)

@@ -182,5 +182,62 @@ __device__ __forceinline__ void row_range(const AttnArgs &a, const RowTile &t, u
     lo = a.window && p >= (int32_t)a.window ? p - (int32_t)a.window + 1 : 0;
 }
 
+// Four outputs of a row, v * 2^n, rounded to its type.
+template <class E> __device__ __forceinline__ void store_row4(E *dst, f32x4_t v, float n)
+{
+    const E e[4] = {static_cast<E>(scale2(v.x, n)), static_cast<E>(scale2(v.y, n)),
+                    static_cast<E>(scale2(v.z, n)), static_cast<E>(scale2(v.w, n))};
+    if ((reinterpret_cast<uintptr_t>(dst) & 7u) == 0) {
+        u32x2_t p;
+        p.x = (uint32_t)__builtin_bit_cast(uint16_t, e[0]) | ((uint32_t)__builtin_bit_cast(uint16_t, e[1]) << 16);
+        p.y = (uint32_t)__builtin_bit_cast(uint16_t, e[2]) | ((uint32_t)__builtin_bit_cast(uint16_t, e[3]) << 16);
+        *reinterpret_cast<u32x2_t *>(dst) = p;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            dst[i] = e[i];
+    }
+}
+
+// Zeros, and log-sums of -inf, for the rows of tokens that no sequence
+// brings, among those of this wave: each of workgroup `part`'s `waves` waves
+// takes fill_tokens of the token axis and lays its lanes over the sequences.
+// Beside the attention's own workgroups it costs little: 64 sequences of 300
+// tokens 9.2 us with no token left out, 10.7 with 192.
+template <class E>
+__device__ __forceinline__ void fill_unowned(const AttnArgs &a, uint32_t part, uint32_t waves)
+{
+    const KvSeqs &s = a.seqs;
+    const uint32_t lane = threadIdx.x & 63u, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t t0 = (part * waves + wave) * a.fill_tokens;
+    if (t0 >= s.tokens)
+        return;
+    const uint32_t n = s.tokens - t0 < a.fill_tokens ? s.tokens - t0 : a.fill_tokens;
+    uint64_t left = n < 64u ? (1ull << n) - 1u : ~0ull;      // a bit per token
+    for (uint32_t b0 = 0; b0 < s.seqs; b0 += 64u) {
+        uint32_t first = ~0u, end = 0;
+        if (b0 + lane < s.seqs) {
+            first = (uint32_t)s.cu[b0 + lane];
+            end = (uint32_t)s.cu[b0 + lane + 1];
+        }
+        if (end > s.tokens)
+            end = 0;
+        for (uint32_t i = 0; i < n; ++i)
+            if (__ballot(t0 + i >= first && t0 + i < end))
+                left &= ~(1ull << i);
+    }
+    const uint32_t pieces = a.pool.dim / 4, all = a.q_heads * pieces;
+    for (; left; left &= left - 1) {
+        const size_t t = t0 + (uint32_t)__builtin_ctzll(left);
+        for (uint32_t i = lane; i < all; i += 64u) {
+            const uint32_t h = i / pieces;
+            store_row4(reinterpret_cast<E *>(a.out) + (int64_t)t * a.out_token + (int64_t)h * a.out_head +
+                           4 * (i - h * pieces), f32x4_t{0.f, 0.f, 0.f, 0.f}, 0.f);
+        }
+        for (uint32_t h = lane; a.lse && h < a.q_heads; h += 64u)
+            a.lse[t * a.q_heads + h] = kNegInf;
+    }
+}
+
 }  // namespace dev
 }  // namespace w8a16

@@ -58,23 +58,6 @@ using namespace dev;
 constexpr uint32_t kInFlight = 16;  // partial loads of a thread at a time in the join: each is a
                                     // round trip past the L2
 
-// Four outputs of a row, v * 2^n, rounded to its type.
-template <class E> __device__ __forceinline__ void store_row4(E *dst, f32x4_t v, float n)
-{
-    const E e[4] = {static_cast<E>(scale2(v.x, n)), static_cast<E>(scale2(v.y, n)),
-                    static_cast<E>(scale2(v.z, n)), static_cast<E>(scale2(v.w, n))};
-    if ((reinterpret_cast<uintptr_t>(dst) & 7u) == 0) {
-        u32x2_t p;
-        p.x = (uint32_t)__builtin_bit_cast(uint16_t, e[0]) | ((uint32_t)__builtin_bit_cast(uint16_t, e[1]) << 16);
-        p.y = (uint32_t)__builtin_bit_cast(uint16_t, e[2]) | ((uint32_t)__builtin_bit_cast(uint16_t, e[3]) << 16);
-        *reinterpret_cast<u32x2_t *>(dst) = p;
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            dst[i] = e[i];
-    }
-}
-
 // What a wave needs to know to load a tile.
 struct TileAt {
     const uint8_t *k, *v;     // this lane's rows of the tile's K and V
@@ -174,8 +157,11 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
     }
 
     RowTile t;
-    if (!seq_extent(a.seqs, b, t))
+    if (!seq_extent(a.seqs, b, t) || chunk >= a.chunks) {
+        if (chunk >= a.chunks)
+            fill_unowned<typename Q::elem>(a, blockIdx.x - a.grid, WAVES);
         return;
+    }
     t.rows = t.count * a.group;
     t.row0 = rtile * NR;
     if (t.row0 >= t.rows)
@@ -362,10 +348,10 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
             p[u].z = f16_pair(s[2 * u + 1][0], s[2 * u + 1][1]);
             p[u].w = f16_pair(s[2 * u + 1][2], s[2 * u + 1][3]);
         }
+        if (hit) {
+            // NaN codes: counted for the rows that see them, then zeroed
 #pragma unroll
-        for (int x = 0; x < VT; ++x) {
-            if (hit) {
-                // NaN codes: counted for the rows that see them, then zeroed
+            for (int x = 0; x < VT; ++x) {
                 u32x4_t bad[2], seen[2];
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
@@ -387,6 +373,9 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
                 for (int i = 0; i < 4; ++i)
                     o[x][i] = n[i] > 0.f ? __builtin_nanf("") : o[x][i];
             }
+        }
+#pragma unroll
+        for (int x = 0; x < VT; ++x) {
             o[x] = mfma16_f16(f16_from_fp8x8(v[x].x, v[x].y, 1.0f), p[0], o[x]);
             o[x] = mfma16_f16(f16_from_fp8x8(v[x].z, v[x].w, 1.0f), p[1], o[x]);
         }
@@ -432,7 +421,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
     // reference, l, output reference) quadruples
     const size_t tile_id = (size_t)grp * a.row_tiles + rtile;
     f32x4_t *const wo = reinterpret_cast<f32x4_t *>(a.ws) + tile_id * a.chunks * NR * dim4;
-    f32x4_t *const wst = reinterpret_cast<f32x4_t *>(a.ws) + (size_t)gridDim.x * NR * dim4 +
+    f32x4_t *const wst = reinterpret_cast<f32x4_t *>(a.ws) + (size_t)a.grid * NR * dim4 +
                          tile_id * a.chunks * NR;
     float out_all = kUnset;
 #pragma unroll
@@ -694,13 +683,14 @@ __global__ __launch_bounds__(256) void w8a16_kv_join_kernel(AttnArgs a, uint32_t
 template <class Q, int DP>
 hipError_t launch_dim(const AttnArgs &a, const w8a16_kv_plan_t &p, hipStream_t stream)
 {
+    const dim3 grid((uint32_t)kv_launch_groups(a, p.waves));
     if constexpr (DP <= 128) {
         if (p.waves == 8) {
-            hipLaunchKernelGGL((w8a16_kv_rows_kernel<Q, DP, 8>), dim3(p.grid), dim3(512), 0, stream, a);
+            hipLaunchKernelGGL((w8a16_kv_rows_kernel<Q, DP, 8>), grid, dim3(512), 0, stream, a);
             return hipGetLastError();
         }
     }
-    hipLaunchKernelGGL((w8a16_kv_rows_kernel<Q, DP, 4>), dim3(p.grid), dim3(256), 0, stream, a);
+    hipLaunchKernelGGL((w8a16_kv_rows_kernel<Q, DP, 4>), grid, dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 

@@ -512,8 +512,10 @@ typedef struct w8a16_kv_plan {
  * query head h, KV head h / (q_heads / kv_heads):
  *   out = sum_j softmax_j(scale * q . k_j) v_j,  lse = ln sum_j exp(scale * q . k_j)
  * over the visible keys j < kv_lens[b]; causal: j <= p; window > 0:
- * j > p - window.  A row that sees nothing gives zeros and lse = -inf; what
- * hidden places hold, NaN included, changes nothing.  q, out: [tokens,
+ * j > p - window.  A row that sees nothing gives zeros and lse = -inf, and so
+ * does a token that no sequence brings: outside all of cu_seqlens' ranges, or
+ * in one that ends past the token axis.  What hidden places hold, NaN
+ * included, changes nothing.  q, out: [tokens,
  * q_heads, head_dim] of `dtype` (BF16 or FP16); lse: FP32 [tokens, q_heads]
  * contiguous, or null.  max_kv: at least the largest kv_lens (0: the block
  * table's width); it shapes the launch only, longer sequences stay right.

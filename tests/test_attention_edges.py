@@ -176,3 +176,42 @@ def test_blocks_of_every_scale(w8, bytes_):
     compare_row(w8, cache, table, 900, q, 0.4, PLANS, "bf16")
     cache.vs[:], cache.v[:] = rng.integers(1, 240, cache.vs.shape), rng.integers(0, 0x7F, cache.v.shape)
     compare_row(w8, cache, table, 900, q, 3.0, PLANS, "bf16")
+
+
+def attend_into(w8, q, cache, table, lens, cu, p, max_new):
+    """out and lse over memory that held 7 everywhere."""
+    out = torch.full((q.shape[0], q.shape[1], q.shape[2] + 4), 7.0, dtype=q.dtype, device="cuda")
+    for _ in range(4):      # what the call's lse may be allocated from
+        torch.full((q.shape[0], q.shape[1]), 7.0, device="cuda")
+    got, lse = w8.kv_attention(q, cache, table, lens, out[..., :q.shape[2]], cu_seqlens=cu, max_new=max_new,
+                               plan_=p, return_lse=True)
+    assert (out[..., q.shape[2]:] == 7).all()
+    return got.cpu(), lse.cpu()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("p", [None] + PLANS, ids=name)
+@pytest.mark.parametrize("cu,owners", [
+    ([0, 3, 7], [(0, 0, 3), (1, 3, 7)]),                      # a batch of fixed capacity
+    ([2, 3, 7], [(0, 2, 3), (1, 3, 7)]), ([0, 0, 0], []), ([300, 300, 300], []),
+    ([0, 3, 301], [(0, 0, 3)]),                               # past the token axis
+    ([0, 3, 2], [(0, 0, 3)]), ([-1, 3, 7], [(1, 3, 7)]), ([0, 1 << 30, 5], []), ([0, 290, 300], None)])
+def test_tokens_of_no_sequence_give_zeros(w8, cu, owners, p):
+    rng = np.random.default_rng(6)
+    tokens, hq, hkv, dim, held = 300, 6, 2, 80, [400, 333]
+    cache = ref.Cache(30, hkv, 32, dim, rng)
+    cache.ks[:], cache.vs[:] = rng.integers(120, 125, (2,) + cache.ks.shape)
+    for x in (cache.k, cache.v):
+        x[:] = rng.integers(0, 0x70, x.shape)
+    dev, table, lens = cache.to(w8), i32(rng.permutation(30)[:26].reshape(2, 13).tolist()), i32(held)
+    q = cuda(rng.normal(size=(tokens, hq, dim)), torch.bfloat16)
+    got, lse = attend_into(w8, q, dev, table, lens, i32(cu), p, 290)
+    if owners is None:
+        owners = [(0, 0, 290), (1, 290, 300)]
+    none = torch.ones(tokens, dtype=torch.bool)
+    for b, first, end in owners:
+        want = w8.kv_attention(q[first:end], dev, table[b:b + 1], lens[b:b + 1], return_lse=True,
+                               plan_=p if p is not None else w8.plan_kv_attention(2, 290, 416, hq, hkv, dim))
+        assert torch.equal(got[first:end], want[0].cpu()) and torch.equal(lse[first:end], want[1].cpu())
+        none[first:end] = False
+    assert (got[none] == 0).all() and (lse[none] == -math.inf).all()
