@@ -182,6 +182,15 @@ __device__ __forceinline__ void row_range(const AttnArgs &a, const RowTile &t, u
     lo = a.window && p >= (int32_t)a.window ? p - (int32_t)a.window + 1 : 0;
 }
 
+// (Such a row gives zeros.  One whose visible scores are all -inf sums to
+// zero too, and has no softmax: its 0 / 0 stays.)
+__device__ __forceinline__ bool sees_nothing(const AttnArgs &a, const RowTile &t, uint32_t row)
+{
+    int32_t lo, hi;
+    row_range(a, t, row, lo, hi);
+    return hi <= lo;
+}
+
 // Four outputs of a row, v * 2^n, rounded to its type.
 template <class E> __device__ __forceinline__ void store_row4(E *dst, f32x4_t v, float n)
 {

@@ -443,7 +443,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
     for (int w = 0; w < WAVES; ++w)
         lr += st_row[w].y * exp2_fast(st_row[w].x - mr.sum);
     const uint32_t tok = a.by_group.div(row), hq = head * a.group + row - tok * a.group;
-    const bool none = mr.sum == kUnset && lr == 0.f;     // the row sees nothing
+    const bool none = sees_nothing(a, t, row);
     const float inv = none ? 0.f : 1.0f / lr, unit = mr.out - mr.sum;
     typename Q::elem *const dst = reinterpret_cast<typename Q::elem *>(a.out) +
                                   (int64_t)(t.first + tok) * a.out_token + (int64_t)hq * a.out_head;
@@ -577,7 +577,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
             continue;
         const float mg = red[THREADS + jr], eg = red[THREADS + NR + jr], lg = red[THREADS + 2 * NR + jr];
         const uint32_t jtok = a.by_group.div(t.row0 + jr), jh = head * a.group + t.row0 + jr - jtok * a.group;
-        const bool empty = mg == kUnset && lg == 0.f;
+        const bool empty = sees_nothing(a, t, t.row0 + jr);
         const float inv_all = empty ? 0.f : 1.0f / lg;
         store_row4(reinterpret_cast<typename Q::elem *>(a.out) + (int64_t)(t.first + jtok) * a.out_token +
                        (int64_t)jh * a.out_head + 4 * c4, acc * inv_all, eg - mg);
@@ -671,7 +671,7 @@ __global__ __launch_bounds__(256) void w8a16_kv_join_kernel(AttnArgs a, uint32_t
     if (lane >= per)
         return;
     const uint32_t tok = a.by_group.div(row), hq = head * a.group + row - tok * a.group;
-    const bool none = m == kUnset && l == 0.f;
+    const bool none = sees_nothing(a, t, row);
     const float inv = none ? 0.f : 1.0f / l;
     store_row4(reinterpret_cast<E *>(a.out) + (int64_t)(t.first + tok) * a.out_token +
                    (int64_t)hq * a.out_head + d, acc * inv, ex - m);

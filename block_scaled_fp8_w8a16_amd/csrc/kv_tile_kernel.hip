@@ -492,7 +492,7 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
     typedef const __attribute__((address_space(4))) AttnArgs *args_ptr;
     args_ptr late = (args_ptr)__builtin_amdgcn_kernarg_segment_ptr();
     asm volatile("" : "+s"(late));
-    const bool none = m.sum == kUnset && l == 0.f;
+    const bool none = rhi <= rlo;
     if (alone) {
         const float inv = none ? 0.f : 1.0f / l;
         const float unit = m.out - m.sum;

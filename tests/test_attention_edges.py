@@ -215,3 +215,28 @@ def test_tokens_of_no_sequence_give_zeros(w8, cu, owners, p):
         assert torch.equal(got[first:end], want[0].cpu()) and torch.equal(lse[first:end], want[1].cpu())
         none[first:end] = False
     assert (got[none] == 0).all() and (lse[none] == -math.inf).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("p", [None] + PLANS, ids=name)
+def test_scores_of_minus_infinity_are_not_hidden_keys(w8, p):
+    """A row all of whose visible keys score -inf has no softmax: NaN, and a
+    log-sum of -inf, unlike a row that sees nothing; beside finite scores
+    they weigh nothing."""
+    cache, table = flat_cache(np.random.default_rng(7), 300, 16, 32)
+    cache.k[:] = 0x38
+    cache.k[0, 0, 0] = 0
+    q = torch.zeros(3, 1, 32, dtype=torch.bfloat16, device="cuda")
+    q[:, 0, 0] = -math.inf
+    dev = cache.to(w8)
+    cache.k[0, 0, 0] = 0x38
+    other = cache.to(w8)
+    bt = i32([list(map(int, table))] * 3)
+    for c in (dev, other):
+        out, lse = w8.kv_attention(q, c, bt, i32([300, 1, 0]), return_lse=True, plan_=p)
+        out, lse = out.cpu(), lse.cpu()
+        if c is other:
+            assert out[:2].isnan().all() and (lse[:2] == -math.inf).all()
+        else:       # -inf times a key of zero
+            assert out[:2].isnan().all() and lse[:2].isnan().all()
+        assert (out[2] == 0).all() and lse[2] == -math.inf
