@@ -207,7 +207,7 @@ int get_workspace(int dev, hipStream_t stream, const w8a16_plan_t &plan, Workspa
         if (cs != hipStreamCaptureStatusNone) {
             char buf[256];
             snprintf(buf, sizeof buf,
-                     "w8a16_gemm: this plan needs %llu bytes of split-K workspace and %u "
+                     "w8a16_gemm: this plan needs %llu bytes of workspace and %u "
                      "counters on a stream being captured, which has %llu and %u; make one "
                      "call with this plan (or a larger one) on the stream before capturing",
                      (unsigned long long)plan.workspace_bytes, plan.counter_count,

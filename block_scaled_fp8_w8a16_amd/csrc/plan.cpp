@@ -766,7 +766,7 @@ const char *status_string(int status)
     case W8A16_ERR_NULL_PTR: return "null pointer argument";
     case W8A16_ERR_BAD_PLAN: return "plan does not fit the problem";
     case W8A16_ERR_HIP: return "HIP runtime error";
-    case W8A16_ERR_WORKSPACE: return "split-K workspace unavailable (growth during capture, "
+    case W8A16_ERR_WORKSPACE: return "workspace unavailable (growth during capture, "
                                      "or beyond the no-alloc scratch)";
     case W8A16_ERR_ENV: return "W8A16_LOG or W8A16_DEBUG_SYNC is set to a value other than 0 or 1";
     case W8A16_ERR_SHAPE: return "size, type, stride or alignment the operator does not take";

@@ -64,7 +64,7 @@ typedef enum w8a16_status {
     W8A16_ERR_NULL_PTR = 6,          /* a, w_fp8, block_scale or c is null */
     W8A16_ERR_BAD_PLAN = 7,          /* a plan that does not fit the problem */
     W8A16_ERR_HIP = 8,               /* allocation or launch failed in HIP */
-    W8A16_ERR_WORKSPACE = 9,         /* the plan's split-K workspace cannot be provided:
+    W8A16_ERR_WORKSPACE = 9,         /* the plan's workspace cannot be provided:
                                         it would have to grow during stream capture,
                                         or it exceeds w8a16_gemm_noalloc's scratch */
     W8A16_ERR_ENV = 10,              /* a diagnostic environment variable holds a value

@@ -240,3 +240,26 @@ def test_scores_of_minus_infinity_are_not_hidden_keys(w8, p):
         else:       # -inf times a key of zero
             assert out[:2].isnan().all() and lse[:2].isnan().all()
         assert (out[2] == 0).all() and lse[2] == -math.inf
+
+
+@pytest.mark.gpu
+def test_workspace_refusal_during_capture_names_the_attention(w8):
+    cache = ref.Cache(64, 1, 64, 64, None).to(w8)
+    # (more chunks than any other test asks for: 142 MB)
+    q = torch.ones(512, 4, 64, dtype=torch.bfloat16, device="cuda")
+    table, lens = i32([list(range(64))] * 512), i32([4096] * 512)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        out = torch.empty_like(q)
+        x = torch.zeros(8, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            x += 1
+            with pytest.raises(w8.W8A16Error) as e:
+                w8.kv_attention(q, cache, table, lens, out, plan_=plan(ROWS, 1))
+        g.replay()
+        side.synchronize()
+    assert e.value.status == w8.ERR_WORKSPACE and (x == 1).all()
+    assert "w8a16_kv_attention: this plan needs" in str(e.value) and "split-K" not in str(e.value)
+    assert "split-K" not in w8.status_string(w8.ERR_WORKSPACE)
