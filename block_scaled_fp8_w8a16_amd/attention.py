@@ -9,7 +9,8 @@ decoder layer between its Q/K/V and output projections.
 Marshalling only, as in the rest of the package: shapes, types and devices
 are checked here, everything else by the C entry points (include/w8a16.h,
 which defines the operators and the cache's layout).  Calls run on the
-current (or given) torch stream and do not synchronise.
+current (or given) torch stream, take the memory of their outputs there, and
+do not synchronise.
 """
 
 from __future__ import annotations
@@ -204,9 +205,20 @@ def _rows(name, t, tokens, heads, dim, dtype):
     return st, sh
 
 
-def _like(torch, t):
+def _new(torch, stream, make, *args, **kw):
+    """make(...): an output's memory, of the stream that will write it (the
+    current stream's might still be written by work that is to come there)."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
+def _like(torch, t, stream):
     """A new contiguous tensor of t's shape and type."""
-    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+    if t.is_contiguous():
+        return _new(torch, stream, torch.empty_like, t)
+    return _new(torch, stream, t.new_empty, t.shape)
 
 
 def rope_table(positions: int, rot_dim: int, *, base: float = 10000.0, scaling: Optional[str] = None,
@@ -220,7 +232,7 @@ def rope_table(positions: int, rot_dim: int, *, base: float = 10000.0, scaling: 
         raise ValueError("scaling must be None, 'linear', 'base' or 'bands'")
     shape = (positions, rot_dim // 2, 2)
     if out is None:
-        out = torch.empty(shape, dtype=torch.float32, device=device)
+        out = _new(torch, stream, torch.empty, shape, dtype=torch.float32, device=device)
     if out.dtype != torch.float32 or out.shape != shape or not out.is_contiguous() or not out.is_cuda:
         raise ValueError("out must be a contiguous float32 GPU tensor [positions, rot_dim/2, 2]")
     cfg = RopeConfig(base, factor, original, low_turns, high_turns, magnitude, ROPE_SCALINGS[scaling])
@@ -249,7 +261,7 @@ def rope(x, table, positions, out=None, *, layout: str = "half", inverse: bool =
     tokens, heads, dim = x.shape
     xt, xh = _rows("x", x, tokens, heads, dim, dtype)
     if out is None:
-        out = _like(torch, x)
+        out = _like(torch, x, stream)
         yt, yh = heads * dim, dim
     else:
         yt, yh = _rows("out", out, tokens, heads, dim, dtype)
@@ -297,7 +309,7 @@ def kv_append(cache, k, v, block_table, kv_lens, *, cu_seqlens=None, max_new: Op
         hq = q.shape[1] if q.dim() == 3 else 0
         qt, qh = _rows("q", q, tokens, hq, dim, dtype)
         if q_out is None:
-            q_out = _like(torch, q)
+            q_out = _like(torch, q, stream)
             ot, oh = hq * dim, dim
         else:
             ot, oh = _rows("q_out", q_out, tokens, hq, dim, dtype)
@@ -333,13 +345,13 @@ def kv_attention(q, cache, block_table, kv_lens, out=None, *, cu_seqlens=None,
     tokens, heads, _ = q.shape
     qt, qh = _rows("q", q, tokens, heads, dim, dtype)
     if out is None:
-        out = _like(torch, q)
+        out = _like(torch, q, stream)
         ot, oh = heads * dim, dim
     else:
         ot, oh = _rows("out", out, tokens, heads, dim, dtype)
     lse, lp = None, 0
     if return_lse:
-        lse = q.new_empty((tokens, heads), dtype=torch.float32)
+        lse = _new(torch, stream, q.new_empty, (tokens, heads), dtype=torch.float32)
         lp = lse.data_ptr()
     if window < 0:
         raise ValueError("window must not be negative")

@@ -263,3 +263,39 @@ def test_workspace_refusal_during_capture_names_the_attention(w8):
     assert e.value.status == w8.ERR_WORKSPACE and (x == 1).all()
     assert "w8a16_kv_attention: this plan needs" in str(e.value) and "split-K" not in str(e.value)
     assert "split-K" not in w8.status_string(w8.ERR_WORKSPACE)
+
+
+@pytest.mark.gpu
+def test_outputs_belong_to_the_given_stream(w8):
+    """A call on a given stream makes its outputs there: not from memory that
+    work of the current stream, still to run, will write."""
+    cache = w8.kv_cache(64, 2, 64, 64)
+    side, main = torch.cuda.Stream(), torch.cuda.current_stream()
+    table, lens = i32([list(range(64))]), i32([4096])
+    x = torch.randn(4096, 2, 64, device="cuda").bfloat16()
+    q = torch.randn(4096, 4, 64, device="cuda").bfloat16()[:, :, ::1]
+    pos, rt = torch.arange(4096, dtype=torch.int32, device="cuda"), w8.rope_table(4096, 64)
+    w8.kv_append(cache, x, x, table, lens, table=rt)
+    torch.cuda.synchronize()
+    calls = [lambda s: [w8.rope(q, rt, pos, stream=s)],
+             lambda s: [w8.kv_append(cache, x, x, table, lens, table=rt, q=q, stream=s)],
+             lambda s: list(w8.kv_attention(q, cache, table, lens, return_lse=True, stream=s)),
+             lambda s: [w8.rope_table(2048, 512, stream=s)]]
+    for call in calls:
+        want = call(None)
+        torch.cuda.synchronize()
+        got = call(side)
+        torch.cuda.synchronize()
+        del got
+        # memory of the outputs' sizes, freed while the current stream has
+        # still to write it
+        held = [torch.empty_like(w) for w in want]
+        torch.cuda._sleep(200_000_000)
+        for h in held:
+            h.fill_(3.0)
+        del h, held
+        got = call(side)
+        side.synchronize()
+        assert not main.query()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
