@@ -92,12 +92,13 @@ def declare(lib) -> None:
 
 
 _state = None
+_codes = _scale_bytes = ()     # torch types of a cache's codes and scale bytes
 
 
 def _setup():
     """(library, torch, dtype codes, raise function, raw stream of a device
     index), resolved once."""
-    global _state
+    global _state, _codes, _scale_bytes
     if _state is None:
         import torch
 
@@ -106,13 +107,16 @@ def _setup():
         # magnitude faster (0.06 against 1.8 us of a call's 8)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _codes = (torch.uint8, torch.float8_e4m3fn)
+        _scale_bytes = (torch.uint8, torch.float8_e8m0fnu)
         _state = (library(), torch,
                   {torch.bfloat16: 1, torch.float16: 2, torch.float32: 3}, _raise_if, raw)
     return _state
 
 
 class KVCache(NamedTuple):
-    """Codes and scale bytes of a paged FP8 cache (uint8 or float8 tensors):
+    """Codes (uint8 or float8_e4m3fn) and scale bytes (uint8 or
+    float8_e8m0fnu) of a paged FP8 cache:
     k [pages, kv_heads, page_size, head_dim], v [pages, kv_heads,
     page_size / 16, head_dim, 16], k_scale and v_scale [pages, kv_heads,
     page_size / 16].  Only the page axis may be strided."""
@@ -155,8 +159,9 @@ def _cache_desc(cache) -> KVCacheDesc:
             vs.shape != ks.shape:
         raise ValueError("cache must be k [pages, heads, page, dim], v [pages, heads, page/16, dim, "
                          "16] and scales [pages, heads, page/16]")
-    if k.element_size() + v.element_size() + ks.element_size() + vs.element_size() != 4:
-        raise ValueError("cache tensors must be uint8 or float8")
+    if k.dtype not in _codes or v.dtype not in _codes or ks.dtype not in _scale_bytes or \
+            vs.dtype not in _scale_bytes:
+        raise ValueError("cache codes must be uint8 or float8_e4m3fn, its scales uint8 or float8_e8m0fnu")
     if not (k.is_cuda and v.is_cuda and ks.is_cuda and vs.is_cuda):
         raise ValueError("cache must be GPU tensors")
     codes, bytes_ = heads * page * dim, heads * blocks

@@ -299,3 +299,15 @@ def test_outputs_belong_to_the_given_stream(w8):
         assert not main.query()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("at,dtype", [(0, "float8_e5m2"), (1, "float8_e4m3fnuz"), (0, "int8"), (1, "bool"),
+                                      (2, "float8_e4m3fn"), (3, "int8"), (0, "float8_e8m0fnu")])
+def test_cache_types_are_checked(at, dtype):
+    cache = list(w8mod.kv_cache(2, 1, 32, 16, device="cpu"))
+    cache[at] = cache[at].view(getattr(torch, dtype))
+    one, i = torch.zeros(1, 1, 16), torch.zeros(1, 1, dtype=torch.int32)
+    for call in (lambda: w8mod.kv_append(cache, one, one, i, i[0]),
+                 lambda: w8mod.kv_attention(one.bfloat16(), cache, i, i[0])):
+        with pytest.raises(ValueError, match="float8_e4m3fn"):
+            call()
