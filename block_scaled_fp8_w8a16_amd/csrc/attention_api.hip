@@ -81,6 +81,19 @@ uint32_t rope_heads_per_thread(uint64_t items)
     return items >= 512ull * kDefaultCUs * kRopeHeads ? kRopeHeads : 1;
 }
 
+// Whether rows of dim elements that a call writes, `token` and `head` apart,
+// lie on top of each other.
+int check_apart(const char *entry, const char *name, int64_t token, int64_t head, uint32_t tokens,
+                uint32_t heads, uint32_t dim)
+{
+    const uint64_t t = token < 0 ? 0 - (uint64_t)token : (uint64_t)token;
+    const uint64_t h = head < 0 ? 0 - (uint64_t)head : (uint64_t)head;
+    if ((tokens > 1 && t < dim) || (heads > 1 && h < dim) || (tokens > 1 && heads > 1 && t == h))
+        return refuse(W8A16_ERR_SHAPE, "%s: %s rows of %u elements overlap (strides %lld by token, %lld by "
+                      "head)", entry, name, dim, (long long)token, (long long)head);
+    return W8A16_OK;
+}
+
 // A rotation's shape: dtype, layout, an even part of the head.
 int check_rope(const char *entry, uint32_t dtype, uint32_t head_dim, uint32_t rot, uint32_t layout)
 {
@@ -233,6 +246,9 @@ int rope(const void *x, const int64_t strides[4], void *y, uint32_t dtype, uint3
         return refuse(W8A16_ERR_SHAPE, "%s: heads must be at least 1", entry);
     if (tokens == 0)
         return W8A16_OK;
+    st = check_apart(entry, "y", strides[2], strides[3], tokens, heads, head_dim);
+    if (st != W8A16_OK)
+        return st;
     RopeArgs a;
     std::memset(static_cast<void *>(&a), 0, sizeof a);
     fill_rope(a.r, x, y, strides, table, table_positions, rot, head_dim, layout, heads, dtype);
@@ -333,6 +349,12 @@ int kv_append(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
     if (units >= (1ull << 31) || groups * 256ull > kMaxThreads)
         return refuse(W8A16_ERR_SHAPE, "%s: %u tokens of %u sequences (max_new=%u) are too many for one "
                       "call", entry, seqs->tokens, seqs->seqs, seqs->max_new);
+    if (g->q) {
+        st = check_apart(entry, "q_out", g->q_out_token_stride, g->q_out_head_stride, seqs->tokens,
+                         g->q_heads, cache->head_dim);
+        if (st != W8A16_OK)
+            return st;
+    }
     hipError_t e = launch_kv_append(a, g->dtype, stream);
     if (e != hipSuccess)
         return named(hip_fail(e, "kernel launch"), entry);
@@ -373,6 +395,10 @@ int kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
                       (double)g->scale);
     if (seqs->tokens == 0)
         return W8A16_OK;
+    st = check_apart(entry, "out", g->out_token_stride, g->out_head_stride, seqs->tokens, g->q_heads,
+                     cache->head_dim);
+    if (st != W8A16_OK)
+        return st;
     const uint32_t group = g->q_heads / cache->kv_heads;
     if ((uint64_t)seqs->max_new * group >= (1ull << 31))
         return refuse(W8A16_ERR_SHAPE, "%s: max_new=%u rows of %u query heads per KV head are too many",

@@ -370,7 +370,8 @@ int w8a16_gemm_w4a4_planned(const void *a, uint32_t a_row_stride, const uint8_t 
  * W8A16_ERR_NULL_PTR, then W8A16_ERR_SHAPE; nothing is enqueued on an error.
  * A call with no tokens enqueues nothing and succeeds.  Strides of
  * activations are in elements, the last axis is contiguous, and rows need
- * only the alignment of their type (16-byte rows run fastest). */
+ * only the alignment of their type (16-byte rows run fastest).  Rows of an
+ * output must not overlap; strides shorter than a row are refused. */
 
 typedef enum w8a16_dtype { W8A16_BF16 = 1, W8A16_FP16 = 2, W8A16_FP32 = 3 } w8a16_dtype;
 

@@ -311,3 +311,14 @@ def test_cache_types_are_checked(at, dtype):
                  lambda: w8mod.kv_attention(one.bfloat16(), cache, i, i[0])):
         with pytest.raises(ValueError, match="float8_e4m3fn"):
             call()
+
+
+@pytest.mark.parametrize("strides", [(0, 64), (256, 0), (63, 1000), (256, -63), (-1, 64)])
+def test_outputs_that_overlap_themselves_are_refused(strides):
+    lib = w8mod.library()
+    c, s, ap, at = _descs(at__out_token_stride=strides[0], at__out_head_stride=strides[1],
+                          ap__q_out_token_stride=strides[0], ap__q_out_head_stride=strides[1])
+    assert lib.w8a16_kv_attention(c, s, at, 0) == w8mod.ERR_SHAPE and "overlap" in w8mod.last_error()
+    assert lib.w8a16_kv_append(c, s, ap, 0) == w8mod.ERR_SHAPE and "overlap" in w8mod.last_error()
+    assert lib.w8a16_rope(16, 256, 64, 16, strides[0], strides[1], 1, 4, 4, 64, 16, 8, 64, 16, 0, 0,
+                          0) == w8mod.ERR_SHAPE and "overlap" in w8mod.last_error()
