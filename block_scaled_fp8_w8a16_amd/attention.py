@@ -16,6 +16,7 @@ do not synchronise.
 from __future__ import annotations
 
 import ctypes
+from contextlib import nullcontext
 from typing import NamedTuple, Optional
 
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
@@ -210,20 +211,19 @@ def _rows(name, t, tokens, heads, dim, dtype):
     return st, sh
 
 
-def _new(torch, stream, make, *args, **kw):
-    """make(...): an output's memory, of the stream that will write it (the
-    current stream's might still be written by work that is to come there)."""
-    if stream is None:
-        return make(*args, **kw)
-    with torch.cuda.stream(stream):
-        return make(*args, **kw)
+def _on(torch, stream):
+    """Where a call makes its outputs: on the stream that will write them (the
+    current stream's memory might still be written by work that is to come
+    there)."""
+    return nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _like(torch, t, stream):
     """A new contiguous tensor of t's shape and type."""
-    if t.is_contiguous():
-        return _new(torch, stream, torch.empty_like, t)
-    return _new(torch, stream, t.new_empty, t.shape)
+    if stream is not None:
+        with _on(torch, stream):
+            return _like(torch, t, None)
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def rope_table(positions: int, rot_dim: int, *, base: float = 10000.0, scaling: Optional[str] = None,
@@ -237,7 +237,8 @@ def rope_table(positions: int, rot_dim: int, *, base: float = 10000.0, scaling: 
         raise ValueError("scaling must be None, 'linear', 'base' or 'bands'")
     shape = (positions, rot_dim // 2, 2)
     if out is None:
-        out = _new(torch, stream, torch.empty, shape, dtype=torch.float32, device=device)
+        with _on(torch, stream):
+            out = torch.empty(shape, dtype=torch.float32, device=device)
     if out.dtype != torch.float32 or out.shape != shape or not out.is_contiguous() or not out.is_cuda:
         raise ValueError("out must be a contiguous float32 GPU tensor [positions, rot_dim/2, 2]")
     cfg = RopeConfig(base, factor, original, low_turns, high_turns, magnitude, ROPE_SCALINGS[scaling])
@@ -356,7 +357,8 @@ def kv_attention(q, cache, block_table, kv_lens, out=None, *, cu_seqlens=None,
         ot, oh = _rows("out", out, tokens, heads, dim, dtype)
     lse, lp = None, 0
     if return_lse:
-        lse = _new(torch, stream, q.new_empty, (tokens, heads), dtype=torch.float32)
+        with _on(torch, stream):
+            lse = q.new_empty((tokens, heads), dtype=torch.float32)
         lp = lse.data_ptr()
     if window < 0:
         raise ValueError("window must not be negative")
