@@ -148,13 +148,11 @@ __device__ __forceinline__ bool seq_extent(const KvSeqs &s, uint32_t b, RowTile 
     if (s.cu) {
         t.first = (uint32_t)s.cu[b];
         end = (uint32_t)s.cu[b + 1];
-        if (t.first > s.tokens || end > s.tokens || end < t.first)
-            return false;
     }
     t.count = end - t.first;
     t.kv_len = s.kv_lens[b];
     t.base = t.kv_len - (int32_t)t.count;
-    return true;
+    return t.first <= s.tokens && end <= s.tokens && end >= t.first;
 }
 
 __device__ __forceinline__ void tile_range(const AttnArgs &a, uint32_t tile_rows, RowTile &t)
