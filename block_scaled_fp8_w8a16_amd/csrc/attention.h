@@ -10,8 +10,10 @@
 
 namespace w8a16 {
 
-// Division of n < 2^31 by a constant d >= 1: with s = ceil(log2 d) and
-// mul = ceil(2^(31 + s) / d), n * mul >> (31 + s) is floor(n / d).
+// Division of n < 2^31 by a constant d >= 1 by a multiplication and a shift
+// (Granlund and Montgomery, "Division by invariant integers using
+// multiplication", 1994): with s = ceil(log2 d) and mul = ceil(2^(31 + s) / d),
+// n * mul >> (31 + s) is floor(n / d).
 struct FastDiv {
     uint32_t d = 1, mul = 1u << 31, shift = 31;
     FastDiv() = default;

@@ -24,15 +24,15 @@
 // Nothing passes through LDS before the waves' results are joined.
 //
 // What bounds it: reading the cache.  64 sequences of up to 8192 tokens (8 KV
-// heads of 128 channels, 673 MB) take 137 us, 4.9 TB/s; one of 131072 tokens, cut
-// into 32 chunks per head, 59 us, 4.6 TB/s, where a large copy moves 4.9.
+// heads of 128 channels, 673 MB) take 136 us, 4.9 TB/s; one of 131072 tokens, cut
+// into 32 chunks per head, 58 us, 4.6 TB/s, where a large copy moves 4.9.
 // Each wave has one 64-key tile of loads in flight (16 KB) while it computes
 // another, 4 waves to a workgroup and two workgroups to a CU up to 128
 // channels; 8 waves where there are few row tiles (figures in kv_plan.cpp).
 // (Refilling two sets of tile registers as they are consumed, so that loads
 // stay in flight longer, gained nothing at 64 channels and spilled at 128.)
 // Short caches are bound by the chain of loads (length, page, block): 300
-// tokens take 8.7 us, 24 windows of about 1000 keys with 25 rows each 13.1,
+// tokens take 7.9 us, 24 windows of about 1000 keys with 25 rows each 12.7,
 // twice what their bytes and about what their widening and exponentials
 // take on a half-filled chip.
 //

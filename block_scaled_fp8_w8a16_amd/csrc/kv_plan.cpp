@@ -80,14 +80,15 @@ int make_kv_plan(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_he
     // the tile kernel takes as long for 33 rows as for 128, which pays where
     // the row tiles would wait for CUs.  8 KV heads of 128 channels, row
     // kernel and tile kernel, us:
-    //   32 rows  64 sequences of 1000 tokens (1024 row tiles)  48  54
-    //   48 rows  64 of 1000 (1536) 64  56;  32 of 2000 (768)  62  74
-    //   64 rows  64 of 1000 (2048) 83  55;  32 of 2000 (1024) 79  73
-    //            16 of 1000 (512)  21  36;  1 of 500 (32)      9  19
-    //  128 rows  16 of 1000 (1024) 35  37;  8 of 4000 (512)   51  51
-    // so up to 128 rows where there are at most 4 row tiles per CU.  Of 256
-    // channels a CU holds one workgroup: 32 rows of one sequence of 16000
-    // 36 and 41, 48 rows 44 and 43, 64 rows 49 and 44.
+    //   32 rows  64 sequences of 1000 tokens (1024 row tiles)  46  55
+    //   48 rows  64 of 1000 (1536) 65  54;  32 of 2000 (768)  62  59
+    //   64 rows  64 of 1000 (2048) 85  52;  32 of 2000 (1024) 81  58
+    //            16 of 1000 (512)  19  32;  1 of 500 (32)      9  19
+    //  128 rows  16 of 1000 (1024) 32  34;  8 of 4000 (512)   49  42
+    // so up to 128 rows where there are at most 4 row tiles per CU (at that
+    // end short caches gain by it and long ones lose).  Of 256 channels a CU
+    // holds one workgroup: 32 rows of one sequence of 16000 34 and 39, 48
+    // rows 40 and 40, 64 rows 44 and 41.
     const bool narrow = head_dim <= 128;
     const uint64_t row_grid = (uint64_t)seqs * kv_heads * div_up(rows, 16);
     p.kernel = rows <= 32 || (narrow && rows <= 128 && row_grid <= 4 * cus) ? W8A16_KV_ROWS : W8A16_KV_TILE;
@@ -104,22 +105,21 @@ int make_kv_plan(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_he
     // Cut the keys while that leaves no more workgroups than run at once: two
     // per CU, one of 8 waves or of heads above 128 channels.  Eight waves
     // where the row tiles alone do not give every CU a workgroup: half as
-    // many chunks to join (32 sequences of 2000 tokens 29 us against 31 with
-    // four waves, 4 new tokens over 16000 20 against 23), but slower where
-    // more workgroups wait (48 sequences 51 against 46, 256 of 500 79 against
-    // 53).
+    // many chunks to join (4 new tokens over 16000 20 us against 22 with four
+    // waves, 32 sequences of 2000 29 either way), but slower where more
+    // workgroups wait (48 sequences 49 against 43, 256 of 500 79 against 55).
     //
     // A cut has to spare more tiles of a workgroup's time than the join
-    // costs.  Row kernel, us: 4 sequences of 768 tokens 9.3 uncut, 10.7 cut;
-    // one of 900 11.8 and 10.8, of 1500 15.6 and 11.0; 16 sequences, which
-    // can be cut in two, of 1200 15.1 and 16.2, of 2000 20.6 and 20.0.  Tile
+    // costs.  Row kernel, us: 4 sequences of 768 tokens 9.7 uncut, 11.0 cut;
+    // one of 900 11.2 and 10.9, of 1500 14.1 and 10.9; 16 sequences, which
+    // can be cut in two, of 1200 14.1 and 15.8, of 2000 19.8 and 19.5.  Tile
     // kernel, whose partial rows grow with the workgroups: 128 new tokens
-    // over 1500 45 and 29 (96 workgroups); 2 x 256 over 1024 32 and 37, over
-    // 2048 60 and 44, 4 x 256 over 2048 of 64 channels 47 and 55, 2 x 512
-    // over 4096 115 and 95 (512 workgroups).
-    // A chunk has at least 4 tiles (2000 tokens: 8 tiles 12.2 us, 4 11.1; of
-    // 256 channels 17.5 and 13.1; 64 new tokens 27 and 24), or 8 where it
-    // would be a CU's second (128 new tokens over 4096: 34 and 37).
+    // over 1500 45 and 27 (96 workgroups); 2 x 256 over 1024 32 and 39, over
+    // 2048 56 and 45, 4 x 256 over 2048 of 64 channels 45 and 58, 2 x 512
+    // over 4096 104 and 102 (512 workgroups).
+    // A chunk has at least 4 tiles (2000 tokens: 8 tiles 11.9 us, 4 10.8; of
+    // 256 channels 16.1 and 12.7; 64 new tokens 27 and 24), or 8 where it
+    // would be a CU's second (128 new tokens over 4096: 34 and 36).
     if (p.kernel == W8A16_KV_ROWS && narrow && p.grid <= cus)
         p.waves = 8;
     const uint64_t slots = narrow && p.waves == 4 ? 2 * cus : cus;

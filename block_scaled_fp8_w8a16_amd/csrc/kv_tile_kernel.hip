@@ -3,16 +3,15 @@
 // The mathematics is that of the row kernel (kv_attention.hip): S^T = K Q^T,
 // l += 2^(x - m), O^T += V^T p^T, p = 2^(x + e - M + 11) in FP16, V as its
 // codes.
-// The issue of vector instructions bounds the time: a wave needs about 320
-// of them (128 conversions of codes, 32 exponentials, the rest sums, maxima
-// and conversions of p) beside the 32 matrix instructions of 64 keys and 128
-// channels.  So a workgroup takes 128 rows, its four waves 32 each with
-// 32x32x16 matrix instructions, two workgroups share a CU where registers
-// allow (up to 128 channels), and:
+// A wave needs about 320 vector instructions (128 conversions of codes, 34
+// exponentials, the rest sums, maxima and conversions of p) beside the 32
+// matrix instructions of 64 keys and 128 channels.  So a workgroup takes 128
+// rows, its four waves 32 each with 32x32x16 matrix instructions, two
+// workgroups share a CU where registers allow (up to 128 channels), and:
 //   * 64 keys at a time, K and V as codes (half of what 16-bit operands
-//     would read from LDS), brought to LDS by DMA three tiles ahead: four
-//     buffers, one barrier per tile.  Each wave brings one block of 16 keys;
-//     page lookups are scalar.
+//     would read from LDS), brought to LDS by DMA into the third buffer of
+//     four from the one in use, one barrier per tile.  Each wave brings one
+//     block of 16 keys; page lookups are scalar.
 //   * Row 8a + 4h + b of the K operand holds key 16h + 4a + b, so a lane
 //     ends up with the 16 scores of one block in order, and its p are the
 //     second product's operand as they stand, whose other side is one
@@ -24,14 +23,19 @@
 //     fall out of step and one's exponentials run under another's matrix
 //     instructions; the second product follows each half's exponentials at
 //     once.
+// What bounds it: the issue of vector instructions (64 % of the time), and at
+// the end of every tile a wait for all loads in flight (see turn() below), so
+// that a tile costs at least its loads' latency: one workgroup alone on a CU
+// takes 1.5 us per tile, two between them 2.3.
 // Measured, 2 x 2048 tokens of 32 query and 8 KV heads over 8192 keys of 128
-// channels: 488 to 508 us by run and card, 947 to 986 TFLOP/s (a plain FP16
-// matrix product of 8192^3 reaches 1151 here).  Before the priority 512, with two buffers and one
-// loop for all tiles 530.  Slower: widening once per workgroup into LDS as
-// 16-bit operands 584, the next tile's scores under this one's exponentials
-// 602, the raised priority for the second product as well 503 or for the
-// exponentials 516.  FP8 products of queries split in two E4M3 numbers took
-// 508 and summed too coarsely (errors of 2e-3 in a row's log-sum).
+// channels: 495 to 530 us by run and card, 908 to 972 TFLOP/s (a plain FP16
+// matrix product of 8192^3 reaches 1151 here).  Tried on forms of this kernel
+// that took 488 to 508: two buffers and one loop for all tiles 530, no
+// priority 512, widening once per workgroup into LDS as 16-bit operands 584,
+// the next tile's scores under this one's exponentials 602, the raised
+// priority for the second product as well 503 or for the exponentials 516.
+// FP8 products of queries split in two E4M3 numbers took 508 and summed too
+// coarsely (errors of 2e-3 in a row's log-sum).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -450,7 +454,10 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
             next = locate(tile0 + tile + kBuffers);
         };
         // The next tile has arrived when no more loads are open than the two
-        // tiles after it take: K and V pieces and two scale bytes each.
+        // tiles after it take: K and V pieces and two scale bytes each.  The
+        // buffers need no more than that; but the scale bytes carried to the
+        // next turn are widened at its start, and the compiler waits for
+        // them there, hence for every load.
         auto turn = [&]() {
             put((buf + 2u) & 3u, was, was_ok);
             wait_vm<2 * (2 * (DP / 64) + 2)>();

@@ -166,11 +166,11 @@ int plan_finalize(uint32_t m, uint32_t n, uint32_t k, w8a16_plan_t *p);
 int make_plan_w8a8(uint32_t m, uint32_t n, uint32_t k, uint32_t cu_count, w8a16_plan_t *out);
 int plan_batched(const w8a16_gemm_desc_t *descs, uint32_t count, uint32_t cu_count,
                  w8a16_plan_t *out);
+// Threads of one launch (a grid's size is held in 32 bits).
+constexpr uint64_t kMaxThreads = (1ull << 32) - 1;
 // Cache attention (kv_plan.cpp).  The row kernel joins a row tile's chunks in
 // the last workgroup to arrive, which holds a factor per chunk and row in
 // LDS; arrival counters sit 64 bytes apart.
-// Threads of one launch (a grid's size is held in 32 bits).
-constexpr uint64_t kMaxThreads = (1ull << 32) - 1;
 constexpr uint32_t kKvMaxChunks = 128;
 constexpr uint32_t kKvCounterStride = 16;
 int kv_plan_finalize(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_heads,
