@@ -531,12 +531,12 @@ typedef struct w8a16_kv_attention_args {
     uint32_t q_heads, dtype, causal, window, max_kv;
 } w8a16_kv_attention_args_t;
 
-/* Sums and softmax statistics are FP32; in the sum of the values a weight is
- * rounded to 11 bits, fewer below 2^-24 of the row's largest and none from
- * 2^-35 on.  Every order of addition is fixed by the plan, so a plan gives
- * the same bits on every run.  A plan with
- * chunks uses the (device, stream) workspace under the rules at the top of
- * this file (growth is refused during capture). */
+/* Sums and softmax statistics are FP32.  In the sum of the values a weight,
+ * times its block's V scale, is rounded to 11 bits, fewer below 2^-24 of the
+ * row's largest such product and none from 2^-35 on.  Every order of addition
+ * is fixed by the plan, so a plan gives the same bits on every run.  A plan
+ * with chunks uses the (device, stream) workspace under the rules at the top
+ * of this file (growth is refused during capture). */
 int w8a16_kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
                        const w8a16_kv_attention_args_t *args, void *stream);
 
