@@ -45,7 +45,7 @@ __device__ __forceinline__ bool token_place(const KvSeqs &s, uint32_t t, uint32_
         b = lo;
         first = (uint32_t)s.cu[b];
         end = (uint32_t)s.cu[b + 1];
-        if (t < first || t >= end)
+        if (t < first || t >= end || end > s.tokens)
             return false;
     } else {
         b = s.by_uniform.div(t);

@@ -450,7 +450,8 @@ typedef struct w8a16_kv_cache {
  * null: tokens / seqs each), n_b of them, and holds kv_lens[b] tokens in all,
  * the new ones among them: its new token j has position kv_lens[b] - n_b + j.
  * A token whose position is negative belongs to no sequence (an empty slot
- * of a padded batch).  Its tokens i * page_size onwards are on page
+ * of a padded batch), nor does one outside all of these ranges, or in a range
+ * that decreases or ends past the token axis.  Its tokens i * page_size onwards are on page
  * block_table[b * block_table_stride + i], i < block_table_width.
  * max_new: at least the largest n_b.  All arrays int32. */
 typedef struct w8a16_kv_seqs {
@@ -514,9 +515,8 @@ typedef struct w8a16_kv_plan {
  *   out = sum_j softmax_j(scale * q . k_j) v_j,  lse = ln sum_j exp(scale * q . k_j)
  * over the visible keys j < kv_lens[b]; causal: j <= p; window > 0:
  * j > p - window.  A row that sees nothing gives zeros and lse = -inf, and so
- * does a token that no sequence brings: outside all of cu_seqlens' ranges, or
- * in one that ends past the token axis.  What hidden places hold, NaN
- * included, changes nothing.  q, out: [tokens,
+ * does a token of no sequence.  What hidden places hold, NaN included,
+ * changes nothing.  q, out: [tokens,
  * q_heads, head_dim] of `dtype` (BF16 or FP16); lse: FP32 [tokens, q_heads]
  * contiguous, or null.  max_kv: at least the largest kv_lens (0: the block
  * table's width); it shapes the launch only, longer sequences stay right.

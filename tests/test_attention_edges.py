@@ -218,6 +218,37 @@ def test_tokens_of_no_sequence_give_zeros(w8, cu, owners, p):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("cu,owners", [([0, 3, 9], [(0, 0, 3)]), ([0, 3, 6], [(0, 0, 3), (1, 3, 6)]),
+                                       ([2, 4, 8], [(0, 2, 4), (1, 4, 8)]), ([-1, 3, 6], [(1, 3, 6)]),
+                                       ([0, 0, 0], []), ([9, 9, 9], [])])
+def test_append_of_tokens_of_no_sequence(w8, cu, owners):
+    """What the attention takes for no sequence's token, the append does too:
+    nothing stored, its query zero."""
+    rng = np.random.default_rng(8)
+    cache = ref.Cache(2, 2, 32, 48)
+    cache.ks[:], cache.vs[:] = 120, 120      # tokens held before, of codes that are numbers
+    for c in (cache.k, cache.v):
+        c[:] = rng.integers(0, 0x70, c.shape)
+    dev, held = cache.to(w8), [20, 31]
+    x = rounded(rng.normal(size=(8, 8, 48)), "bf16")
+    rt = ref.table64(40, 48).astype(np.float32)
+    want = np.zeros((8, 4, 48), np.float32)
+    for b, first, end in owners:
+        pos, start = np.arange(held[b] - (end - first), held[b]), held[b] - (end - first)
+        want[first:end] = ref.rotate32(x[first:end, :4], rt, pos, "half")
+        kr = ref.rotate32(x[first:end, 4:6], rt, pos, "half")
+        for h in range(2):
+            cache.append(None, False, h, [b], start, held[b], kr[:, h])
+            cache.append(None, True, h, [b], start, held[b], x[first:end, 6 + h])
+    xd = cuda(x, torch.bfloat16)
+    got = w8.kv_append(dev, xd[:, 4:6], xd[:, 6:], i32([[0], [1]]), i32(held), cu_seqlens=i32(cu),
+                       table=cuda(rt), q=xd[:, :4])
+    assert torch.equal(got.cpu(), torch.from_numpy(want).to(torch.bfloat16))
+    for g, w in zip(dev, (cache.k, cache.v, cache.ks, cache.vs)):
+        assert (g.cpu().numpy() == w).all()
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("p", [None] + PLANS, ids=name)
 def test_scores_of_minus_infinity_are_not_hidden_keys(w8, p):
     """A row all of whose visible keys score -inf has no softmax: NaN, and a
