@@ -259,17 +259,19 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
                     o[x][i] *= f;
         }
     };
-    // Scores of one block to operands of the second product, and to l; hidden:
-    // some may be -inf under a scale of NaN or 0.
-    auto weigh = [&](f32x16_t &s, float c, float e, auto hidden) {
-        const float mu = m.out - e;
-        float shift = m.shift(e);
-        if (fabsf(shift) > kFar) {
-            shift = kNegInf;
+    // A block far from the row's others: its weights by themselves to l, its
+    // operands' sum to nothing.
+    auto far = [&](const f32x16_t &s, float c, float &shift) {
+        shift = kNegInf;
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                l += s[i] == kNegInf ? 0.f : exp2_fast(fmaf(s[i], c, -m.sum));
-        }
+        for (int i = 0; i < 16; ++i)
+            l += s[i] == kNegInf ? 0.f : exp2_fast(fmaf(s[i], c, -m.sum));
+    };
+    // Scores of one block to operands of the second product, and to l, where
+    // their sum counts 2^shift; hidden: some may be -inf under a scale of NaN
+    // or 0.
+    auto weigh = [&](f32x16_t &s, float c, float e, float shift, auto hidden) {
+        const float mu = m.out - e;
         float sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -307,10 +309,20 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
             mx[x] = largest(s[x]) * c[x];
         }
         refer(mx, e);
+        // (one branch for the tile: the masked form's one for each half cost
+        // 2 to 4 % here, 64 channels 345 us and 337, and both forms' one for
+        // the tile spilled at 128 channels)
+        float shift[2] = {m.shift(e[0]), m.shift(e[1])};
+        if (__ballot(fabsf(shift[0]) > kFar || fabsf(shift[1]) > kFar)) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                if (fabsf(shift[x]) > kFar)
+                    far(s[x], c[x], shift[x]);
+        }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             u32x4_t p[2];
-            weigh(s[x], c[x], e[x], std::false_type{});
+            weigh(s[x], c[x], e[x], shift[x], std::false_type{});
             pack(s[x], p);
 #pragma unroll
             for (int d = 0; d < VT; ++d) {
@@ -343,7 +355,10 @@ __device__ __forceinline__ void kv_tile(const AttnArgs &a)
         u32x4_t p[2][2];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            weigh(s[x], c[x], e[x], std::true_type{});
+            float shift = m.shift(e[x]);
+            if (fabsf(shift) > kFar)
+                far(s[x], c[x], shift);
+            weigh(s[x], c[x], e[x], shift, std::true_type{});
             pack(s[x], p[x]);
         }
         // Codes of half x that some row of the wave may see.
