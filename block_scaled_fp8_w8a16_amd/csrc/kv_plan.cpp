@@ -115,8 +115,8 @@ int make_kv_plan(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_he
     // can be cut in two, of 1200 14.1 and 15.8, of 2000 19.8 and 19.5.  Tile
     // kernel, whose partial rows grow with the workgroups: 128 new tokens
     // over 1500 45 and 27 (96 workgroups); 2 x 256 over 1024 32 and 39, over
-    // 2048 56 and 45, 4 x 256 over 2048 of 64 channels 45 and 58, 2 x 512
-    // over 4096 104 and 102 (512 workgroups).
+    // 2048 56 and 42, 4 x 256 over 2048 of 64 channels 42 and 56, 2 x 512
+    // over 4096 102 and 100 (512 workgroups).
     // A chunk has at least 4 tiles (2000 tokens: 8 tiles 11.9 us, 4 10.8; of
     // 256 channels 16.1 and 12.7; 64 new tokens 27 and 24), or 8 where it
     // would be a CU's second (128 new tokens over 4096: 34 and 36).
