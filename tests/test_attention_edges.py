@@ -2,7 +2,6 @@
 below a row's largest, blocks of very unlike scale, blocks hidden from some
 rows, tokens of no sequence, and refusals."""
 
-import ctypes
 import math
 
 import numpy as np
@@ -10,7 +9,7 @@ import pytest
 
 import attention_ref as ref
 import block_scaled_fp8_w8a16_amd as w8mod
-from test_attention import HALF_ULP, DT, _descs, check_attention, cuda, i32, rounded, w8  # noqa: F401
+from test_attention import HALF_ULP, DT, _descs, cuda, i32, rounded, w8  # noqa: F401
 
 torch = pytest.importorskip("torch")
 
