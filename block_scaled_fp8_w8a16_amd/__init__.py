@@ -58,8 +58,8 @@ EXPORTS = ("w8a16_check_args", "w8a16_plan", "w8a16_plan_finalize", "w8a16_gemm"
            "w8a16_gemm_planned", "w8a16_gemm_noalloc", "w8a16_plan_batched", "w8a16_gemm_batched",
            "w8a16_act_quant_fp8", "w8a16_plan_w8a8", "w8a16_gemm_w8a8",
            "w8a16_gemm_w8a8_planned", "w8a16_gemm_w4a4", "w8a16_plan_w4a4",
-           "w8a16_gemm_w4a4_planned", "w8a16_rope_table", "w8a16_rope", "w8a16_kv_append",
-           "w8a16_kv_attention", "w8a16_plan_kv_attention", "w8a16_status_string",
+           "w8a16_gemm_w4a4_planned", "w8a16_rope_table", "w8a16_rope", "w8a16_rope_axes",
+           "w8a16_kv_append", "w8a16_kv_append_axes", "w8a16_kv_attention", "w8a16_plan_kv_attention", "w8a16_status_string",
            "w8a16_last_error")
 
 MAX_BATCH = 8

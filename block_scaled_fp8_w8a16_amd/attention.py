@@ -20,6 +20,8 @@ from contextlib import nullcontext
 from typing import NamedTuple, Optional
 
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_ORDERS = {"split": 0, "turns": 1, "own": 2}
+ROPE_MAX_AXES = 4
 ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "bands": 3}
 KV_BLOCK = 16
 KV_KERNEL_ROWS = 1
@@ -59,6 +61,12 @@ class KVAppendArgs(ctypes.Structure):
          ("dtype", _u32), ("q_heads", _u32)]
 
 
+class Axes(ctypes.Structure):
+    """w8a16_axes_t"""
+    _fields_ = [("positions", _vp), ("axis_stride", _i64), ("count", _u32), ("order", _u32),
+                ("pairs", _u32 * ROPE_MAX_AXES), ("table_pairs", _u32)]
+
+
 class KVPlan(ctypes.Structure):
     """w8a16_kv_plan_t"""
     _fields_ = [("kernel", _u32), ("row_blocks", _u32), ("waves", _u32), ("row_tiles", _u32), ("chunk_tiles", _u32),
@@ -84,11 +92,14 @@ def declare(lib) -> None:
     lib.w8a16_rope_table.argtypes = [ptr(RopeConfig), _vp, _u32, _u32, _vp]
     lib.w8a16_rope.argtypes = [_vp, _i64, _i64, _vp, _i64, _i64, _u32, _u32, _u32, _u32, _vp, _u32,
                                _u32, _vp, _u32, _u32, _vp]
+    lib.w8a16_rope_axes.argtypes = [_vp, _i64, _i64, _vp, _i64, _i64, _u32, _u32, _u32, _u32, _vp, _u32,
+                                    ptr(Axes), _u32, _u32, _vp]
+    lib.w8a16_kv_append_axes.argtypes = [ptr(KVCacheDesc), ptr(KVSeqs), ptr(KVAppendArgs), ptr(Axes), _vp]
     lib.w8a16_kv_append.argtypes = [ptr(KVCacheDesc), ptr(KVSeqs), ptr(KVAppendArgs), _vp]
     lib.w8a16_kv_attention.argtypes = [ptr(KVCacheDesc), ptr(KVSeqs), ptr(KVAttentionArgs), _vp]
     lib.w8a16_plan_kv_attention.argtypes = [_u32] * 8 + [ptr(KVPlan)]
-    for name in ("w8a16_rope_table", "w8a16_rope", "w8a16_kv_append", "w8a16_kv_attention",
-                 "w8a16_plan_kv_attention"):
+    for name in ("w8a16_rope_table", "w8a16_rope", "w8a16_rope_axes", "w8a16_kv_append",
+                 "w8a16_kv_append_axes", "w8a16_kv_attention", "w8a16_plan_kv_attention"):
         getattr(lib, name).restype = ctypes.c_int
 
 
@@ -255,11 +266,35 @@ def _check_table(f32, table):
     return table.data_ptr(), positions, 2 * pairs
 
 
-def rope(x, table, positions, out=None, *, layout: str = "half", inverse: bool = False, stream=None):
+def _axes(i32, positions, tokens, sections, order, table_pairs) -> Axes:
+    """Positions of several axes; sections: pairs of each."""
+    if order not in ROPE_ORDERS:
+        raise ValueError("order must be 'split', 'turns' or 'own'")
+    count = len(sections)
+    if not 0 < count <= ROPE_MAX_AXES or min(sections) < 0:
+        raise ValueError("sections must be the pairs of 1 to %d axes" % ROPE_MAX_AXES)
+    if positions is None or positions.dtype != i32 or positions.shape != (count, tokens) or \
+            not positions.is_cuda or (tokens > 1 and positions.stride(1) != 1):
+        raise ValueError("positions must be an int32 GPU tensor [%d, %d] with a unit stride along tokens" %
+                         (count, tokens))
+    return Axes(positions.data_ptr(), positions.stride(0), count, ROPE_ORDERS[order],
+                (_u32 * ROPE_MAX_AXES)(*sections), table_pairs)
+
+
+def rope(x, table, positions, out=None, *, layout: str = "half", inverse: bool = False, sections=None,
+         order: str = "split", stream=None):
     """x [tokens, heads, head_dim] (bfloat16, float16 or float32) with the
     first 2 * table.shape[1] elements of each head rotated to `positions`
     (int32 [tokens]).  inverse=True rotates back, which is also the gradient:
-    dx = rope(dy, ..., inverse=True).  out may be x.  Returns out."""
+    dx = rope(dy, ..., inverse=True).  out may be x.  Returns out.
+
+    sections: pairs of each of up to four axes (a picture's frame, row and
+    column); positions is then int32 [axes, tokens] and the first
+    2 * sum(sections) elements are rotated.  order: "split" (the first
+    sections[0] pairs are axis 0's, and so on), "turns" (pair i is axis
+    i % axes's while that one has pairs left, else axis 0's) or "own" (as
+    split, each axis starting again at the table's first column); the table has
+    sum(sections) pairs, in "own" at least max(sections)."""
     lib, torch, dtypes, check, raw = _setup()
     dtype = x.dtype
     if x.dim() != 3 or dtype not in dtypes:
@@ -271,12 +306,21 @@ def rope(x, table, positions, out=None, *, layout: str = "half", inverse: bool =
         yt, yh = heads * dim, dim
     else:
         yt, yh = _rows("out", out, tokens, heads, dim, dtype)
-    if positions.shape != (tokens,) or positions.dtype != torch.int32 or \
-            not positions.is_contiguous() or not positions.is_cuda:
-        raise ValueError("positions must be a contiguous int32 GPU tensor [tokens]")
     if layout not in ROPE_LAYOUTS:
         raise ValueError("layout must be 'half' or 'interleaved'")
     tp, tn, rot = _check_table(torch.float32, table)
+    if sections is not None:
+        st = lib.w8a16_rope_axes(x.data_ptr(), xt, xh, out.data_ptr(), yt, yh, dtypes[dtype], tokens, heads,
+                                 dim, tp, tn,
+                                 _axes(torch.int32, positions, tokens, sections, order, table.shape[1]),
+                                 ROPE_LAYOUTS[layout], inverse,
+                                 raw(x.get_device()) if stream is None else stream.cuda_stream)
+        if st:
+            check(st)
+        return out
+    if positions.shape != (tokens,) or positions.dtype != torch.int32 or \
+            not positions.is_contiguous() or not positions.is_cuda:
+        raise ValueError("positions must be a contiguous int32 GPU tensor [tokens]")
     st = lib.w8a16_rope(x.data_ptr(), xt, xh, out.data_ptr(), yt, yh, dtypes[dtype], tokens, heads, dim,
                         tp, tn, rot, positions.data_ptr(), ROPE_LAYOUTS[layout], inverse,
                         raw(x.get_device()) if stream is None else stream.cuda_stream)
@@ -286,7 +330,8 @@ def rope(x, table, positions, out=None, *, layout: str = "half", inverse: bool =
 
 
 def kv_append(cache, k, v, block_table, kv_lens, *, cu_seqlens=None, max_new: Optional[int] = None,
-              table=None, layout: str = "half", q=None, q_out=None, stream=None):
+              table=None, layout: str = "half", q=None, q_out=None, positions=None, sections=None,
+              order: str = "split", stream=None):
     """Append the new tokens' keys and values (k, v [tokens, kv_heads,
     head_dim]) to `cache`, keys rotated by `table` if given; with q [tokens,
     q_heads, head_dim] also rotate the queries, in the same launch.
@@ -295,7 +340,9 @@ def kv_append(cache, k, v, block_table, kv_lens, *, cu_seqlens=None, max_new: Op
     counted.  block_table int32 [seqs, pages].  cu_seqlens int32 [seqs + 1]:
     offsets of the sequences' new tokens; None: tokens / seqs each.  max_new:
     at least the most new tokens of one sequence (None: all tokens; a closer
-    bound launches less).  Returns q_out (None without q)."""
+    bound launches less).  sections, positions (int32 [axes, tokens]) and
+    order: rotate by positions of several axes, as rope does, in place of each
+    token's place in its sequence.  Returns q_out (None without q)."""
     lib, torch, dtypes, check, raw = _setup()
     dtype = k.dtype
     if k.dim() != 3 or dtype not in dtypes:
@@ -323,10 +370,21 @@ def kv_append(cache, k, v, block_table, kv_lens, *, cu_seqlens=None, max_new: Op
     else:
         q_out = None
     seqs = _seqs_desc(torch.int32, block_table, kv_lens, cu_seqlens, tokens, max_new)
+    axes = None
+    if sections is not None:
+        if table is None:
+            raise ValueError("positions of several axes need a table")
+        axes = _axes(torch.int32, positions, tokens, sections, order, table.shape[1])
+        rot = 2 * sum(sections)
+    elif positions is not None:
+        raise ValueError("positions need sections")
     args = KVAppendArgs(k.data_ptr(), v.data_ptr(), qp, op, kt, kh, vt, vh, qt, qh, ot, oh, tp, tn, rot,
                         ROPE_LAYOUTS[layout], dtypes[dtype], hq)
-    st = lib.w8a16_kv_append(desc, seqs, args,
-                             raw(k.get_device()) if stream is None else stream.cuda_stream)
+    queue = raw(k.get_device()) if stream is None else stream.cuda_stream
+    if axes is None:
+        st = lib.w8a16_kv_append(desc, seqs, args, queue)
+    else:
+        st = lib.w8a16_kv_append_axes(desc, seqs, args, axes, queue)
     if st:
         check(st)
     return q_out

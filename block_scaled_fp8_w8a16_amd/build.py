@@ -20,9 +20,9 @@ LIB = os.path.join(HERE, "libw8a16.so")
 SOURCES = ["plan.cpp", "api.hip", "stream_kernel.hip", "tile_m64.hip", "tile_m128.hip",
            "wide_kernel.hip", "split_reduce.hip", "ring_kernel.hip", "w8a8_kernel.hip",
            "w4a4_kernel.hip", "kv_plan.cpp", "attention_api.hip", "rope_kernel.hip",
-           "kv_append.hip", "kv_attention.hip", "kv_tile_kernel.hip"]
+           "kv_append.hip", "kv_append_axes.hip", "kv_attention.hip", "kv_tile_kernel.hip"]
 HEADERS = ["plan.h", "kernels.h", "device_common.h", "tile_kernel.h", "host.h", "attention.h",
-           "attention_device.h", "rope_device.h"]
+           "attention_device.h", "rope_device.h", "kv_append_kernel.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

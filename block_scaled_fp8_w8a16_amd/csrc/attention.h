@@ -44,6 +44,19 @@ struct RopeRows {
     uint32_t pairs;                             // P: pairs per item (1, 4 or 8)
 };
 
+// Rotation by several positions of a token (frame, row, column, ...): which
+// of them turns a pair, and by which column of the table.
+struct RopeAxes {
+    const int32_t *positions;                   // axis a of token t at a * stride + t
+    int64_t stride;
+    uint32_t count, columns;                    // axes; the table's pairs per position
+    uint32_t first[W8A16_ROPE_MAX_AXES];        // axis a's first pair (axes past count: past every pair)
+    uint32_t stop[W8A16_ROPE_MAX_AXES];         // in turns: axis a > 0 has the pairs a, a + count, ... below it
+    uint32_t turns, own;                        // the order (neither: split)
+    uint32_t by_count;                          // 65536 / count + 1: i * by_count >> 16 is i / count for i < 512
+    uint32_t whole;                             // every item's pairs are of one axis
+};
+
 // Heads a thread rotates where there are enough of them to fill the chip.
 constexpr uint32_t kRopeHeads = 4;
 
@@ -53,6 +66,10 @@ struct RopeArgs {
     uint32_t total;                             // threads: tokens * head groups * items
     FastDiv by_row;                             // head groups * items
     uint32_t inverse, heads_per_thread;         // 1 or kRopeHeads
+};
+
+struct RopeAxesArgs : RopeArgs {
+    RopeAxes axes;
 };
 
 struct KvPool {
@@ -84,6 +101,10 @@ struct AppendArgs {
     FastDiv by_q_groups;
 };
 
+struct AppendAxesArgs : AppendArgs {
+    RopeAxes axes;             // positions of the token axis; the items of a.q and of the keys are whole or not together
+};
+
 struct AttnArgs {
     KvPool pool;
     KvSeqs seqs;
@@ -107,7 +128,9 @@ constexpr uint32_t kKvTile = 64;                // keys per tile
 hipError_t launch_rope_table(const w8a16_rope_config_t &c, float *table, uint32_t positions,
                              uint32_t rot_dim, hipStream_t stream);
 hipError_t launch_rope(const RopeArgs &a, uint32_t dtype, hipStream_t stream);
+hipError_t launch_rope_axes(const RopeAxesArgs &a, uint32_t dtype, hipStream_t stream);
 hipError_t launch_kv_append(const AppendArgs &a, uint32_t dtype, hipStream_t stream);
+hipError_t launch_kv_append_axes(const AppendAxesArgs &a, uint32_t dtype, hipStream_t stream);
 // Workgroups of the attention's launch: the plan's and, where offsets are
 // given, those of the tokens outside them.
 inline uint64_t kv_launch_groups(const AttnArgs &a, uint32_t waves)

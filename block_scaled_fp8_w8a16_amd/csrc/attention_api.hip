@@ -106,6 +106,67 @@ int check_rope(const char *entry, uint32_t dtype, uint32_t head_dim, uint32_t ro
     return W8A16_OK;
 }
 
+// Positions of several axes, beside a rotation of `rot` elements and a table.
+int check_axes(const char *entry, const w8a16_axes_t *x, uint32_t table_positions)
+{
+    if (x->order > W8A16_ROPE_OWN)
+        return refuse(W8A16_ERR_SHAPE, "%s: order=%u is not a w8a16_rope_order", entry, x->order);
+    if (!x->count || x->count > W8A16_ROPE_MAX_AXES)
+        return refuse(W8A16_ERR_SHAPE, "%s: %u axes, must be 1..%u", entry, x->count,
+                      (unsigned)W8A16_ROPE_MAX_AXES);
+    uint64_t sum = 0, most = 0;
+    for (uint32_t a = 0; a < x->count; ++a) {
+        sum += x->pairs[a];
+        most = x->pairs[a] > most ? x->pairs[a] : most;
+    }
+    if (!sum || sum > 512)
+        return refuse(W8A16_ERR_SHAPE, "%s: the axes' %llu pairs must be 1..512 in all", entry,
+                      (unsigned long long)sum);
+    for (uint32_t a = 1; x->order == W8A16_ROPE_TURNS && a < x->count; ++a)
+        if (x->pairs[a] && a + x->count * (uint64_t)(x->pairs[a] - 1) >= sum)
+            return refuse(W8A16_ERR_SHAPE, "%s: axis %u of %u does not find %u pairs by turns among %llu",
+                          entry, a, x->count, x->pairs[a], (unsigned long long)sum);
+    if (x->order == W8A16_ROPE_OWN ? x->table_pairs < most : x->table_pairs != sum)
+        return refuse(W8A16_ERR_SHAPE, "%s: a table of %u pairs, needs %llu", entry, x->table_pairs,
+                      (unsigned long long)(x->order == W8A16_ROPE_OWN ? most : sum));
+    if (!table_positions)
+        return refuse(W8A16_ERR_SHAPE, "%s: the table has no position", entry);
+    return W8A16_OK;
+}
+
+uint32_t axes_rot(const w8a16_axes_t *x)
+{
+    uint32_t sum = 0;
+    for (uint32_t a = 0; a < x->count && a < W8A16_ROPE_MAX_AXES; ++a)
+        sum += x->pairs[a];
+    return 2 * sum;
+}
+
+// pairs: of the widest item that takes its angles from these.
+void fill_axes(RopeAxes &r, const w8a16_axes_t *x, uint32_t pairs)
+{
+    r.positions = x->positions;
+    r.stride = x->axis_stride;
+    r.count = x->count;
+    r.columns = x->table_pairs;
+    r.turns = x->order == W8A16_ROPE_TURNS;
+    r.own = x->order == W8A16_ROPE_OWN;
+    r.by_count = 65536u / x->count + 1u;
+    uint32_t at = 0, axes = 0;
+    r.whole = 1;
+    for (uint32_t a = 0; a < W8A16_ROPE_MAX_AXES; ++a) {
+        const uint32_t n = a < x->count ? x->pairs[a] : 0u;
+        r.first[a] = a < x->count ? at : ~0u;
+        r.stop[a] = x->count * n;
+        axes += n ? 1 : 0;
+        if (n && at % pairs)
+            r.whole = 0;
+        at += n;
+    }
+    if (r.turns && axes > 1 && pairs > 1)
+        r.whole = 0;
+}
+
 int check_cache(const char *entry, const w8a16_kv_cache_t *c)
 {
     if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale)
@@ -229,16 +290,22 @@ int rope_table(const w8a16_rope_config_t *c, float *table, uint32_t positions, u
     return named(launched(stream), entry);
 }
 
-int rope(const void *x, const int64_t strides[4], void *y, uint32_t dtype, uint32_t tokens,
-         uint32_t heads, uint32_t head_dim, const float *table, uint32_t table_positions,
-         uint32_t rot, const int32_t *positions, uint32_t layout, uint32_t inverse, hipStream_t stream)
+// positions: one per token, or null with axes.
+int rope(const char *entry, const void *x, const int64_t strides[4], void *y, uint32_t dtype,
+         uint32_t tokens, uint32_t heads, uint32_t head_dim, const float *table, uint32_t table_positions,
+         uint32_t rot, const int32_t *positions, const w8a16_axes_t *axes, uint32_t layout,
+         uint32_t inverse, hipStream_t stream)
 {
-    const char *entry = "w8a16_rope";
     int st = check_levers(entry);
     if (st != W8A16_OK)
         return st;
     if (tokens && (!x || !y || !table || !positions))
         return refuse(W8A16_ERR_NULL_PTR, "%s: x, y, table and positions must be non-null", entry);
+    if (axes) {
+        st = check_axes(entry, axes, table_positions);
+        if (st != W8A16_OK)
+            return st;
+    }
     st = check_rope(entry, dtype, head_dim, rot, layout);
     if (st != W8A16_OK)
         return st;
@@ -249,7 +316,7 @@ int rope(const void *x, const int64_t strides[4], void *y, uint32_t dtype, uint3
     st = check_apart(entry, "y", strides[2], strides[3], tokens, heads, head_dim);
     if (st != W8A16_OK)
         return st;
-    RopeArgs a;
+    RopeAxesArgs a;
     std::memset(static_cast<void *>(&a), 0, sizeof a);
     fill_rope(a.r, x, y, strides, table, table_positions, rot, head_dim, layout, heads, dtype);
     a.heads_per_thread = rope_heads_per_thread((uint64_t)heads * a.r.items * tokens);
@@ -262,23 +329,29 @@ int rope(const void *x, const int64_t strides[4], void *y, uint32_t dtype, uint3
     a.total = (uint32_t)total;
     a.by_row = FastDiv((uint32_t)row);
     a.inverse = inverse != 0;
-    hipError_t e = launch_rope(a, dtype, stream);
+    if (axes)
+        fill_axes(a.axes, axes, a.r.pairs);
+    hipError_t e = axes ? launch_rope_axes(a, dtype, stream) : launch_rope(a, dtype, stream);
     if (e != hipSuccess)
         return named(hip_fail(e, "kernel launch"), entry);
     if (log_enabled()) {
-        char line[200];
-        snprintf(line, sizeof line,
-                 "w8a16: %s tokens=%u heads=%u head_dim=%u rot_dim=%u: %u pairs of %u heads per thread\n",
-                 entry, tokens, heads, head_dim, rot, a.r.pairs, a.heads_per_thread);
+        char line[240];
+        int n = snprintf(line, sizeof line,
+                         "w8a16: %s tokens=%u heads=%u head_dim=%u rot_dim=%u: %u pairs of %u heads per "
+                         "thread", entry, tokens, heads, head_dim, rot, a.r.pairs, a.heads_per_thread);
+        if (axes)
+            n += snprintf(line + n, sizeof line - n, ", %u axes%s", axes->count,
+                          a.axes.whole ? "" : " within an item");
+        snprintf(line + n, sizeof line - n, "\n");
         log_line(line);
     }
     return named(launched(stream), entry);
 }
 
-int kv_append(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
-              const w8a16_kv_append_args_t *g, hipStream_t stream)
+// axes: null for the sequences' own positions.
+int kv_append(const char *entry, const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
+              const w8a16_kv_append_args_t *g, const w8a16_axes_t *axes, hipStream_t stream)
 {
-    const char *entry = "w8a16_kv_append";
     int st = check_levers(entry);
     if (st != W8A16_OK)
         return st;
@@ -290,8 +363,18 @@ int kv_append(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
         return st;
     if (!g || (seqs->tokens && (!g->k || !g->v)) || (g->q && !g->q_out))
         return refuse(W8A16_ERR_NULL_PTR, "%s: k, v and, with q, q_out must be non-null", entry);
+    if (axes && seqs->tokens && (!axes->positions || !g->table))
+        return refuse(W8A16_ERR_NULL_PTR, "%s: positions and table must be non-null", entry);
     if (g->dtype < W8A16_BF16 || g->dtype > W8A16_FP32)
         return refuse(W8A16_ERR_SHAPE, "%s: dtype=%u is not a w8a16_dtype", entry, g->dtype);
+    if (axes) {
+        st = check_axes(entry, axes, g->table_positions);
+        if (st != W8A16_OK)
+            return st;
+        if (g->rot_dim != axes_rot(axes))
+            return refuse(W8A16_ERR_SHAPE, "%s: rot_dim=%u must be twice the axes' pairs, %u", entry,
+                          g->rot_dim, axes_rot(axes));
+    }
     if (g->table) {
         st = check_rope(entry, g->dtype, cache->head_dim, g->rot_dim, g->layout);
         if (st != W8A16_OK)
@@ -301,7 +384,7 @@ int kv_append(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
         return refuse(W8A16_ERR_SHAPE, "%s: queries need a table and q_heads >= 1", entry);
     if (seqs->tokens == 0)
         return W8A16_OK;
-    AppendArgs a;
+    AppendAxesArgs a;
     std::memset(static_cast<void *>(&a), 0, sizeof a);
     a.pool = pool_of(*cache);
     a.seqs = seqs_of(*seqs);
@@ -355,7 +438,9 @@ int kv_append(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
         if (st != W8A16_OK)
             return st;
     }
-    hipError_t e = launch_kv_append(a, g->dtype, stream);
+    if (axes)
+        fill_axes(a.axes, axes, g->q && a.q.pairs > a.vec ? a.q.pairs : a.vec);
+    hipError_t e = axes ? launch_kv_append_axes(a, g->dtype, stream) : launch_kv_append(a, g->dtype, stream);
     if (e != hipSuccess)
         return named(hip_fail(e, "kernel launch"), entry);
     if (log_enabled()) {
@@ -526,8 +611,24 @@ int w8a16_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, voi
 {
     const int64_t strides[4] = {x_token_stride, x_head_stride, y_token_stride, y_head_stride};
     return w8a16::guarded("w8a16_rope", [&] {
-        return w8a16::rope(x, strides, y, dtype, tokens, heads, head_dim, table, table_positions, rot_dim,
-                           positions, layout, inverse, static_cast<hipStream_t>(stream));
+        return w8a16::rope("w8a16_rope", x, strides, y, dtype, tokens, heads, head_dim, table,
+                           table_positions, rot_dim, positions, nullptr, layout, inverse,
+                           static_cast<hipStream_t>(stream));
+    });
+}
+
+int w8a16_rope_axes(const void *x, int64_t x_token_stride, int64_t x_head_stride, void *y,
+                    int64_t y_token_stride, int64_t y_head_stride, uint32_t dtype, uint32_t tokens,
+                    uint32_t heads, uint32_t head_dim, const float *table, uint32_t table_positions,
+                    const w8a16_axes_t *axes, uint32_t layout, uint32_t inverse, void *stream)
+{
+    const int64_t strides[4] = {x_token_stride, x_head_stride, y_token_stride, y_head_stride};
+    return w8a16::guarded("w8a16_rope_axes", [&] {
+        const w8a16_axes_t none = {};
+        const w8a16_axes_t *const given = axes ? axes : &none;     // (null positions, refused as such)
+        return w8a16::rope("w8a16_rope_axes", x, strides, y, dtype, tokens, heads, head_dim, table,
+                           table_positions, w8a16::axes_rot(given), given->positions, given, layout,
+                           inverse, static_cast<hipStream_t>(stream));
     });
 }
 
@@ -535,7 +636,18 @@ int w8a16_kv_append(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
                     const w8a16_kv_append_args_t *args, void *stream)
 {
     return w8a16::guarded("w8a16_kv_append", [&] {
-        return w8a16::kv_append(cache, seqs, args, static_cast<hipStream_t>(stream));
+        return w8a16::kv_append("w8a16_kv_append", cache, seqs, args, nullptr,
+                                static_cast<hipStream_t>(stream));
+    });
+}
+
+int w8a16_kv_append_axes(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
+                         const w8a16_kv_append_args_t *args, const w8a16_axes_t *axes, void *stream)
+{
+    return w8a16::guarded("w8a16_kv_append_axes", [&] {
+        const w8a16_axes_t none = {};
+        return w8a16::kv_append("w8a16_kv_append_axes", cache, seqs, args, axes ? axes : &none,
+                                static_cast<hipStream_t>(stream));
     });
 }
 

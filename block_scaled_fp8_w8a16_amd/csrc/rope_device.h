@@ -56,13 +56,88 @@ __device__ __forceinline__ bool token_place(const KvSeqs &s, uint32_t t, uint32_
     return pos >= 0;
 }
 
+// Cosines and sines of a token's pairs p0 .. p0 + P - 1: of one position's
+// table row, null for a position outside the table (NaN).
+struct RowAngles {
+    const float *cs;
+    template <int P> __device__ __forceinline__ void load(uint32_t p0, float (&c)[P], float (&s)[P]) const
+    {
+        const float nan = __builtin_nanf("");
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            c[i] = cs ? cs[2 * (p0 + i)] : nan;
+            s[i] = cs ? cs[2 * (p0 + i) + 1] : nan;
+        }
+    }
+};
+
+// The same of a token with a position for each axis.  The positions are
+// loaded once; pairs of one axis (a.whole) take their angles as one piece of
+// the table, others one by one.
+struct AxesAngles {
+    const RopeAxes &a;
+    const float2 *table;
+    uint32_t positions, at[W8A16_ROPE_MAX_AXES];
+
+    __device__ __forceinline__ AxesAngles(const RopeAxes &axes, const float *tab, uint32_t table_positions,
+                                          uint32_t token)
+        : a(axes), table(reinterpret_cast<const float2 *>(tab)), positions(table_positions)
+    {
+#pragma unroll
+        for (uint32_t x = 0; x < W8A16_ROPE_MAX_AXES; ++x)
+            at[x] = (uint32_t)a.positions[(x < a.count ? (int64_t)x * a.stride : 0) + token];
+    }
+    // Position and table column of pair i.
+    __device__ __forceinline__ uint32_t place(uint32_t i, uint32_t &col) const
+    {
+        uint32_t p = at[0], from = 0;
+        if (a.turns) {
+            const uint32_t x = i - (i * a.by_count >> 16) * a.count;
+#pragma unroll
+            for (uint32_t y = 1; y < W8A16_ROPE_MAX_AXES; ++y)
+                p = x == y && i < a.stop[y] ? at[y] : p;
+        } else {
+#pragma unroll
+            for (uint32_t y = 1; y < W8A16_ROPE_MAX_AXES; ++y)
+                if (i >= a.first[y]) {
+                    p = at[y];
+                    from = a.first[y];
+                }
+        }
+        col = a.own ? i - from : i;
+        return p;
+    }
+    template <int P> __device__ __forceinline__ void load(uint32_t p0, float (&c)[P], float (&s)[P]) const
+    {
+        const float nan = __builtin_nanf("");
+        uint32_t col;
+        if (a.whole) {
+            const uint32_t p = place(p0, col);
+            const float2 *row = table + (size_t)(p < positions ? p : 0u) * a.columns + col;
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const float2 v = row[i];
+                c[i] = p < positions ? v.x : nan;
+                s[i] = p < positions ? v.y : nan;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                const uint32_t p = place(p0 + i, col);
+                const float2 v = table[(size_t)(p < positions ? p : 0u) * a.columns + col];
+                c[i] = p < positions ? v.x : nan;
+                s[i] = p < positions ? v.y : nan;
+            }
+        }
+    }
+};
+
 // Item `item` of N heads from head `h` on (those below r.heads): P pairs, or
-// 2P elements past rot.  T: element type; x, y: the token's rows; cs: the
-// position's table row, null for a position outside the table.  The heads'
-// loads are issued together and share the cosines and sines.
-template <class T, int P, int N, bool HALF>
+// 2P elements past rot.  T: element type; x, y: the token's rows.  The
+// heads' loads are issued together and share the cosines and sines.
+template <class T, int P, int N, bool HALF, class Angles>
 __device__ __forceinline__ void rope_heads(const RopeRows &r, const T *x, T *y, uint32_t h, uint32_t item,
-                                           const float *cs, bool inverse)
+                                           const Angles &angles, bool inverse)
 {
     typedef typename Vec<T, P>::type V;
     x += (int64_t)h * r.x_head;
@@ -94,13 +169,10 @@ __device__ __forceinline__ void rope_heads(const RopeRows &r, const T *x, T *y, 
     }
     if (pair) {
         float c[P], s[P];
-        const float nan = __builtin_nanf("");
+        angles.load(p0, c, s);
 #pragma unroll
-        for (int i = 0; i < P; ++i) {
-            c[i] = cs ? cs[2 * (p0 + i)] : nan;
-            s[i] = cs ? cs[2 * (p0 + i) + 1] : nan;
+        for (int i = 0; i < P; ++i)
             s[i] = inverse ? -s[i] : s[i];
-        }
         constexpr bool apart = HALF || P == 1;
 #pragma unroll
         for (int n = 0; n < N; ++n) {

@@ -16,6 +16,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "attention.h"
 #include "rope_device.h"
 
@@ -55,35 +57,41 @@ __global__ __launch_bounds__(256) void w8a16_rope_table_kernel(w8a16_rope_config
     reinterpret_cast<float2 *>(table)[idx] = v;
 }
 
-template <class T, int P, int N, bool HALF>
-__global__ __launch_bounds__(256) void w8a16_rope_kernel(RopeArgs a)
+// Args: RopeArgs, or RopeAxesArgs for several axes.
+template <class T, int P, int N, bool HALF, class Args>
+__global__ __launch_bounds__(256) void w8a16_rope_kernel(Args a)
 {
     const uint32_t idx = blockIdx.x * 256u + threadIdx.x;
     if (idx >= a.total)
         return;
     const uint32_t t = a.by_row.div(idx), rest = idx - t * a.by_row.d;
     const uint32_t hg = a.r.by_items.div(rest), item = rest - hg * a.r.items;
-    const uint32_t pos = (uint32_t)a.positions[t];
-    const float *cs = pos < a.r.table_positions ? a.r.table + (size_t)pos * a.r.rot : nullptr;
-    rope_heads<T, P, N, HALF>(a.r, reinterpret_cast<const T *>(a.r.x) + (int64_t)t * a.r.x_token,
-                        reinterpret_cast<T *>(a.r.y) + (int64_t)t * a.r.y_token, hg * N, item, cs,
-                        a.inverse != 0);
+    const T *x = reinterpret_cast<const T *>(a.r.x) + (int64_t)t * a.r.x_token;
+    T *y = reinterpret_cast<T *>(a.r.y) + (int64_t)t * a.r.y_token;
+    if constexpr (std::is_same<Args, RopeAxesArgs>::value) {
+        rope_heads<T, P, N, HALF>(a.r, x, y, hg * N, item, AxesAngles(a.axes, a.r.table, a.r.table_positions, t),
+                                  a.inverse != 0);
+    } else {
+        const uint32_t pos = (uint32_t)a.positions[t];
+        const float *cs = pos < a.r.table_positions ? a.r.table + (size_t)pos * a.r.rot : nullptr;
+        rope_heads<T, P, N, HALF>(a.r, x, y, hg * N, item, RowAngles{cs}, a.inverse != 0);
+    }
 }
 
-template <class T, int N, bool HALF>
-hipError_t launch_heads(const RopeArgs &a, hipStream_t stream)
+template <class T, int N, bool HALF, class Args>
+hipError_t launch_heads(const Args &a, hipStream_t stream)
 {
     const dim3 grid((a.total + 255u) / 256u), block(256);
     switch (a.r.pairs) {
-    case 8: hipLaunchKernelGGL((w8a16_rope_kernel<T, 8, N, HALF>), grid, block, 0, stream, a); break;
-    case 4: hipLaunchKernelGGL((w8a16_rope_kernel<T, 4, N, HALF>), grid, block, 0, stream, a); break;
-    default: hipLaunchKernelGGL((w8a16_rope_kernel<T, 1, N, HALF>), grid, block, 0, stream, a); break;
+    case 8: hipLaunchKernelGGL((w8a16_rope_kernel<T, 8, N, HALF, Args>), grid, block, 0, stream, a); break;
+    case 4: hipLaunchKernelGGL((w8a16_rope_kernel<T, 4, N, HALF, Args>), grid, block, 0, stream, a); break;
+    default: hipLaunchKernelGGL((w8a16_rope_kernel<T, 1, N, HALF, Args>), grid, block, 0, stream, a); break;
     }
     return hipGetLastError();
 }
 
-template <class T>
-hipError_t launch_type(const RopeArgs &a, hipStream_t stream)
+template <class T, class Args>
+hipError_t launch_type(const Args &a, hipStream_t stream)
 {
     if (a.heads_per_thread == 1)
         return a.r.half ? launch_heads<T, 1, true>(a, stream) : launch_heads<T, 1, false>(a, stream);
@@ -102,13 +110,28 @@ hipError_t launch_rope_table(const w8a16_rope_config_t &c, float *table, uint32_
     return hipGetLastError();
 }
 
-hipError_t launch_rope(const RopeArgs &a, uint32_t dtype, hipStream_t stream)
+namespace {
+
+template <class Args>
+hipError_t launch_any(const Args &a, uint32_t dtype, hipStream_t stream)
 {
     switch (dtype) {
     case W8A16_BF16: return launch_type<__bf16>(a, stream);
     case W8A16_FP16: return launch_type<_Float16>(a, stream);
     default: return launch_type<float>(a, stream);
     }
+}
+
+}  // namespace
+
+hipError_t launch_rope(const RopeArgs &a, uint32_t dtype, hipStream_t stream)
+{
+    return launch_any(a, dtype, stream);
+}
+
+hipError_t launch_rope_axes(const RopeAxesArgs &a, uint32_t dtype, hipStream_t stream)
+{
+    return launch_any(a, dtype, stream);
 }
 
 }  // namespace w8a16

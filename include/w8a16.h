@@ -77,7 +77,7 @@ typedef enum w8a16_status {
  * first call of an entry point that enqueues work (w8a16_gemm,
  * _gemm_planned, _gemm_noalloc, _gemm_batched, _act_quant_fp8,
  * _gemm_w8a8[_planned], _gemm_w4a4[_planned], _rope_table, _rope,
- * _kv_append, _kv_attention); unset, empty or "0" is off,
+ * _rope_axes, _kv_append[_axes], _kv_attention); unset, empty or "0" is off,
  * "1" is on, and any other value makes each of those calls return
  * W8A16_ERR_ENV, before any other check, with the variable named in
  * w8a16_last_error().  The pure planning calls ignore them.
@@ -423,6 +423,42 @@ int w8a16_rope(const void *x, int64_t x_token_stride, int64_t x_head_stride, voi
                uint32_t rot_dim, const int32_t *positions, uint32_t layout, uint32_t inverse,
                void *stream);
 
+/* Rotary positions of several axes: a token has a position on each of 1 to
+ * W8A16_ROPE_MAX_AXES axes (a picture's or video's frame, row and column),
+ * and each pair of a head turns by one of them.  Axis a has pairs[a] pairs
+ * (0 is allowed); rot_dim is twice their sum, at most 1024.
+ *   SPLIT  the first pairs[0] pairs are axis 0's, the next pairs[1] axis 1's, ...
+ *   TURNS  pair i is axis a = i mod count's while i < count * pairs[a], else
+ *          (and where a = 0) axis 0's.  Each axis a > 0 must find its pairs:
+ *          a + count * (pairs[a] - 1) below the sum
+ *   OWN    as SPLIT, and each axis counts its pairs from 0: the pair takes
+ *          column i of the table for the i-th pair of its axis
+ * In SPLIT and TURNS pair i takes column i. */
+#define W8A16_ROPE_MAX_AXES 4
+typedef enum w8a16_rope_order {
+    W8A16_ROPE_SPLIT = 0,
+    W8A16_ROPE_TURNS = 1,
+    W8A16_ROPE_OWN = 2
+} w8a16_rope_order;
+typedef struct w8a16_axes {
+    const int32_t *positions; /* token t on axis a: positions[a * axis_stride + t] */
+    int64_t axis_stride;
+    uint32_t count;           /* axes */
+    uint32_t order;           /* w8a16_rope_order */
+    uint32_t pairs[W8A16_ROPE_MAX_AXES];
+    uint32_t table_pairs;     /* columns of the table: the sum of pairs; OWN: at least the largest */
+} w8a16_axes_t;
+
+/* w8a16_rope with a position per axis: with (c, s) =
+ * table[positions[axis of i][t]][column of i] for pair i, the same formula,
+ * roundings, gradient and errors.  table: FP32 [table_positions, table_pairs,
+ * 2], at least one position; a position outside it gives NaN in its axis's
+ * elements alone. */
+int w8a16_rope_axes(const void *x, int64_t x_token_stride, int64_t x_head_stride, void *y,
+                    int64_t y_token_stride, int64_t y_head_stride, uint32_t dtype, uint32_t tokens,
+                    uint32_t heads, uint32_t head_dim, const float *table, uint32_t table_positions,
+                    const w8a16_axes_t *axes, uint32_t layout, uint32_t inverse, void *stream);
+
 /* The cache.  A page holds page_size tokens (a multiple of W8A16_KV_BLOCK up
  * to 1024) of every KV head; inside a page, blocks of 16 tokens of one head
  * share a scale.
@@ -487,6 +523,13 @@ typedef struct w8a16_kv_append_args {
  * append to the same page. */
 int w8a16_kv_append(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
                     const w8a16_kv_append_args_t *args, void *stream);
+
+/* w8a16_kv_append whose keys and queries turn by positions of several axes,
+ * as in w8a16_rope_axes, in place of their place in the sequence (which still
+ * says where they are stored).  args->table must be given, and args->rot_dim
+ * be twice the axes' pairs. */
+int w8a16_kv_append_axes(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
+                         const w8a16_kv_append_args_t *args, const w8a16_axes_t *axes, void *stream);
 
 /* Launch plan of the attention. */
 typedef enum w8a16_kv_kernel {
