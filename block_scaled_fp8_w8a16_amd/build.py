@@ -18,11 +18,13 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libw8a16.so")
 
 SOURCES = ["plan.cpp", "api.hip", "stream_kernel.hip", "tile_m64.hip", "tile_m128.hip",
+           "stream_epilogue.hip", "ring_epilogue.hip", "tile_epilogue.hip",
            "wide_kernel.hip", "split_reduce.hip", "ring_kernel.hip", "w8a8_kernel.hip",
            "w4a4_kernel.hip", "kv_plan.cpp", "attention_api.hip", "rope_kernel.hip",
            "kv_append.hip", "kv_append_axes.hip", "kv_attention.hip", "kv_tile_kernel.hip"]
 HEADERS = ["plan.h", "kernels.h", "device_common.h", "tile_kernel.h", "host.h", "attention.h",
-           "attention_device.h", "rope_device.h", "kv_append_kernel.h"]
+           "attention_device.h", "rope_device.h", "kv_append_kernel.h",
+           "stream_kernel.h", "ring_kernel.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
@@ -36,6 +38,7 @@ DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 # expensive part of its loop.  The VGPR form of the MFMA keeps them in VGPRs.
 _VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
 EXTRA_FLAGS = {"tile_m64.hip": _VGPR_FORM, "tile_m128.hip": _VGPR_FORM,
+               "tile_epilogue.hip": _VGPR_FORM,
                "w8a8_kernel.hip": _VGPR_FORM, "kv_attention.hip": _VGPR_FORM,
                "kv_tile_kernel.hip": _VGPR_FORM}
 

@@ -309,12 +309,58 @@ int check_call(const void *a, uint32_t a_row_stride, const void *w_fp8,
     return W8A16_OK;
 }
 
+// An epilogue's arguments as the kernels take them.
+int check_epilogue(const char *entry, const w8a16_epilogue_t *x, const void *c, uint32_t c_row_stride,
+                   uint32_t n, Epilogue *e)
+{
+    char buf[224];
+    if (!x) {
+        snprintf(buf, sizeof buf, "%s: null epilogue", entry);
+        return fail(W8A16_ERR_NULL_PTR, buf);
+    }
+    if (x->activation > W8A16_ACT_GELU_TANH) {
+        snprintf(buf, sizeof buf, "%s: activation=%u is not a w8a16_activation", entry, x->activation);
+        return fail(W8A16_ERR_SHAPE, buf);
+    }
+    auto known = [](uint32_t t) { return t == W8A16_BF16 || t == W8A16_FP32; };
+    if ((x->bias && !known(x->bias_dtype)) || (x->residual && !known(x->residual_dtype)) ||
+        !known(x->out_dtype)) {
+        snprintf(buf, sizeof buf, "%s: bias_dtype=%u, residual_dtype=%u and out_dtype=%u must be W8A16_BF16 "
+                 "or W8A16_FP32", entry, x->bias_dtype, x->residual_dtype, x->out_dtype);
+        return fail(W8A16_ERR_SHAPE, buf);
+    }
+    if ((x->gate && x->gate_row_stride < n) || (x->residual && x->residual_row_stride < n)) {
+        snprintf(buf, sizeof buf, "%s: gate_row_stride=%u and residual_row_stride=%u must be at least n=%u",
+                 entry, x->gate_row_stride, x->residual_row_stride, n);
+        return fail(W8A16_ERR_PITCH_TOO_SHORT, buf);
+    }
+    std::memset(e, 0, sizeof *e);
+    e->bias = static_cast<const uint8_t *>(x->bias);
+    e->gate = static_cast<const uint8_t *>(x->gate);
+    e->residual = static_cast<const uint8_t *>(x->residual);
+    e->gate_stride = x->gate_row_stride;
+    e->residual_stride = x->residual_row_stride;
+    e->activation = x->activation;
+    e->bias_f32 = x->bias_dtype == W8A16_FP32;
+    e->residual_f32 = x->residual_dtype == W8A16_FP32;
+    e->out_f32 = x->out_dtype == W8A16_FP32;
+    auto whole = [](const void *p, uint32_t stride, bool f32) {
+        return stride % 4 == 0 && reinterpret_cast<uintptr_t>(p) % (f32 ? 16 : 8) == 0;
+    };
+    e->vec = (whole(x->bias, 0, e->bias_f32) ? kVecBias : 0) |
+             (whole(x->gate, x->gate_row_stride, false) ? kVecGate : 0) |
+             (whole(x->residual, x->residual_row_stride, e->residual_f32) ? kVecResidual : 0) |
+             (whole(c, c_row_stride, e->out_f32) ? kVecOut : 0);
+    return W8A16_OK;
+}
+
 // Enqueue the plan's kernels.  `fixed`: the split-K workspace to use (the
 // no-alloc entry's scratch); null takes the (device, stream) workspace.
+// `epilogue`: null for a plain GEMM; else `plan` is a default plan.
 int run(const char *entry, const char *why, const void *a, uint32_t a_row_stride,
         const void *w_fp8, const float *block_scale, void *c, uint32_t c_row_stride,
         uint32_t m, uint32_t n, uint32_t k, const w8a16_plan_t &plan, hipStream_t stream,
-        const Workspace *fixed = nullptr)
+        const Workspace *fixed = nullptr, const Epilogue *epilogue = nullptr)
 {
     int dev = 0;
     hipError_t e = hipGetDevice(&dev);
@@ -330,8 +376,9 @@ int run(const char *entry, const char *why, const void *a, uint32_t a_row_stride
                 return st;
         }
     }
-    GemmArgs g;
-    std::memset(&g, 0, sizeof g);
+    EpilogueArgs with;
+    std::memset(static_cast<void *>(&with), 0, sizeof with);
+    GemmArgs &g = with;
     g.a = static_cast<const uint8_t *>(a);
     g.w = static_cast<const uint8_t *>(w_fp8);
     g.scale = block_scale;
@@ -347,7 +394,12 @@ int run(const char *entry, const char *why, const void *a, uint32_t a_row_stride
     g.n_tiles = plan.n_tiles;
     g.splits = plan.splits;
     g.steps_per_split = plan.steps_per_split;
-    if (plan.kernel == W8A16_KERNEL_STREAM)
+    if (epilogue) {
+        with.e = *epilogue;
+        e = plan.kernel == W8A16_KERNEL_STREAM ? launch_stream(with, plan, stream)
+            : plan.kernel == W8A16_KERNEL_RING ? launch_ring(with, plan, stream)
+                                               : launch_tile(with, plan, stream);
+    } else if (plan.kernel == W8A16_KERNEL_STREAM)
         e = launch_stream(g, plan, stream);
     else if (plan.kernel == W8A16_KERNEL_RING)
         e = launch_ring(g, plan, stream);
@@ -393,6 +445,39 @@ int w8a16_gemm(const void *a, uint32_t a_row_stride, const void *w_fp8,
         return st;
     return run("w8a16_gemm", plan_reason(), a, a_row_stride, w_fp8, block_scale, c,
                c_row_stride, m, n, k, plan, static_cast<hipStream_t>(stream));
+}
+
+int w8a16_gemm_epilogue(const void *a, uint32_t a_row_stride, const void *w_fp8,
+                        const float *block_scale, void *c, uint32_t c_row_stride, uint32_t m,
+                        uint32_t n, uint32_t k, const w8a16_epilogue_t *epilogue, void *stream)
+{
+    using namespace w8a16;
+    const char *entry = "w8a16_gemm_epilogue";
+    int st = check_levers(entry);
+    if (st != W8A16_OK)
+        return st;
+    st = check_call(a, a_row_stride, w_fp8, block_scale, c, c_row_stride, m, n, k);
+    if (st != W8A16_OK)
+        return fail_with_name(st, entry);
+    Epilogue e;
+    st = check_epilogue(entry, epilogue, c, c_row_stride, n, &e);
+    if (st != W8A16_OK)
+        return st;
+    int dev = 0;
+    hipError_t he = hipGetDevice(&dev);
+    if (he != hipSuccess)
+        return fail_with_name(hip_fail(he, "hipGetDevice"), entry);
+    uint32_t cus = 0;
+    st = device_cu_count(dev, &cus);
+    if (st != W8A16_OK)
+        return fail_with_name(st, entry);
+    w8a16_plan_t plan;
+    st = make_plan(m, n, k, cus, &plan);
+    if (st != W8A16_OK)
+        return fail_with_name(st, entry);
+    st = run(entry, plan_reason(), a, a_row_stride, w_fp8, block_scale, c, c_row_stride, m, n, k, plan,
+             static_cast<hipStream_t>(stream), nullptr, &e);
+    return st == W8A16_OK ? st : fail_with_name(st, entry);
 }
 
 int w8a16_gemm_planned(const void *a, uint32_t a_row_stride, const void *w_fp8,

@@ -152,9 +152,104 @@ __device__ __forceinline__ void barrier_lds()
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
+// What an epilogue reads for one output, or for four adjacent ones; nothing
+// for a plain GEMM.  Loaded apart from the store, so that the loads can be
+// under way while the sums are still being made.
+struct NoInputs {};
+template <int N> struct EpilogueInputs { float bias[N], gate[N], residual[N]; };
+
+template <int N>
+__device__ __forceinline__ NoInputs load_inputs(const GemmArgs &, uint32_t, uint32_t)
+{
+    return {};
+}
+
+// N elements from index i of a BF16 or FP32 array (n of them exist); vec: as
+// one piece where all N do.
+template <int N>
+__device__ __forceinline__ void load_row(float (&x)[N], const uint8_t *base, size_t i, uint32_t n, bool f32,
+                                         bool vec)
+{
+    if (N == 4 && vec && n >= 4) {
+        if (f32) {
+            const f32x4_t v = *reinterpret_cast<const f32x4_t *>(base + 4 * i);
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                x[k] = v[k];
+        } else {
+            const u32x2_t v = *reinterpret_cast<const u32x2_t *>(base + 2 * i);
+#pragma unroll
+            for (int k = 0; k < N; ++k)
+                x[k] = __builtin_bit_cast(float, k & 1 ? v[k >> 1] & 0xffff0000u : v[k >> 1] << 16);
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if ((uint32_t)k < n)
+            x[k] = f32 ? reinterpret_cast<const float *>(base)[i + k]
+                       : __builtin_bit_cast(float, (uint32_t)reinterpret_cast<const uint16_t *>(base)[i + k] << 16);
+}
+
+template <int N>
+__device__ __forceinline__ EpilogueInputs<N> load_inputs(const EpilogueArgs &g, uint32_t row, uint32_t col)
+{
+    EpilogueInputs<N> in = {};
+    if (row >= g.m || col >= g.n)
+        return in;
+    const Epilogue &e = g.e;
+    if (e.bias)
+        load_row<N>(in.bias, e.bias, col, g.n - col, e.bias_f32, e.vec & kVecBias);
+    if (e.gate)
+        load_row<N>(in.gate, e.gate, (size_t)row * e.gate_stride + col, g.n - col, false, e.vec & kVecGate);
+    if (e.residual)
+        load_row<N>(in.residual, e.residual, (size_t)row * e.residual_stride + col, g.n - col, e.residual_f32,
+                    e.vec & kVecResidual);
+    return in;
+}
+
+// x / (1 + e^-x) and its like: exp() of the device library, within 1 ulp, so
+// that an FP32 output keeps its digits.  x * sigmoid(2 u) is the hyperbolic
+// form 0.5 x (1 + tanh u) without its cancellation, and erfc() is 1 + erf().
+__device__ __forceinline__ float activate(float x, uint32_t act)
+{
+    switch (act) {
+    case W8A16_ACT_RELU: return x < 0.f ? 0.f : x;
+    case W8A16_ACT_SILU: return x / (1.0f + expf(-x));
+    case W8A16_ACT_GELU: return 0.5f * x * erfcf(-0.70710678118654752f * x);
+    case W8A16_ACT_GELU_TANH: {
+        const float u = 0.79788456080286536f * fmaf(0.044715f * x * x, x, x);
+        return x / (1.0f + expf(-2.0f * u));
+    }
+    default: return x;
+    }
+}
+
+template <int N>
+__device__ __forceinline__ void finish(const EpilogueArgs &g, float (&v)[N], const EpilogueInputs<N> &in)
+{
+    const Epilogue &e = g.e;
+    if (e.bias)
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            v[k] += in.bias[k];
+    if (e.activation)
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            v[k] = activate(v[k], e.activation);
+    if (e.gate)
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            v[k] *= in.gate[k];
+    if (e.residual)
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            v[k] += in.residual[k];
+}
+
 // Store four adjacent outputs C[row][col..col+3] (FP32 -> BF16).
-__device__ __forceinline__ void store_c4(const GemmArgs &g, f32x4_t v, uint32_t row,
-                                         uint32_t col)
+__device__ __forceinline__ void store_c4(const GemmArgs &g, f32x4_t v, uint32_t row, uint32_t col,
+                                         NoInputs = {})
 {
     if (row >= g.m || col >= g.n)
         return;
@@ -172,6 +267,61 @@ __device__ __forceinline__ void store_c4(const GemmArgs &g, f32x4_t v, uint32_t 
         if (col + 2 < g.n) dst[2] = (uint16_t)b2;
         if (col + 3 < g.n) dst[3] = (uint16_t)b3;
     }
+}
+
+__device__ __forceinline__ void store_c4(const EpilogueArgs &g, f32x4_t v, uint32_t row, uint32_t col,
+                                         const EpilogueInputs<4> &in)
+{
+    if (row >= g.m || col >= g.n)
+        return;
+    float x[4] = {v.x, v.y, v.z, v.w};
+    finish(g, x, in);
+    const size_t at = (size_t)row * g.c_stride + col;
+    const bool whole = (g.e.vec & kVecOut) && col + 3 < g.n;
+    if (g.e.out_f32) {
+        float *dst = reinterpret_cast<float *>(g.c) + at;
+        if (whole)
+            *reinterpret_cast<f32x4_t *>(dst) = f32x4_t{x[0], x[1], x[2], x[3]};
+        else
+#pragma unroll
+            for (uint32_t k = 0; k < 4; ++k)
+                if (col + k < g.n)
+                    dst[k] = x[k];
+        return;
+    }
+    uint16_t *dst = reinterpret_cast<uint16_t *>(g.c) + at;
+    if (whole) {
+        u32x2_t packed;
+        packed.x = f32_to_bf16_bits(x[0]) | (f32_to_bf16_bits(x[1]) << 16);
+        packed.y = f32_to_bf16_bits(x[2]) | (f32_to_bf16_bits(x[3]) << 16);
+        *reinterpret_cast<u32x2_t *>(dst) = packed;
+    } else {
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k)
+            if (col + k < g.n)
+                dst[k] = (uint16_t)f32_to_bf16_bits(x[k]);
+    }
+}
+
+// Store one output C[row][col].
+__device__ __forceinline__ void store_c1(const GemmArgs &g, float v, uint32_t row, uint32_t col, NoInputs)
+{
+    if (row < g.m && col < g.n)
+        reinterpret_cast<uint16_t *>(g.c)[(size_t)row * g.c_stride + col] = (uint16_t)f32_to_bf16_bits(v);
+}
+
+__device__ __forceinline__ void store_c1(const EpilogueArgs &g, float v, uint32_t row, uint32_t col,
+                                         const EpilogueInputs<1> &in)
+{
+    if (row >= g.m || col >= g.n)
+        return;
+    float x[1] = {v};
+    finish(g, x, in);
+    const size_t at = (size_t)row * g.c_stride + col;
+    if (g.e.out_f32)
+        reinterpret_cast<float *>(g.c)[at] = x[0];
+    else
+        reinterpret_cast<uint16_t *>(g.c)[at] = (uint16_t)f32_to_bf16_bits(x[0]);
 }
 
 }  // namespace dev

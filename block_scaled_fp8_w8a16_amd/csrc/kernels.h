@@ -25,6 +25,23 @@ struct GemmArgs {
     uint32_t m_tiles, n_tiles, splits, steps_per_split;
 };
 
+// What w8a16_gemm_epilogue does to a sum before it is stored.
+struct Epilogue {
+    const uint8_t *bias;        // [n], null: none
+    const uint8_t *gate;        // BF16 [m, gate_stride], null: none
+    const uint8_t *residual;    // [m, residual_stride], null: none
+    uint32_t gate_stride, residual_stride, activation;
+    uint32_t bias_f32, residual_f32, out_f32;    // FP32 rather than BF16
+    uint32_t vec;               // kVec* bits: four outputs' elements are one aligned piece
+};
+constexpr uint32_t kVecBias = 1, kVecGate = 2, kVecResidual = 4, kVecOut = 8;
+
+// Kernels are built for GemmArgs, and those a default plan can name for
+// EpilogueArgs as well.
+struct EpilogueArgs : GemmArgs {
+    Epilogue e;
+};
+
 // Up to W8A16_MAX_BATCH GEMMs in one grid of the stream kernel: problem i
 // owns logical workgroups start[i] .. start[i + 1] - 1 (start[0] == 0).
 struct BatchArgs {
@@ -81,6 +98,10 @@ inline hipError_t allow_lds(const void *kern, uint32_t bytes, uint32_t limit,
 }
 
 hipError_t launch_stream(const GemmArgs &g, const w8a16_plan_t &p, hipStream_t stream);
+// The same with an epilogue, of the variants that w8a16_plan() chooses.
+hipError_t launch_stream(const EpilogueArgs &g, const w8a16_plan_t &p, hipStream_t stream);
+hipError_t launch_ring(const EpilogueArgs &g, const w8a16_plan_t &p, hipStream_t stream);
+hipError_t launch_tile(const EpilogueArgs &g, const w8a16_plan_t &p, hipStream_t stream);
 hipError_t launch_act_quant(const QuantArgs &q, hipStream_t stream);
 // W8A8: g.a holds FP8 codes (g.a_stride in bytes), a_scales FP32 [m, k/128].
 hipError_t launch_w8a8(const GemmArgs &g, const float *a_scales, const w8a16_plan_t &p,
@@ -95,6 +116,8 @@ hipError_t launch_wide(const GemmArgs &g, const w8a16_plan_t &p, hipStream_t str
 // Adds the K splits of a tile plan's workspace ([splits][ws_rows][ws_cols]
 // FP32, whole tiles) in split order and stores C.
 hipError_t launch_split_reduce(const GemmArgs &g, uint32_t ws_cols, uint32_t ws_rows,
+                               hipStream_t stream);
+hipError_t launch_split_reduce(const EpilogueArgs &g, uint32_t ws_cols, uint32_t ws_rows,
                                hipStream_t stream);
 
 }  // namespace w8a16

@@ -125,8 +125,9 @@ __device__ __forceinline__ void wait_vm_ahead(uint32_t ahead)
 
 // NTW: the weight's DMA carries the non-temporal hint (one row tile reads
 // each weight byte once; the host picks the instance).
-template <int MT, int NT, int WST, int AST, int KH, bool PROD, bool NTW>
-__global__ __launch_bounds__(64 * (4 * KH + (PROD ? 2 : 0))) void w8a16_tile_kernel(GemmArgs g)
+// Args: GemmArgs, or EpilogueArgs.
+template <int MT, int NT, int WST, int AST, int KH, bool PROD, bool NTW, class Args>
+__global__ __launch_bounds__(64 * (4 * KH + (PROD ? 2 : 0))) void w8a16_tile_kernel(Args g)
 {
     constexpr int WAUX = NTW ? kNonTemporal : 0;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -369,11 +370,17 @@ __global__ __launch_bounds__(64 * (4 * KH + (PROD ? 2 : 0))) void w8a16_tile_ker
     const uint32_t row_off = (MT / 2) * wm + rr;
     const uint32_t col_off = (NT / 2) * wn + 4u * gq;
     if (g.splits == 1) {
+        // (a column block's inputs all before its first store)
 #pragma unroll
-        for (int j = 0; j < NBW; ++j)
+        for (int j = 0; j < NBW; ++j) {
+            decltype(load_inputs<4>(g, 0u, 0u)) in[MBW];
 #pragma unroll
             for (int b = 0; b < MBW; ++b)
-                store_c4(g, acc[j][b], m0 + row_off + 16u * b, n0 + col_off + 16u * j);
+                in[b] = load_inputs<4>(g, m0 + row_off + 16u * b, n0 + col_off + 16u * j);
+#pragma unroll
+            for (int b = 0; b < MBW; ++b)
+                store_c4(g, acc[j][b], m0 + row_off + 16u * b, n0 + col_off + 16u * j, in[b]);
+        }
         return;
     }
     // Workspace [splits][m_tiles * MT][n_tiles * NT] FP32, whole tiles.
@@ -387,15 +394,15 @@ __global__ __launch_bounds__(64 * (4 * KH + (PROD ? 2 : 0))) void w8a16_tile_ker
                                          col_off + 16u * j) = acc[j][b];
 }
 
-template <int MT, int NT, int WST, int AST, int KH, bool PROD, bool NTW>
-hipError_t launch_tile_n(const GemmArgs &g, const w8a16_plan_t &p, hipStream_t stream)
+template <int MT, int NT, int WST, int AST, int KH, bool PROD, bool NTW, class Args>
+hipError_t launch_tile_n(const Args &g, const w8a16_plan_t &p, hipStream_t stream)
 {
     if constexpr (!tile_variant_ok(MT / 16, NT / 16, WST, AST, 4 * KH + (PROD ? 2 : 0)) ||
                   !tile_depth_built(MT / 16, NT / 16, WST, AST)) {
         (void)g, (void)p, (void)stream;
         return hipErrorInvalidValue;
     } else {
-    auto kern = w8a16_tile_kernel<MT, NT, WST, AST, KH, PROD, NTW>;
+    auto kern = w8a16_tile_kernel<MT, NT, WST, AST, KH, PROD, NTW, Args>;
     static std::atomic<uint64_t> lds_set{0};
     hipError_t e = allow_lds(reinterpret_cast<const void *>(kern), p.lds_bytes, kMaxLdsBytes,
                              lds_set);
@@ -409,8 +416,8 @@ hipError_t launch_tile_n(const GemmArgs &g, const w8a16_plan_t &p, hipStream_t s
     }
 }
 
-template <int MT, int NT, int WST, int AST, int KH, bool PROD>
-hipError_t launch_tile_t(const GemmArgs &g, const w8a16_plan_t &p, hipStream_t stream)
+template <int MT, int NT, int WST, int AST, int KH, bool PROD, class Args>
+hipError_t launch_tile_t(const Args &g, const w8a16_plan_t &p, hipStream_t stream)
 {
     if (g.m_tiles == 1)
         return launch_tile_n<MT, NT, WST, AST, KH, PROD, true>(g, p, stream);

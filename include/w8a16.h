@@ -76,7 +76,7 @@ typedef enum w8a16_status {
 /* Diagnostics.  Two environment variables, read once per process at the
  * first call of an entry point that enqueues work (w8a16_gemm,
  * _gemm_planned, _gemm_noalloc, _gemm_batched, _act_quant_fp8,
- * _gemm_w8a8[_planned], _gemm_w4a4[_planned], _rope_table, _rope,
+ * _gemm_epilogue, _gemm_w8a8[_planned], _gemm_w4a4[_planned], _rope_table, _rope,
  * _rope_axes, _kv_append[_axes], _kv_attention); unset, empty or "0" is off,
  * "1" is on, and any other value makes each of those calls return
  * W8A16_ERR_ENV, before any other check, with the variable named in
@@ -587,6 +587,36 @@ int w8a16_kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seq
 int w8a16_plan_kv_attention(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_heads,
                             uint32_t kv_heads, uint32_t head_dim, uint32_t window,
                             uint32_t cu_count, w8a16_kv_plan_t *out);
+
+/* ---- Product with an epilogue ---------------------------------------------
+ *   c[i][j] = residual[i][j] + act(s + bias[j]) * gate[i][j]
+ * with s the FP32 sum that w8a16_gemm() rounds, everything after it in FP32,
+ * and one rounding to c's type; parts that are null are left out. */
+typedef enum w8a16_activation {
+    W8A16_ACT_NONE = 0,
+    W8A16_ACT_RELU = 1,
+    W8A16_ACT_SILU = 2,       /* x / (1 + exp(-x)) */
+    W8A16_ACT_GELU = 3,       /* x (1 + erf(x / sqrt 2)) / 2 */
+    W8A16_ACT_GELU_TANH = 4   /* x (1 + tanh(sqrt(2 / pi) (x + 0.044715 x^3))) / 2 */
+} w8a16_activation;
+
+typedef struct w8a16_epilogue {
+    const void *bias;         /* [n], contiguous */
+    const void *gate;         /* BF16 [m, gate_row_stride] */
+    const void *residual;     /* [m, residual_row_stride]; may be c, with c's type and stride */
+    uint32_t gate_row_stride, residual_row_stride;   /* in elements, at least n */
+    uint32_t activation;      /* w8a16_activation */
+    uint32_t bias_dtype, residual_dtype, out_dtype;  /* w8a16_dtype: W8A16_BF16 or W8A16_FP32 */
+} w8a16_epilogue_t;
+
+/* w8a16_gemm() with an epilogue: same operands, plan, workspace and checks,
+ * then W8A16_ERR_NULL_PTR (null epilogue), W8A16_ERR_SHAPE (an unknown
+ * activation or type) and W8A16_ERR_PITCH_TOO_SHORT (a stride below n).  c:
+ * [m, c_row_stride] of out_dtype, aligned to it like bias, gate and residual
+ * to theirs.  c must not overlap another operand, but for residual as above. */
+int w8a16_gemm_epilogue(const void *a, uint32_t a_row_stride, const void *w_fp8,
+                        const float *block_scale, void *c, uint32_t c_row_stride, uint32_t m,
+                        uint32_t n, uint32_t k, const w8a16_epilogue_t *epilogue, void *stream);
 
 /* Static text for a status code (never null). */
 const char *w8a16_status_string(int status);
