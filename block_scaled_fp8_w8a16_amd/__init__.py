@@ -24,7 +24,7 @@ from typing import Optional
 
 from . import attention as _attention
 from .attention import (KV_BLOCK, KV_KERNEL_ROWS, KV_KERNEL_TILE, KVCache, KVPlan, kv_append, kv_attention, kv_cache,
-                        plan_kv_attention, rope, rope_table)
+                        plan_kv_attention, plan_kv_shared, rope, rope_table)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libw8a16.so")
@@ -59,7 +59,8 @@ EXPORTS = ("w8a16_check_args", "w8a16_plan", "w8a16_plan_finalize", "w8a16_gemm"
            "w8a16_act_quant_fp8", "w8a16_plan_w8a8", "w8a16_gemm_w8a8",
            "w8a16_gemm_w8a8_planned", "w8a16_gemm_w4a4", "w8a16_plan_w4a4",
            "w8a16_gemm_w4a4_planned", "w8a16_rope_table", "w8a16_rope", "w8a16_rope_axes",
-           "w8a16_kv_append", "w8a16_kv_append_axes", "w8a16_kv_attention", "w8a16_plan_kv_attention", "w8a16_status_string",
+           "w8a16_kv_append", "w8a16_kv_append_axes", "w8a16_kv_attention",
+           "w8a16_kv_attention_span", "w8a16_plan_kv_shared", "w8a16_plan_kv_attention", "w8a16_status_string",
            "w8a16_last_error")
 
 MAX_BATCH = 8

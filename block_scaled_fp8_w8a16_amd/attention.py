@@ -86,6 +86,11 @@ class KVAttentionArgs(ctypes.Structure):
                 ("max_kv", _u32)]
 
 
+class KVSpan(ctypes.Structure):
+    """w8a16_kv_span_t"""
+    _fields_ = [("sinks", _u32), ("shared", _u32)]
+
+
 def declare(lib) -> None:
     """Argument types of the entry points."""
     ptr = ctypes.POINTER
@@ -97,9 +102,13 @@ def declare(lib) -> None:
     lib.w8a16_kv_append_axes.argtypes = [ptr(KVCacheDesc), ptr(KVSeqs), ptr(KVAppendArgs), ptr(Axes), _vp]
     lib.w8a16_kv_append.argtypes = [ptr(KVCacheDesc), ptr(KVSeqs), ptr(KVAppendArgs), _vp]
     lib.w8a16_kv_attention.argtypes = [ptr(KVCacheDesc), ptr(KVSeqs), ptr(KVAttentionArgs), _vp]
+    lib.w8a16_kv_attention_span.argtypes = [ptr(KVCacheDesc), ptr(KVSeqs), ptr(KVAttentionArgs), ptr(KVSpan),
+                                            _vp]
+    lib.w8a16_plan_kv_shared.argtypes = [_u32] * 9 + [ptr(KVPlan)] * 2
     lib.w8a16_plan_kv_attention.argtypes = [_u32] * 8 + [ptr(KVPlan)]
     for name in ("w8a16_rope_table", "w8a16_rope", "w8a16_rope_axes", "w8a16_kv_append",
-                 "w8a16_kv_append_axes", "w8a16_kv_attention", "w8a16_plan_kv_attention"):
+                 "w8a16_kv_append_axes", "w8a16_kv_attention", "w8a16_kv_attention_span",
+                 "w8a16_plan_kv_shared", "w8a16_plan_kv_attention"):
         getattr(lib, name).restype = ctypes.c_int
 
 
@@ -392,14 +401,18 @@ def kv_append(cache, k, v, block_table, kv_lens, *, cu_seqlens=None, max_new: Op
 
 def kv_attention(q, cache, block_table, kv_lens, out=None, *, cu_seqlens=None,
                  max_new: Optional[int] = None, max_kv: Optional[int] = None,
-                 scale: Optional[float] = None, causal: bool = True, window: int = 0,
-                 return_lse: bool = False, plan_: Optional[KVPlan] = None, stream=None):
+                 scale: Optional[float] = None, causal: bool = True, window: int = 0, sinks: int = 0,
+                 shared: int = 0, return_lse: bool = False, plan_: Optional[KVPlan] = None, stream=None):
     """Attention of the new tokens' queries q [tokens, q_heads, head_dim]
     (bfloat16 or float16) over `cache`.  block_table, kv_lens, cu_seqlens and
     max_new as for kv_append (which has stored the new tokens before);
     max_kv: at least the largest of kv_lens, for the launch's shape (None:
     what the block table can hold).  scale: None for 1 / sqrt(head_dim).
-    window: keys a query sees at most, itself counted (0: all).  Returns
+    window: keys a query sees at most, itself counted (0: all).  sinks: the
+    first tokens that stay visible behind a window.  shared: tokens that all
+    sequences start with, on the same pages (the block table's rows agree on
+    them): whole pages of them are read once for the batch where that pays;
+    results are the same up to the order of additions.  Returns
     out, or (out, lse) with lse float32 [tokens, q_heads]."""
     lib, torch, dtypes, check, raw = _setup()
     desc = _cache_desc(cache)
@@ -418,15 +431,18 @@ def kv_attention(q, cache, block_table, kv_lens, out=None, *, cu_seqlens=None,
         with _on(torch, stream):
             lse = q.new_empty((tokens, heads), dtype=torch.float32)
         lp = lse.data_ptr()
-    if window < 0:
-        raise ValueError("window must not be negative")
+    if window < 0 or sinks < 0 or shared < 0:
+        raise ValueError("window, sinks and shared must not be negative")
     seqs = _seqs_desc(torch.int32, block_table, kv_lens, cu_seqlens, tokens, max_new)
     args = KVAttentionArgs(q.data_ptr(), out.data_ptr(), lp, qt, qh, ot, oh,
                            None if plan_ is None else ctypes.pointer(plan_),
                            dim ** -0.5 if scale is None else scale, heads, dtypes[dtype], causal,
                            window, max_kv or 0)
-    st = lib.w8a16_kv_attention(desc, seqs, args,
-                                raw(q.get_device()) if stream is None else stream.cuda_stream)
+    queue = raw(q.get_device()) if stream is None else stream.cuda_stream
+    if sinks or shared:
+        st = lib.w8a16_kv_attention_span(desc, seqs, args, KVSpan(min(sinks, 1 << 30), min(shared, 1 << 30)), queue)
+    else:
+        st = lib.w8a16_kv_attention(desc, seqs, args, queue)
     if st:
         check(st)
     return (out, lse) if return_lse else out
@@ -440,3 +456,15 @@ def plan_kv_attention(seqs: int, max_new: int, max_kv: int, q_heads: int, kv_hea
     _raise_if(library().w8a16_plan_kv_attention(seqs, max_new, max_kv, q_heads, kv_heads, head_dim,
                                                 window, cu_count, ctypes.byref(p)))
     return p
+
+
+def plan_kv_shared(seqs: int, tokens: int, max_new: int, max_kv: int, shared: int, q_heads: int,
+                   kv_heads: int, head_dim: int, cu_count: int = 0):
+    """Default plans of kv_attention over a shared part of whole pages: (the
+    pass over it, the pass over the sequences' own keys), or (None, plan)
+    where one pass over everything is as fast (no GPU call)."""
+    from . import _raise_if, library
+    first, own = KVPlan(), KVPlan()
+    _raise_if(library().w8a16_plan_kv_shared(seqs, tokens, max_new, max_kv, shared, q_heads, kv_heads,
+                                             head_dim, cu_count, ctypes.byref(first), ctypes.byref(own)))
+    return (first if first.grid else None), own

@@ -123,6 +123,25 @@ struct AttnArgs {
     uint32_t fill_tokens;      // that one of their waves takes (at most 64)
 };
 
+// A window beside which the first tokens stay visible.
+struct SinkArgs : AttnArgs {
+    uint32_t sinks;            // at least 1
+};
+
+// The two passes over a cache whose sequences share their first `shared`
+// tokens (a multiple of the block): all rows of the call over those, as if
+// of one sequence, then each sequence over its own.  The first leaves its
+// chunks' partial rows for the second's join.
+struct PrefixArgs : AttnArgs {
+    uint32_t shared;
+};
+struct SuffixArgs : AttnArgs {
+    uint32_t shared;
+    const float *prefix;       // partial rows [(head, row tile)][chunk][row][dim], then their statistics
+    uint32_t prefix_tiles, prefix_chunks, prefix_shift;    // row tiles, of 2^shift rows
+    uint64_t prefix_rows;      // partial rows in all
+};
+
 constexpr uint32_t kKvTile = 64;                // keys per tile
 
 hipError_t launch_rope_table(const w8a16_rope_config_t &c, float *table, uint32_t positions,
@@ -133,17 +152,22 @@ hipError_t launch_kv_append(const AppendArgs &a, uint32_t dtype, hipStream_t str
 hipError_t launch_kv_append_axes(const AppendAxesArgs &a, uint32_t dtype, hipStream_t stream);
 // Workgroups of the attention's launch: the plan's and, where offsets are
 // given, those of the tokens outside them.
+inline uint64_t kv_launch_groups(const PrefixArgs &a, uint32_t) { return a.grid; }
 inline uint64_t kv_launch_groups(const AttnArgs &a, uint32_t waves)
 {
     const uint32_t tokens = a.fill_tokens * waves;
     return (uint64_t)a.grid + (a.seqs.cu ? (a.seqs.tokens + tokens - 1) / tokens : 0u);
 }
-hipError_t launch_kv_rows(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t dtype,
-                          hipStream_t stream);
-hipError_t launch_kv_tile(const AttnArgs &a, uint32_t dtype, hipStream_t stream);
+// Args: AttnArgs, SinkArgs, PrefixArgs or SuffixArgs (defined in
+// kv_attention.hip, kv_attention_sinks.hip, kv_attention_shared.hip; the tile
+// kernel's in kv_tile*.hip).
+template <class Args>
+hipError_t launch_kv_rows(const Args &a, const w8a16_kv_plan_t &p, uint32_t dtype, hipStream_t stream);
+template <class Args> hipError_t launch_kv_tile(const Args &a, uint32_t dtype, hipStream_t stream);
 // Adds the chunks' partial results of the tile kernel; max_rows: rows of the
-// longest sequence.
-hipError_t launch_kv_join(const AttnArgs &a, const w8a16_kv_plan_t &p, uint32_t max_rows,
-                          uint32_t dtype, hipStream_t stream);
+// longest sequence.  (Not PrefixArgs.)
+template <class Args>
+hipError_t launch_kv_join(const Args &a, const w8a16_kv_plan_t &p, uint32_t max_rows, uint32_t dtype,
+                          hipStream_t stream);
 
 }  // namespace w8a16

@@ -6,6 +6,7 @@
 #include <cstdio>
 #include <cstring>
 #include <exception>
+#include <type_traits>
 
 #include "attention.h"
 #include "host.h"
@@ -455,10 +456,31 @@ int kv_append(const char *entry, const w8a16_kv_cache_t *cache, const w8a16_kv_s
     return named(launched(stream), entry);
 }
 
-int kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
-                 const w8a16_kv_attention_args_t *g, hipStream_t stream)
+// The launches of one plan's attention.
+template <class Args>
+hipError_t launch_attention(const Args &a, const w8a16_kv_plan_t &p, uint32_t max_rows, uint32_t dtype,
+                            hipStream_t stream)
 {
-    const char *entry = "w8a16_kv_attention";
+    if (p.kernel == W8A16_KV_ROWS)
+        return launch_kv_rows(a, p, dtype, stream);
+    hipError_t e = launch_kv_tile(a, dtype, stream);
+    if constexpr (!std::is_same<Args, PrefixArgs>::value)
+        if (e == hipSuccess && (p.chunks > 1 || std::is_same<Args, SuffixArgs>::value))
+            e = launch_kv_join(a, p, max_rows, dtype, stream);
+    return e;
+}
+
+void fill_plan(AttnArgs &a, const w8a16_kv_plan_t &p)
+{
+    a.grid = p.grid;
+    a.row_tiles = p.row_tiles;
+    a.chunks = p.chunks;
+    a.chunk_tiles = p.chunk_tiles;
+}
+
+int kv_attention(const char *entry, const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
+                 const w8a16_kv_attention_args_t *g, const w8a16_kv_span_t &span, hipStream_t stream)
+{
     int st = check_levers(entry);
     if (st != W8A16_OK)
         return st;
@@ -501,21 +523,29 @@ int kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
     if (st != W8A16_OK)
         return named(st, entry);
     const uint32_t window = g->window < 0x7fffffffu ? g->window : 0;
-    w8a16_kv_plan_t p;
-    if (g->plan) {
+    const uint32_t sinks = !window ? 0 : span.sinks < (1u << 30) ? span.sinks : 1u << 30;
+    // whole pages that all sequences hold (a window is not worth two passes)
+    uint32_t shared = span.shared < max_kv ? span.shared : max_kv;
+    shared = window ? 0 : shared / cache->page_size * cache->page_size;
+    w8a16_kv_plan_t p, first;
+    if (shared) {
+        st = make_kv_shared_plans(seqs->seqs, seqs->tokens, seqs->max_new, max_kv, shared, g->q_heads,
+                                  cache->kv_heads, cache->head_dim, cus, g->plan, &first, &p);
+        shared = first.grid ? shared : 0;
+    } else if (g->plan) {
         p = *g->plan;
         st = kv_plan_finalize(seqs->seqs, seqs->max_new, max_kv, g->q_heads, cache->kv_heads,
-                              cache->head_dim, window, &p);
+                              cache->head_dim, window, &p, sinks);
     } else {
         st = make_kv_plan(seqs->seqs, seqs->max_new, max_kv, g->q_heads, cache->kv_heads,
-                          cache->head_dim, window, cus, &p);
+                          cache->head_dim, window, cus, &p, sinks);
     }
     if (st != W8A16_OK)
         return st;
-    AttnArgs a;
+    SuffixArgs a;
     std::memset(static_cast<void *>(&a), 0, sizeof a);
     a.seqs = seqs_of(*seqs);
-    a.grid = p.grid;
+    fill_plan(a, p);
     // (a long token axis by some 512 workgroups)
     const uint32_t fill = seqs->tokens / (512u * p.waves) + 1;
     a.fill_tokens = fill < 64u ? fill : 64u;
@@ -525,8 +555,8 @@ int kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
     if (p.workspace_bytes) {
         w8a16_plan_t need;
         std::memset(&need, 0, sizeof need);
-        need.workspace_bytes = p.workspace_bytes;
-        if (p.kernel == W8A16_KV_ROWS)
+        need.workspace_bytes = p.workspace_bytes + (shared ? first.workspace_bytes : 0);
+        if (p.kernel == W8A16_KV_ROWS && p.chunks > 1)
             need.counter_count = p.grid / p.chunks * kKvCounterStride;
         Workspace ws;
         st = get_workspace(dev, stream, need, &ws);
@@ -549,25 +579,51 @@ int kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
     a.q_heads = g->q_heads;
     a.causal = g->causal != 0;
     a.window = window;
-    a.row_tiles = p.row_tiles;
-    a.chunks = p.chunks;
-    a.chunk_tiles = p.chunk_tiles;
-    e = p.kernel == W8A16_KV_ROWS ? launch_kv_rows(a, p, g->dtype, stream)
-                                  : launch_kv_tile(a, g->dtype, stream);
-    if (e == hipSuccess && p.kernel == W8A16_KV_TILE && p.chunks > 1)
-        e = launch_kv_join(a, p, seqs->max_new * group, g->dtype, stream);
+    const uint32_t max_rows = seqs->max_new * group;
+    if (shared) {
+        PrefixArgs b;
+        static_cast<AttnArgs &>(b) = a;
+        fill_plan(b, first);
+        b.ws = a.ws + p.workspace_bytes / sizeof(float);
+        b.shared = a.shared = shared;
+        a.prefix = b.ws;
+        a.prefix_tiles = first.row_tiles;
+        a.prefix_chunks = first.chunks;
+        a.prefix_shift = first.row_blocks == 1 ? 4 : 7;
+        a.prefix_rows = (uint64_t)first.grid << a.prefix_shift;
+        e = launch_attention(b, first, 0, g->dtype, stream);
+        if (e == hipSuccess)
+            e = launch_attention(a, p, max_rows, g->dtype, stream);
+    } else if (sinks) {
+        SinkArgs b;
+        static_cast<AttnArgs &>(b) = a;
+        b.sinks = sinks;
+        e = launch_attention(b, p, max_rows, g->dtype, stream);
+    } else {
+        e = launch_attention(static_cast<const AttnArgs &>(a), p, max_rows, g->dtype, stream);
+    }
     if (e != hipSuccess)
         return named(hip_fail(e, "kernel launch"), entry);
     if (log_enabled()) {
-        char line[320];
-        snprintf(line, sizeof line,
-                 "w8a16: %s tokens=%u seqs=%u q_heads=%u kv_heads=%u head_dim=%u max_new=%u max_kv=%u "
-                 "window=%u: kernel=%s row_blocks=%u row_tiles=%u chunks=%u (%u tiles each) grid=%u "
-                 "workspace=%llu%s\n", entry, seqs->tokens, seqs->seqs, g->q_heads, cache->kv_heads,
-                 cache->head_dim, seqs->max_new, max_kv, window,
-                 p.kernel == W8A16_KV_ROWS ? "kv-rows" : "kv-tile", p.row_blocks, p.row_tiles, p.chunks,
-                 p.chunk_tiles, p.grid, (unsigned long long)p.workspace_bytes,
-                 g->plan ? ": caller's plan" : "");
+        char line[512];
+        int n = snprintf(line, sizeof line,
+                         "w8a16: %s tokens=%u seqs=%u q_heads=%u kv_heads=%u head_dim=%u max_new=%u max_kv=%u "
+                         "window=%u", entry, seqs->tokens, seqs->seqs, g->q_heads, cache->kv_heads,
+                         cache->head_dim, seqs->max_new, max_kv, window);
+        if (sinks)
+            n += snprintf(line + n, sizeof line - n, " sinks=%u", sinks);
+        auto plan = [&](const w8a16_kv_plan_t &x) {
+            n += snprintf(line + n, sizeof line - n,
+                          ": kernel=%s row_blocks=%u row_tiles=%u chunks=%u (%u tiles each) grid=%u workspace=%llu",
+                          x.kernel == W8A16_KV_ROWS ? "kv-rows" : "kv-tile", x.row_blocks, x.row_tiles,
+                          x.chunks, x.chunk_tiles, x.grid, (unsigned long long)x.workspace_bytes);
+        };
+        if (shared) {
+            n += snprintf(line + n, sizeof line - n, " shared=%u", shared);
+            plan(first);
+        }
+        plan(p);
+        snprintf(line + n, sizeof line - n, "%s\n", g->plan ? ": caller's plan" : "");
         log_line(line);
     }
     return named(launched(stream), entry);
@@ -655,7 +711,17 @@ int w8a16_kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seq
                        const w8a16_kv_attention_args_t *args, void *stream)
 {
     return w8a16::guarded("w8a16_kv_attention", [&] {
-        return w8a16::kv_attention(cache, seqs, args, static_cast<hipStream_t>(stream));
+        return w8a16::kv_attention("w8a16_kv_attention", cache, seqs, args, w8a16_kv_span_t{},
+                                   static_cast<hipStream_t>(stream));
+    });
+}
+
+int w8a16_kv_attention_span(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
+                            const w8a16_kv_attention_args_t *args, const w8a16_kv_span_t *span, void *stream)
+{
+    return w8a16::guarded("w8a16_kv_attention_span", [&] {
+        return w8a16::kv_attention("w8a16_kv_attention_span", cache, seqs, args, span ? *span : w8a16_kv_span_t{},
+                                   static_cast<hipStream_t>(stream));
     });
 }
 

@@ -4,8 +4,11 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "attention.h"
 #include "device_common.h"
+#include "rope_device.h"
 
 namespace w8a16 {
 namespace dev {
@@ -155,6 +158,55 @@ __device__ __forceinline__ bool seq_extent(const KvSeqs &s, uint32_t b, RowTile 
     return t.first <= s.tokens && end <= s.tokens && end >= t.first;
 }
 
+// The workgroup's sequence; the first pass over a shared prefix takes all of
+// the call's tokens for one.
+__device__ __forceinline__ bool extent(const AttnArgs &a, uint32_t b, RowTile &t)
+{
+    return seq_extent(a.seqs, b, t);
+}
+
+__device__ __forceinline__ bool extent(const PrefixArgs &a, uint32_t, RowTile &t)
+{
+    t.first = 0;
+    t.count = a.seqs.tokens;
+    t.kv_len = (int32_t)a.shared;
+    t.base = 0;
+    return true;
+}
+
+__device__ __forceinline__ uint32_t sequences(const AttnArgs &a) { return a.seqs.seqs; }
+__device__ __forceinline__ uint32_t sequences(const PrefixArgs &) { return 1; }
+
+// The row of the block table that leads to the keys: for a shared prefix
+// that of a sequence which holds all of it, else (every row then sees less
+// of it) of the longest.
+__device__ __forceinline__ uint32_t table_row(const AttnArgs &, uint32_t b) { return b; }
+
+__device__ __forceinline__ uint32_t table_row(const PrefixArgs &a, uint32_t)
+{
+    const uint32_t lane = threadIdx.x & 63u;
+    int32_t most = -1;
+    uint32_t longest = 0;
+    for (uint32_t b0 = 0; b0 < a.seqs.seqs; b0 += 64u) {
+        const int32_t len = b0 + lane < a.seqs.seqs ? a.seqs.kv_lens[b0 + lane] : -1;
+        const uint64_t whole = __ballot(len >= (int32_t)a.shared);
+        if (whole)
+            return __builtin_amdgcn_readfirstlane(b0 + (uint32_t)__builtin_ctzll(whole));
+        if (len > most) {
+            most = len;
+            longest = b0 + lane;
+        }
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+        const int32_t len = __shfl_xor(most, off, 64);
+        const uint32_t b = __shfl_xor(longest, off, 64);
+        longest = len > most || (len == most && b < longest) ? b : longest;
+        most = len > most ? len : most;
+    }
+    return __builtin_amdgcn_readfirstlane(longest);
+}
+
 __device__ __forceinline__ void tile_range(const AttnArgs &a, uint32_t tile_rows, RowTile &t)
 {
     const uint32_t last = t.row0 + tile_rows < t.rows ? t.row0 + tile_rows : t.rows;
@@ -180,8 +232,97 @@ __device__ __forceinline__ void row_range(const AttnArgs &a, const RowTile &t, u
     lo = a.window && p >= (int32_t)a.window ? p - (int32_t)a.window + 1 : 0;
 }
 
+__device__ __forceinline__ void row_range(const PrefixArgs &a, const RowTile &t, uint32_t row, int32_t &lo,
+                                          int32_t &hi)
+{
+    lo = hi = 0;
+    if (row >= t.rows)
+        return;
+    uint32_t b;
+    int32_t p;
+    if (!token_place(a.seqs, a.by_group.div(row), b, p))
+        return;
+    const int32_t len = a.causal ? p + 1 : a.seqs.kv_lens[b];
+    hi = len < (int32_t)a.shared ? len : (int32_t)a.shared;
+}
+
+// (all lanes of the wave together)
+__device__ __forceinline__ void tile_range(const PrefixArgs &a, uint32_t tile_rows, RowTile &t)
+{
+    int32_t most = 0, least = (int32_t)a.shared;
+    for (uint32_t r = threadIdx.x & 63u; r < tile_rows && t.row0 + r < t.rows; r += 64u) {
+        int32_t lo, hi;
+        row_range(a, t, t.row0 + r, lo, hi);
+        most = hi > most ? hi : most;
+        least = hi < least ? hi : least;
+    }
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+        const int32_t x = __shfl_xor(most, off, 64), y = __shfl_xor(least, off, 64);
+        most = x > most ? x : most;
+        least = y < least ? y : least;
+    }
+    t.lo = t.all_lo = 0;
+    t.hi = __builtin_amdgcn_readfirstlane(most);
+    t.all_hi = __builtin_amdgcn_readfirstlane(least);
+}
+
+__device__ __forceinline__ void row_range(const SuffixArgs &a, const RowTile &t, uint32_t row, int32_t &lo,
+                                          int32_t &hi)
+{
+    row_range(static_cast<const AttnArgs &>(a), t, row, lo, hi);
+    lo = (int32_t)a.shared;
+}
+
+__device__ __forceinline__ void tile_range(const SuffixArgs &a, uint32_t tile_rows, RowTile &t)
+{
+    tile_range(static_cast<const AttnArgs &>(a), tile_rows, t);
+    t.lo = t.all_lo = (int32_t)a.shared;
+    t.hi = t.hi > t.lo ? t.hi : t.lo;
+}
+
+// First tokens that rows see besides their range (no further than it ends),
+// and their tiles in front of a row tile's range.
+__device__ __forceinline__ int32_t sinks_of(const AttnArgs &) { return 0; }
+__device__ __forceinline__ int32_t sinks_of(const SinkArgs &a) { return (int32_t)a.sinks; }
+
+template <class Args> constexpr bool has_sinks = std::is_same<Args, SinkArgs>::value;
+template <class Args> constexpr bool is_prefix = std::is_same<Args, PrefixArgs>::value;
+template <class Args> constexpr bool is_suffix = std::is_same<Args, SuffixArgs>::value;
+
+// The tiles a row tile goes over, numbered from 0: those of its sinks, as far
+// as they lie before its range, then its range's.
+struct TileList {
+    uint32_t front, tile0, tiles;
+    template <class Args> __device__ __forceinline__ TileList(const Args &a, const RowTile &t)
+    {
+        tile0 = (uint32_t)t.lo / kKvTile;
+        front = 0;
+        if constexpr (has_sinks<Args>) {
+            const uint32_t n = (a.sinks - 1u) / kKvTile + 1u;
+            front = n < tile0 ? n : tile0;
+        }
+        tiles = ((uint32_t)t.hi + kKvTile - 1) / kKvTile - tile0 + front;
+    }
+    __device__ __forceinline__ uint32_t at(uint32_t n) const { return n < front ? n : n - front + tile0; }
+};
+
+// Where the first pass has left the partial row of row `row` of the call
+// (token * group + head of the group) and chunk c of the prefix.
+template <class Args>
+__device__ __forceinline__ size_t prefix_partial(const Args &a, uint32_t head, uint32_t row, uint32_t c)
+{
+    if constexpr (is_suffix<Args>) {
+        const uint32_t tile = row >> a.prefix_shift;
+        return ((((size_t)head * a.prefix_tiles + tile) * a.prefix_chunks + c) << a.prefix_shift) +
+               (row - (tile << a.prefix_shift));
+    }
+    return 0;
+}
+
 // (Such a row gives zeros.  One whose visible scores are all -inf sums to
 // zero too, and has no softmax: its 0 / 0 stays.)
+// (Over a shared prefix: whatever part of the keys a pass takes.)
 __device__ __forceinline__ bool sees_nothing(const AttnArgs &a, const RowTile &t, uint32_t row)
 {
     int32_t lo, hi;

@@ -16,12 +16,29 @@ constexpr uint64_t kCutTiles = 10;     // that a cut has to spare, and one more
 
 uint64_t div_up(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
+// The tiles a row tile can see: all of the cache, or the window's, those its
+// rows' positions add, and the sinks'; at least one.
+uint64_t tiles_of(uint32_t max_new, uint32_t max_kv, uint32_t window, uint32_t sinks)
+{
+    uint64_t keys = max_kv;
+    if (window && (uint64_t)window + max_new < keys)
+        keys = (uint64_t)window + max_new;
+    uint64_t tiles = div_up(keys, kKeysPerTile) + (window ? 1 : 0);
+    if (window && sinks) {
+        tiles += div_up(sinks, kKeysPerTile);
+        const uint64_t all = div_up(max_kv, kKeysPerTile);
+        tiles = tiles < all ? tiles : all;
+    }
+    return tiles < 1 ? 1 : tiles;
+}
+
 }  // namespace
 
 // Fills the derived fields of a plan whose kernel, row_blocks and
 // chunk_tiles are set, or refuses it.
 int kv_plan_finalize(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_heads,
-                     uint32_t kv_heads, uint32_t head_dim, uint32_t window, w8a16_kv_plan_t *p)
+                     uint32_t kv_heads, uint32_t head_dim, uint32_t window, w8a16_kv_plan_t *p,
+                     uint32_t sinks)
 {
     const bool rows_ok = p->kernel == W8A16_KV_ROWS && p->row_blocks == 1 &&
                          (p->waves == 4 || (p->waves == 8 && head_dim <= 128));
@@ -31,15 +48,8 @@ int kv_plan_finalize(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t 
                                         "row_blocks 1 and 4 waves (or 8, of heads up to 128), or "
                                         "W8A16_KV_TILE with row_blocks 8 and 4 waves, and "
                                         "chunk_tiles of at least 1");
-    // the tiles a row tile can see: all of the cache, or the window's and
-    // those its rows' positions add
     const uint64_t tile_rows = 16ull * p->row_blocks, rows = (uint64_t)max_new * (q_heads / kv_heads);
-    uint64_t keys = max_kv;
-    if (window && (uint64_t)window + max_new < keys)
-        keys = (uint64_t)window + max_new;
-    uint64_t tiles = div_up(keys, kKeysPerTile) + (window ? 1 : 0);
-    if (tiles < 1)
-        tiles = 1;
+    const uint64_t tiles = tiles_of(max_new, max_kv, window, sinks);
     const uint64_t row_tiles = div_up(rows, tile_rows), chunks = div_up(tiles, p->chunk_tiles);
     const uint64_t grid = (uint64_t)seqs * kv_heads * row_tiles * chunks;
     if (grid * 64ull * p->waves > kMaxThreads)
@@ -59,7 +69,7 @@ int kv_plan_finalize(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t 
 
 int make_kv_plan(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_heads,
                  uint32_t kv_heads, uint32_t head_dim, uint32_t window, uint32_t cu_count,
-                 w8a16_kv_plan_t *out)
+                 w8a16_kv_plan_t *out, uint32_t sinks)
 {
     if (!out)
         return fail(W8A16_ERR_NULL_PTR, "w8a16_plan_kv_attention: null plan");
@@ -95,13 +105,10 @@ int make_kv_plan(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_he
     p.row_blocks = p.kernel == W8A16_KV_ROWS ? 1 : 8;
     p.waves = 4;
     p.chunk_tiles = 1u << 30;
-    int st = kv_plan_finalize(seqs, max_new, max_kv, q_heads, kv_heads, head_dim, window, &p);
+    int st = kv_plan_finalize(seqs, max_new, max_kv, q_heads, kv_heads, head_dim, window, &p, sinks);
     if (st != W8A16_OK)
         return st;
-    uint64_t tiles = div_up(window && (uint64_t)window + max_new < max_kv
-                                ? (uint64_t)window + max_new : max_kv, kKeysPerTile) + (window ? 1 : 0);
-    if (tiles < 1)
-        tiles = 1;
+    const uint64_t tiles = tiles_of(max_new, max_kv, window, sinks);
     // Cut the keys while that leaves no more workgroups than run at once: two
     // per CU, one of 8 waves or of heads above 128 channels.  Eight waves
     // where the row tiles alone do not give every CU a workgroup: half as
@@ -137,14 +144,85 @@ int make_kv_plan(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_he
     if (per + join >= tiles)
         per = tiles;
     p.chunk_tiles = (uint32_t)per;
-    st = kv_plan_finalize(seqs, max_new, max_kv, q_heads, kv_heads, head_dim, window, &p);
+    st = kv_plan_finalize(seqs, max_new, max_kv, q_heads, kv_heads, head_dim, window, &p, sinks);
     if (st != W8A16_OK)
         return st;
     *out = p;
     return W8A16_OK;
 }
 
+namespace {
+
+// A join takes both passes' chunks of a row tile.
+constexpr uint64_t kMaxPassChunks = kKvMaxChunks / 2;
+
+// A pass's plan over `keys` keys, with room for its partial rows; `given`
+// (null: none) in place of the default.
+int pass_plan(uint32_t seqs, uint32_t max_new, uint32_t keys, uint32_t q_heads, uint32_t kv_heads,
+              uint32_t head_dim, uint32_t cu_count, const w8a16_kv_plan_t *given, w8a16_kv_plan_t *p)
+{
+    int st;
+    if (given) {
+        *p = *given;
+        st = kv_plan_finalize(seqs, max_new, keys, q_heads, kv_heads, head_dim, 0, p);
+    } else {
+        st = make_kv_plan(seqs, max_new, keys, q_heads, kv_heads, head_dim, 0, cu_count, p);
+        if (st == W8A16_OK && p->chunks > kMaxPassChunks) {
+            p->chunk_tiles = (uint32_t)div_up(div_up(keys, kKeysPerTile), kMaxPassChunks);
+            st = kv_plan_finalize(seqs, max_new, keys, q_heads, kv_heads, head_dim, 0, p);
+        }
+    }
+    if (st != W8A16_OK)
+        return st;
+    if (p->chunks > kMaxPassChunks)
+        return fail(W8A16_ERR_BAD_PLAN, "w8a16_kv_attention: behind a shared part a plan may have at most "
+                                        "64 chunks");
+    p->workspace_bytes = (uint64_t)p->grid * 16 * p->row_blocks * (head_dim + 4) * 4;
+    return W8A16_OK;
+}
+
+}  // namespace
+
+int make_kv_shared_plans(uint32_t seqs, uint32_t tokens, uint32_t max_new, uint32_t max_kv,
+                         uint32_t shared, uint32_t q_heads, uint32_t kv_heads, uint32_t head_dim,
+                         uint32_t cu_count, const w8a16_kv_plan_t *given, w8a16_kv_plan_t *prefix,
+                         w8a16_kv_plan_t *suffix)
+{
+    std::memset(prefix, 0, sizeof *prefix);
+    // (the second pass starts with the tile that the shared keys end in)
+    const uint32_t before = shared / (uint32_t)kKeysPerTile * (uint32_t)kKeysPerTile;
+    const uint32_t own = max_kv > before ? max_kv - before : 1u;
+    if (given || (shared && seqs > 1)) {
+        int st = pass_plan(1, tokens, shared, q_heads, kv_heads, head_dim, cu_count, nullptr, prefix);
+        if (st == W8A16_OK)
+            st = pass_plan(seqs, max_new, own, q_heads, kv_heads, head_dim, cu_count, given, suffix);
+        if (st == W8A16_OK || given)
+            return st;
+        std::memset(prefix, 0, sizeof *prefix);
+    }
+    return make_kv_plan(seqs, max_new, max_kv, q_heads, kv_heads, head_dim, 0, cu_count, suffix);
+}
+
 }  // namespace w8a16
+
+extern "C" int w8a16_plan_kv_shared(uint32_t seqs, uint32_t tokens, uint32_t max_new, uint32_t max_kv,
+                                    uint32_t shared, uint32_t q_heads, uint32_t kv_heads,
+                                    uint32_t head_dim, uint32_t cu_count, w8a16_kv_plan_t *prefix,
+                                    w8a16_kv_plan_t *own)
+{
+    using namespace w8a16;
+    if (!prefix || !own)
+        return fail(W8A16_ERR_NULL_PTR, "w8a16_plan_kv_shared: null plan");
+    w8a16_kv_plan_t p;
+    int st = make_kv_plan(seqs, max_new, max_kv, q_heads, kv_heads, head_dim, 0, cu_count, &p);
+    if (st == W8A16_OK && (tokens < max_new || shared > max_kv))
+        st = fail(W8A16_ERR_SHAPE, "w8a16_plan_kv_shared: tokens must be at least max_new, and shared at "
+                                   "most max_kv");
+    if (st != W8A16_OK)
+        return st;
+    return make_kv_shared_plans(seqs, tokens, max_new, max_kv, shared, q_heads, kv_heads, head_dim, cu_count,
+                                nullptr, prefix, own);
+}
 
 extern "C" int w8a16_plan_kv_attention(uint32_t seqs, uint32_t max_new, uint32_t max_kv,
                                        uint32_t q_heads, uint32_t kv_heads, uint32_t head_dim,

@@ -174,10 +174,20 @@ constexpr uint64_t kMaxThreads = (1ull << 32) - 1;
 constexpr uint32_t kKvMaxChunks = 128;
 constexpr uint32_t kKvCounterStride = 16;
 int kv_plan_finalize(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_heads,
-                     uint32_t kv_heads, uint32_t head_dim, uint32_t window, w8a16_kv_plan_t *p);
+                     uint32_t kv_heads, uint32_t head_dim, uint32_t window, w8a16_kv_plan_t *p,
+                     uint32_t sinks = 0);
 int make_kv_plan(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_heads,
                  uint32_t kv_heads, uint32_t head_dim, uint32_t window, uint32_t cu_count,
-                 w8a16_kv_plan_t *out);
+                 w8a16_kv_plan_t *out, uint32_t sinks = 0);
+// Attention over sequences that share their first `shared` tokens in two
+// passes: all tokens' rows over the shared keys, and each sequence over its
+// own.  Both always leave partial rows (workspace_bytes is set with one chunk
+// as well).  prefix->grid 0: one pass over everything is as fast (suffix then
+// is its plan).  With `given`, two passes, the second by that plan.
+int make_kv_shared_plans(uint32_t seqs, uint32_t tokens, uint32_t max_new, uint32_t max_kv,
+                         uint32_t shared, uint32_t q_heads, uint32_t kv_heads, uint32_t head_dim,
+                         uint32_t cu_count, const w8a16_kv_plan_t *given, w8a16_kv_plan_t *prefix,
+                         w8a16_kv_plan_t *suffix);
 // Replace the "w8a16_gemm" prefix of the last error by `name`.
 int fail_with_name(int status, const char *name);
 // Prefix the last error with "w8a16_gemm_batched: descriptor <index>: ".

@@ -77,7 +77,7 @@ typedef enum w8a16_status {
  * first call of an entry point that enqueues work (w8a16_gemm,
  * _gemm_planned, _gemm_noalloc, _gemm_batched, _act_quant_fp8,
  * _gemm_epilogue, _gemm_w8a8[_planned], _gemm_w4a4[_planned], _rope_table, _rope,
- * _rope_axes, _kv_append[_axes], _kv_attention); unset, empty or "0" is off,
+ * _rope_axes, _kv_append[_axes], _kv_attention[_span]); unset, empty or "0" is off,
  * "1" is on, and any other value makes each of those calls return
  * W8A16_ERR_ENV, before any other check, with the variable named in
  * w8a16_last_error().  The pure planning calls ignore them.
@@ -582,6 +582,36 @@ typedef struct w8a16_kv_attention_args {
  * of this file (growth is refused during capture). */
 int w8a16_kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
                        const w8a16_kv_attention_args_t *args, void *stream);
+
+/* What more of the cache is seen, and what of it is read once.
+ * sinks: the first tokens of a sequence that stay visible behind a window: a
+ *   row sees key j < kv_lens[b] (causal: j <= p) if j > p - window or
+ *   j < sinks.  Without a window it says nothing.
+ * shared: at least two sequences hold the same first `shared` tokens, on the
+ *   same pages: for every two of them, their rows of the block table agree on
+ *   the pages of the first min(shared, the shorter one's kv_lens) tokens.
+ *   The whole pages among them are read once for all rows where that pays.
+ *   Results are those without it, up to the order of additions.  With a
+ *   window it is not used.  A given plan is that of the second pass, over the
+ *   keys from the shared part's last 64-key tile on, and asks for two passes;
+ *   it may have 64 chunks. */
+typedef struct w8a16_kv_span {
+    uint32_t sinks, shared;
+} w8a16_kv_span_t;
+
+/* w8a16_kv_attention() with a span (null: none).  A call that reads a shared
+ * part once uses the workspace whatever its plan. */
+int w8a16_kv_attention_span(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seqs,
+                            const w8a16_kv_attention_args_t *args, const w8a16_kv_span_t *span,
+                            void *stream);
+
+/* Default plans of the attention over a shared part (whole pages): of the
+ * pass of all `tokens` rows over it, and of the pass over the sequences' own
+ * keys; prefix->grid 0 where one pass over everything, with the plan in *own,
+ * is as fast.  Pure: no GPU call. */
+int w8a16_plan_kv_shared(uint32_t seqs, uint32_t tokens, uint32_t max_new, uint32_t max_kv,
+                         uint32_t shared, uint32_t q_heads, uint32_t kv_heads, uint32_t head_dim,
+                         uint32_t cu_count, w8a16_kv_plan_t *prefix, w8a16_kv_plan_t *own);
 
 /* Default plan of the attention.  Pure: no GPU call. */
 int w8a16_plan_kv_attention(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_heads,
