@@ -22,7 +22,7 @@ SOURCES = ["plan.cpp", "api.hip", "stream_kernel.hip", "tile_m64.hip", "tile_m12
            "wide_kernel.hip", "split_reduce.hip", "ring_kernel.hip", "w8a8_kernel.hip",
            "w4a4_kernel.hip", "kv_plan.cpp", "attention_api.hip", "rope_kernel.hip",
            "kv_append.hip", "kv_append_axes.hip", "kv_attention.hip", "kv_tile_kernel.hip",
-           "kv_attention_sinks.hip", "kv_attention_shared.hip", "kv_tile_sinks.hip", "kv_tile_shared.hip"]
+           "kv_attention_sinks.hip", "kv_tile_sinks.hip", "kv_shared_kernel.hip"]
 HEADERS = ["plan.h", "kernels.h", "device_common.h", "tile_kernel.h", "host.h", "attention.h",
            "attention_device.h", "rope_device.h", "kv_append_kernel.h",
            "stream_kernel.h", "ring_kernel.h", "kv_rows_kernel.h", "kv_tile_kernel.h"]
@@ -42,8 +42,7 @@ EXTRA_FLAGS = {"tile_m64.hip": _VGPR_FORM, "tile_m128.hip": _VGPR_FORM,
                "tile_epilogue.hip": _VGPR_FORM,
                "w8a8_kernel.hip": _VGPR_FORM, "kv_attention.hip": _VGPR_FORM,
                "kv_tile_kernel.hip": _VGPR_FORM, "kv_attention_sinks.hip": _VGPR_FORM,
-               "kv_attention_shared.hip": _VGPR_FORM, "kv_tile_sinks.hip": _VGPR_FORM,
-               "kv_tile_shared.hip": _VGPR_FORM}
+               "kv_tile_sinks.hip": _VGPR_FORM, "kv_shared_kernel.hip": _VGPR_FORM}
 
 
 def _compile_cmd(src: str, obj: str) -> list:

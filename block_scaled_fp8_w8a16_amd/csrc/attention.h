@@ -152,22 +152,23 @@ hipError_t launch_kv_append(const AppendArgs &a, uint32_t dtype, hipStream_t str
 hipError_t launch_kv_append_axes(const AppendAxesArgs &a, uint32_t dtype, hipStream_t stream);
 // Workgroups of the attention's launch: the plan's and, where offsets are
 // given, those of the tokens outside them.
-inline uint64_t kv_launch_groups(const PrefixArgs &a, uint32_t) { return a.grid; }
 inline uint64_t kv_launch_groups(const AttnArgs &a, uint32_t waves)
 {
     const uint32_t tokens = a.fill_tokens * waves;
     return (uint64_t)a.grid + (a.seqs.cu ? (a.seqs.tokens + tokens - 1) / tokens : 0u);
 }
-// Args: AttnArgs, SinkArgs, PrefixArgs or SuffixArgs (defined in
-// kv_attention.hip, kv_attention_sinks.hip, kv_attention_shared.hip; the tile
-// kernel's in kv_tile*.hip).
+// Args: AttnArgs or SinkArgs (defined in kv_attention.hip and
+// kv_attention_sinks.hip; the tile kernel's in kv_tile*.hip).
 template <class Args>
 hipError_t launch_kv_rows(const Args &a, const w8a16_kv_plan_t &p, uint32_t dtype, hipStream_t stream);
 template <class Args> hipError_t launch_kv_tile(const Args &a, uint32_t dtype, hipStream_t stream);
 // Adds the chunks' partial results of the tile kernel; max_rows: rows of the
-// longest sequence.  (Not PrefixArgs.)
+// longest sequence.
 template <class Args>
 hipError_t launch_kv_join(const Args &a, const w8a16_kv_plan_t &p, uint32_t max_rows, uint32_t dtype,
                           hipStream_t stream);
+// Both passes over a shared prefix, and their join.
+hipError_t launch_kv_shared(const PrefixArgs &a, const w8a16_kv_plan_t &pa, const SuffixArgs &b,
+                            const w8a16_kv_plan_t &pb, uint32_t max_rows, uint32_t dtype, hipStream_t stream);
 
 }  // namespace w8a16

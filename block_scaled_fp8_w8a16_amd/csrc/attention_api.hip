@@ -6,7 +6,6 @@
 #include <cstdio>
 #include <cstring>
 #include <exception>
-#include <type_traits>
 
 #include "attention.h"
 #include "host.h"
@@ -464,10 +463,7 @@ hipError_t launch_attention(const Args &a, const w8a16_kv_plan_t &p, uint32_t ma
     if (p.kernel == W8A16_KV_ROWS)
         return launch_kv_rows(a, p, dtype, stream);
     hipError_t e = launch_kv_tile(a, dtype, stream);
-    if constexpr (!std::is_same<Args, PrefixArgs>::value)
-        if (e == hipSuccess && (p.chunks > 1 || std::is_same<Args, SuffixArgs>::value))
-            e = launch_kv_join(a, p, max_rows, dtype, stream);
-    return e;
+    return e == hipSuccess && p.chunks > 1 ? launch_kv_join(a, p, max_rows, dtype, stream) : e;
 }
 
 void fill_plan(AttnArgs &a, const w8a16_kv_plan_t &p)
@@ -549,14 +545,14 @@ int kv_attention(const char *entry, const w8a16_kv_cache_t *cache, const w8a16_k
     // (a long token axis by some 512 workgroups)
     const uint32_t fill = seqs->tokens / (512u * p.waves) + 1;
     a.fill_tokens = fill < 64u ? fill : 64u;
-    if (kv_launch_groups(a, p.waves) * 64ull * p.waves > kMaxThreads)
+    if ((kv_launch_groups(a, p.waves) + (shared ? first.grid : 0u)) * 64ull * p.waves > kMaxThreads)
         return refuse(W8A16_ERR_SHAPE, "%s: %u tokens of %u sequences are too many for one call", entry,
                       seqs->tokens, seqs->seqs);
     if (p.workspace_bytes) {
         w8a16_plan_t need;
         std::memset(&need, 0, sizeof need);
         need.workspace_bytes = p.workspace_bytes + (shared ? first.workspace_bytes : 0);
-        if (p.kernel == W8A16_KV_ROWS && p.chunks > 1)
+        if (p.kernel == W8A16_KV_ROWS && !shared)
             need.counter_count = p.grid / p.chunks * kKvCounterStride;
         Workspace ws;
         st = get_workspace(dev, stream, need, &ws);
@@ -591,9 +587,7 @@ int kv_attention(const char *entry, const w8a16_kv_cache_t *cache, const w8a16_k
         a.prefix_chunks = first.chunks;
         a.prefix_shift = first.row_blocks == 1 ? 4 : 7;
         a.prefix_rows = (uint64_t)first.grid << a.prefix_shift;
-        e = launch_attention(b, first, 0, g->dtype, stream);
-        if (e == hipSuccess)
-            e = launch_attention(a, p, max_rows, g->dtype, stream);
+        e = launch_kv_shared(b, first, a, p, max_rows, g->dtype, stream);
     } else if (sinks) {
         SinkArgs b;
         static_cast<AttnArgs &>(b) = a;

@@ -167,16 +167,19 @@ int pass_plan(uint32_t seqs, uint32_t max_new, uint32_t keys, uint32_t q_heads, 
         st = kv_plan_finalize(seqs, max_new, keys, q_heads, kv_heads, head_dim, 0, p);
     } else {
         st = make_kv_plan(seqs, max_new, keys, q_heads, kv_heads, head_dim, 0, cu_count, p);
-        if (st == W8A16_OK && p->chunks > kMaxPassChunks) {
-            p->chunk_tiles = (uint32_t)div_up(div_up(keys, kKeysPerTile), kMaxPassChunks);
+        if (st == W8A16_OK) {
+            p->waves = 4;
+            const uint64_t least = div_up(div_up(keys, kKeysPerTile), kMaxPassChunks);
+            if (p->chunk_tiles < least)
+                p->chunk_tiles = (uint32_t)least;
             st = kv_plan_finalize(seqs, max_new, keys, q_heads, kv_heads, head_dim, 0, p);
         }
     }
     if (st != W8A16_OK)
         return st;
-    if (p->chunks > kMaxPassChunks)
-        return fail(W8A16_ERR_BAD_PLAN, "w8a16_kv_attention: behind a shared part a plan may have at most "
-                                        "64 chunks");
+    if (p->chunks > kMaxPassChunks || p->waves != 4)
+        return fail(W8A16_ERR_BAD_PLAN, "w8a16_kv_attention: behind a shared part a plan has 4 waves and at "
+                                        "most 64 chunks");
     p->workspace_bytes = (uint64_t)p->grid * 16 * p->row_blocks * (head_dim + 4) * 4;
     return W8A16_OK;
 }
@@ -196,6 +199,13 @@ int make_kv_shared_plans(uint32_t seqs, uint32_t tokens, uint32_t max_new, uint3
         int st = pass_plan(1, tokens, shared, q_heads, kv_heads, head_dim, cu_count, nullptr, prefix);
         if (st == W8A16_OK)
             st = pass_plan(seqs, max_new, own, q_heads, kv_heads, head_dim, cu_count, given, suffix);
+        // (one tile kernel is enough: own rows that want it are the prefix's too)
+        if (st == W8A16_OK && suffix->kernel == W8A16_KV_TILE && prefix->kernel == W8A16_KV_ROWS) {
+            w8a16_kv_plan_t tiles = *prefix;
+            tiles.kernel = W8A16_KV_TILE;
+            tiles.row_blocks = 8;
+            st = pass_plan(1, tokens, shared, q_heads, kv_heads, head_dim, cu_count, &tiles, prefix);
+        }
         if (st == W8A16_OK || given)
             return st;
         std::memset(prefix, 0, sizeof *prefix);

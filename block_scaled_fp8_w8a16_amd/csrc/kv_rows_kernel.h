@@ -66,21 +66,34 @@ struct TileAt {
     bool ok;
 };
 
+// LDS of a workgroup.
+template <int DP, int WAVES> struct RowsLds {
+    static constexpr int SEG = DP % 128 || WAVES > 4 ? 64 : 128;    // channels joined at a time
+    static constexpr int PART = 16 * (SEG + 4);
+    float part[WAVES * PART];           // [wave][16][SEG + 4]
+    f32x4_t stat[WAVES][16];            // sum reference, l, output reference
+    float red[2 * 64 * WAVES];
+    uint32_t last;
+};
+
+// Workgroup `group_id` of a launch of a.grid.  Either pass over a shared prefix
+// leaves partial rows and no outputs.
 template <class Q, int DP, int WAVES, class Args>
-__global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w8a16_kv_rows_kernel(Args a)
+__device__ __forceinline__ void kv_rows(const Args &a, uint32_t group_id, RowsLds<DP, WAVES> &lds)
 {
+    auto &part = lds.part;
+    auto &stat = lds.stat;
+    auto &red = lds.red;
+    auto &last = lds.last;
+    constexpr bool PARTS = is_prefix<Args> || is_suffix<Args>;
     constexpr int QC = DP / 64;       // 64-channel groups of the first product
     constexpr int VT = DP / 16;       // 16-channel tiles of the second
     constexpr uint32_t THREADS = 64 * WAVES;
-    constexpr int SEG = DP % 128 || WAVES > 4 ? 64 : 128;    // channels joined at a time
+    constexpr int SEG = RowsLds<DP, WAVES>::SEG;
     static_assert(DP % SEG == 0, "the join's passes take whole output tiles");
     constexpr int NR = 16;            // rows
-    constexpr int PART = 16 * (SEG + 4);
+    constexpr int PART = RowsLds<DP, WAVES>::PART;
     static_assert(WAVES * PART >= (int)kKvMaxChunks * NR && WAVES * PART >= 4 * (int)THREADS, "LDS of the join");
-    __shared__ __attribute__((aligned(16))) float part[WAVES * PART];   // [wave][16][SEG + 4]
-    __shared__ f32x4_t stat[WAVES][NR];      // sum reference, l, output reference
-    __shared__ float red[2 * THREADS];
-    __shared__ uint32_t last;
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t col = lane & 15u, g = lane >> 4;
@@ -90,7 +103,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
     // fastest, a power of two of them would put each chunk on its own XCD,
     // and ragged lengths leave the later chunks empty
     const uint32_t groups = sequences(a) * pool.heads;
-    const uint32_t grp = blockIdx.x % groups, rest = blockIdx.x / groups;
+    const uint32_t grp = group_id % groups, rest = group_id / groups;
     const uint32_t rtile = rest % a.row_tiles, chunk = rest / a.row_tiles;
     const uint32_t head = grp % pool.heads, b = grp / pool.heads;
 
@@ -177,7 +190,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
     t.row0 = rtile * NR;
     if (t.row0 >= t.rows || extra) {
         if (extra)
-            fill_unowned<typename Q::elem>(a, blockIdx.x - a.grid, WAVES);
+            fill_unowned<typename Q::elem>(a, group_id - a.grid, WAVES);
         return;
     }
     tile_range(a, NR, t);
@@ -190,7 +203,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
     // the lengths have been too small
     const uint32_t end = chunk + 1 == a.chunks || begin + a.chunk_tiles > tiles
                              ? tiles : begin + a.chunk_tiles;
-    const bool alone = !is_prefix<Args> && !is_suffix<Args> && (a.chunks == 1 || tiles <= a.chunk_tiles);
+    const bool alone = !PARTS && (a.chunks == 1 || tiles <= a.chunk_tiles);
 
     // queries: column col is row row0 + col; the lane's
     // channels of group i are 64 i + 16 g .. + 15 (8 for each of two products)
@@ -486,14 +499,14 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
                 acc += *reinterpret_cast<const f32x4_t *>(&part[w * PART + tr * (SEG + 4) + c]);
             if (alone)
                 store_row4(dst + s0 + c, acc * inv, unit);
-            else if (is_prefix<Args>)
+            else if (PARTS)
                 wo[((size_t)chunk * NR + tr) * dim4 + (s0 + c) / 4] = acc;
             else
                 store_agent(wo + ((size_t)chunk * NR + tr) * dim4 + (s0 + c) / 4, acc);
         }
     }
     if (tr < n_rows && threadIdx.x % TPR == 0) {
-        if (is_prefix<Args>)
+        if (PARTS)
             wst[(size_t)chunk * NR + tr] = f32x4_t{mr.sum, lr, mr.out, 0.f};
         else if (!alone)
             store_agent(wst + (size_t)chunk * NR + tr, f32x4_t{mr.sum, lr, mr.out, 0.f});
@@ -501,7 +514,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
             a.lse[(size_t)(t.first + tok) * a.q_heads + hq] =
                 none ? kNegInf : (mr.sum + log2f(lr)) * 0.69314718055994531f;
     }
-    if (alone || is_prefix<Args>)
+    if (alone || PARTS)
         return;
 
     // The last of the row tile's chunks to arrive joins them, in chunk
@@ -509,41 +522,17 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
     // past the L1 see them, and are complete before the arrival counts.
     uint32_t n = (tiles + a.chunk_tiles - 1) / a.chunk_tiles;
     n = n < a.chunks ? n : a.chunks;
-    if constexpr (is_suffix<Args>)
-        n = n ? n : 1u;
     wait_vm<0>();
     __syncthreads();
     uint32_t *const counter = a.counters + tile_id * kKvCounterStride;
     const uint32_t tid = threadIdx.x;
-    if (!is_suffix<Args> || n > 1) {
-        if (tid == 0)
-            last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u == n;
-        __syncthreads();
-        if (!last)
-            return;
-        if (tid == 0)      // ready for the next call that uses this workspace
-            __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    // behind a shared prefix, its chunks follow the row tile's own (an
-    // earlier launch has left them)
-    const uint32_t own = n;
-    if constexpr (is_suffix<Args>)
-        n += a.prefix_chunks;
-    auto prefix_row = [&](uint32_t r, uint32_t c) {
-        return prefix_partial(a, head, t.first * a.group + t.row0 + r, c - own);
-    };
-    auto stat_of = [&](uint32_t c, uint32_t r) {
-        if constexpr (is_suffix<Args>)
-            if (c >= own)
-                return reinterpret_cast<const f32x4_t *>(a.prefix)[a.prefix_rows * dim4 + prefix_row(r, c)];
-        return load_agent(wst + (size_t)c * NR + r);
-    };
-    auto part_of = [&](uint32_t c, uint32_t r, uint32_t c4) {
-        if constexpr (is_suffix<Args>)
-            if (c >= own)
-                return reinterpret_cast<const f32x4_t *>(a.prefix)[prefix_row(r, c) * dim4 + c4];
-        return load_agent(wo + ((size_t)c * NR + r) * dim4 + c4);
-    };
+    if (tid == 0)
+        last = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + 1u == n;
+    __syncthreads();
+    if (!last)
+        return;
+    if (tid == 0)      // ready for the next call that uses this workspace
+        __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     // statistics: thread (row sr, every SG-th chunk from sg on)
     constexpr uint32_t SG = THREADS / NR, PER = kKvMaxChunks / SG;
     const uint32_t sr = tid % NR, sg = tid / NR;
@@ -553,7 +542,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
     for (uint32_t i = 0; i < PER; ++i) {
         st[i] = f32x4_t{kUnset, 0.f, kUnset, 0.f};
         if (sr < n_rows && sg + i * SG < n)
-            st[i] = stat_of(sg + i * SG, sr);
+            st[i] = load_agent(wst + (size_t)(sg + i * SG) * NR + sr);
     }
 #pragma unroll
     for (uint32_t i = 0; i < PER; ++i) {
@@ -604,7 +593,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
 #pragma unroll
                 for (uint32_t u = 0; u < kInFlight; ++u)
                     if (c + u * teams < n)
-                        v[u] = part_of(c + u * teams, jr, c4);
+                        v[u] = load_agent(wo + ((size_t)(c + u * teams) * NR + jr) * dim4 + c4);
 #pragma unroll
                 for (uint32_t u = 0; u < kInFlight; ++u)
                     if (c + u * teams < n)
@@ -632,9 +621,16 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
     }
 }
 
-// Adds the chunks' partial results of the tile kernel: one wave per (row, KV
-// head).  Its lanes are groups of dim / 4, four channels each, that take the
-// chunks in turn; the groups' sums are added in group order.
+template <class Q, int DP, int WAVES, class Args>
+__global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w8a16_kv_rows_kernel(Args a)
+{
+    __shared__ __attribute__((aligned(16))) RowsLds<DP, WAVES> lds;
+    kv_rows<Q, DP, WAVES>(a, blockIdx.x, lds);
+}
+
+// Adds the chunks' partial results of the tile kernel, or of the two passes
+// over a shared prefix: one wave per (row, KV head).  Its lanes are groups of
+// dim / 4, four channels each, that take the chunks in turn; the groups' sums are added in group order.
 template <class E, class Args>
 __global__ __launch_bounds__(256) void w8a16_kv_join_kernel(Args a, uint32_t tile_rows,
                                                             uint32_t rows_used, uint32_t rows_all,

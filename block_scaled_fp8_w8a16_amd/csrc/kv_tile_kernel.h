@@ -80,8 +80,11 @@ __device__ __forceinline__ float max_halves(float x)
     return fmaxf(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
 }
 
-template <class Q, int DP, class Args>
-__device__ __forceinline__ void kv_tile(const Args &a)
+// Workgroup `group_id` of a launch of a.grid; AT: where `a` stands among the
+// kernel's arguments, in bytes.  Either pass over a shared prefix leaves
+// partial rows and no outputs.
+template <class Q, int DP, size_t AT, class Args>
+__device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_t *lds)
 {
     constexpr int QC = DP / 32;             // 32-channel groups of the first product
     constexpr int VT = DP / 32;             // 32-channel tiles of the second
@@ -90,7 +93,6 @@ __device__ __forceinline__ void kv_tile(const Args &a)
     constexpr uint32_t SWZ = DP == 128 || DP == 256 ? 7 : 3;
     struct Scale { uint32_t ks, vs; };
     // kBuffers buffers of K and V codes, then the blocks' scale bytes
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     Scale (*const scl)[4] = reinterpret_cast<Scale (*)[4]>(lds + kBuffers * BUF);
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -100,16 +102,16 @@ __device__ __forceinline__ void kv_tile(const Args &a)
     // KV heads fastest: with 8 or more of them a head's row tiles share an
     // XCD's L2; the row tiles with the longest rows start first.
     const uint32_t groups = sequences(a) * pool.heads;
-    uint32_t id = blockIdx.x;
+    uint32_t id = group_id;
     const uint32_t grp = id % groups;
     id /= groups;
     const uint32_t chunk = id % a.chunks, rtile = a.row_tiles - 1u - id / a.chunks;
     const uint32_t head = grp % pool.heads, b = grp / pool.heads;
 
     RowTile t;
-    if (!extent(a, b, t) || blockIdx.x >= a.grid) {
-        if (blockIdx.x >= a.grid)
-            fill_unowned<typename Q::elem>(a, blockIdx.x - a.grid, 4);
+    if (!extent(a, b, t) || group_id >= a.grid) {
+        if (group_id >= a.grid)
+            fill_unowned<typename Q::elem>(a, group_id - a.grid, 4);
         return;
     }
     t.rows = t.count * a.group;
@@ -514,12 +516,13 @@ __device__ __forceinline__ void kv_tile(const Args &a)
     l += __shfl_xor(l, 32, 64);
     if (row >= t.rows)
         return;
-    // What only the outputs need of the arguments (the kernel's one) is read
+    // What only the outputs need of the arguments is read
     // here: loaded with the others it would stay in scalar registers, or be
     // moved out of them and back, all through the loop (windows of 1000 keys,
     // 64 channels: 71.3 us, so 67.8).
     typedef const __attribute__((address_space(4))) Args *args_ptr;
-    args_ptr late = (args_ptr)__builtin_amdgcn_kernarg_segment_ptr();
+    args_ptr late = (args_ptr)((const __attribute__((address_space(4))) uint8_t *)
+                                   __builtin_amdgcn_kernarg_segment_ptr() + AT);
     asm volatile("" : "+s"(late));
     const bool none = rhi <= rlo;
     if (alone) {
@@ -580,13 +583,17 @@ __device__ __forceinline__ void kv_tile(const Args &a)
 template <class Q, int DP, class Args>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void w8a16_kv_tile_kernel(Args a)
 {
-    kv_tile<Q, DP>(a);
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    kv_tile<Q, DP, 0>(a, blockIdx.x, lds);
 }
+
+// Dynamic LDS: codes and scale bytes.
+template <int DP> constexpr uint32_t tile_lds = kBuffers * (8 * 16 * DP + 4 * 8);
 
 template <class Q, int DP, class Args>
 hipError_t launch_dim(const Args &a, hipStream_t stream)
 {
-    const uint32_t bytes = kBuffers * (8 * 16 * DP + 4 * 8);     // codes and scale bytes
+    const uint32_t bytes = tile_lds<DP>;
     static std::atomic<uint64_t> lds_set{0};
     auto kern = w8a16_kv_tile_kernel<Q, DP, Args>;
     hipError_t e = allow_lds(reinterpret_cast<const void *>(kern), bytes, bytes, lds_set);

@@ -594,7 +594,7 @@ int w8a16_kv_attention(const w8a16_kv_cache_t *cache, const w8a16_kv_seqs_t *seq
  *   Results are those without it, up to the order of additions.  With a
  *   window it is not used.  A given plan is that of the second pass, over the
  *   keys from the shared part's last 64-key tile on, and asks for two passes;
- *   it may have 64 chunks. */
+ *   it has 4 waves and may have 64 chunks. */
 typedef struct w8a16_kv_span {
     uint32_t sinks, shared;
 } w8a16_kv_span_t;

@@ -275,10 +275,9 @@ SHARED = [
 ]
 
 
-def own_plan(w8, new, group, waves=4, chunk=2):
+def own_plan(w8, new, group, chunk=2):
     tile = max(new) * group > 32
-    return w8.KVPlan(kernel=2 if tile else 1, row_blocks=8 if tile else 1, waves=4 if tile else waves,
-                     chunk_tiles=chunk)
+    return w8.KVPlan(kernel=2 if tile else 1, row_blocks=8 if tile else 1, waves=4, chunk_tiles=chunk)
 
 
 @pytest.mark.gpu
@@ -296,9 +295,6 @@ def test_shared(w8, case, chunk):
     if chunk == 1:        # the default, one pass or two
         out, lse = call(w8, dev, table, q, dtype, new, totals, **kw)
         compare(out, lse, want, dtype)
-    if chunk == 2 and dim <= 128:
-        plan = own_plan(w8, new, hq // hkv, waves=8)
-        compare(*call(w8, dev, table, q, dtype, new, totals, plan_=plan, **kw), want, dtype)
 
 
 @pytest.mark.gpu
@@ -395,11 +391,12 @@ def test_strided_rows(w8):
 
 
 @pytest.mark.gpu
-def test_plans_of_too_many_chunks_are_refused(w8):
+@pytest.mark.parametrize("kw", [dict(waves=4, chunk_tiles=2), dict(waves=8, chunk_tiles=64)])
+def test_plans_that_are_refused(w8, kw):      # more than 64 chunks, or 8 waves
     cache = w8.kv_cache(70, 1, 128, 16)
     bt = torch.arange(70, dtype=torch.int32, device="cuda").expand(2, 70).contiguous()
     q = torch.zeros(2, 1, 16, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(w8.W8A16Error) as e:
         w8.kv_attention(q, cache, bt, i32([8000, 8000]), shared=128,
-                        plan_=w8.KVPlan(kernel=1, row_blocks=1, waves=4, chunk_tiles=2))
+                        plan_=w8.KVPlan(kernel=1, row_blocks=1, **kw))
     assert e.value.status == w8.ERR_BAD_PLAN
