@@ -156,25 +156,12 @@ namespace {
 // A join takes both passes' chunks of a row tile.
 constexpr uint64_t kMaxPassChunks = kKvMaxChunks / 2;
 
-// A pass's plan over `keys` keys, with room for its partial rows; `given`
-// (null: none) in place of the default.
+// A pass's plan over `keys` keys, with room for its partial rows: the given
+// kernel and chunks.
 int pass_plan(uint32_t seqs, uint32_t max_new, uint32_t keys, uint32_t q_heads, uint32_t kv_heads,
-              uint32_t head_dim, uint32_t cu_count, const w8a16_kv_plan_t *given, w8a16_kv_plan_t *p)
+              uint32_t head_dim, w8a16_kv_plan_t *p)
 {
-    int st;
-    if (given) {
-        *p = *given;
-        st = kv_plan_finalize(seqs, max_new, keys, q_heads, kv_heads, head_dim, 0, p);
-    } else {
-        st = make_kv_plan(seqs, max_new, keys, q_heads, kv_heads, head_dim, 0, cu_count, p);
-        if (st == W8A16_OK) {
-            p->waves = 4;
-            const uint64_t least = div_up(div_up(keys, kKeysPerTile), kMaxPassChunks);
-            if (p->chunk_tiles < least)
-                p->chunk_tiles = (uint32_t)least;
-            st = kv_plan_finalize(seqs, max_new, keys, q_heads, kv_heads, head_dim, 0, p);
-        }
-    }
+    const int st = kv_plan_finalize(seqs, max_new, keys, q_heads, kv_heads, head_dim, 0, p);
     if (st != W8A16_OK)
         return st;
     if (p->chunks > kMaxPassChunks || p->waves != 4)
@@ -182,6 +169,71 @@ int pass_plan(uint32_t seqs, uint32_t max_new, uint32_t keys, uint32_t q_heads, 
                                         "most 64 chunks");
     p->workspace_bytes = (uint64_t)p->grid * 16 * p->row_blocks * (head_dim + 4) * 4;
     return W8A16_OK;
+}
+
+w8a16_kv_plan_t chunked(uint32_t kernel, uint64_t chunk_tiles)
+{
+    w8a16_kv_plan_t p;
+    std::memset(&p, 0, sizeof p);
+    p.kernel = kernel;
+    p.row_blocks = kernel == W8A16_KV_ROWS ? 1 : 8;
+    p.waves = 4;
+    p.chunk_tiles = (uint32_t)chunk_tiles;
+    return p;
+}
+
+// Times of the attention over caches with a shared part, in us, to choose
+// between one pass and two and between their chunks.  Fitted to 8 KV heads
+// of 128 channels, 2 to 128 sequences of 1 to 250 new tokens behind 512 to
+// 30016 shared ones; most of some 300 times agree within 10 %, e.g. 64
+// sequences of 32 heads behind 8192 with 8, 16 and 4 tiles to a chunk: 32.9,
+// 41.1 and 43.5 (here 35, 39, 42), one pass 89.9 (90); 128 of up to 2000 own
+// tokens with 32 and 16: 85.7 and 92.8 (88, 92).
+struct Cost {
+    double cus, slots, size;       // size: of a tile against 128 channels' (above them a CU holds one
+                                   // workgroup, and its loads wait more)
+    Cost(uint32_t cu_count, uint32_t head_dim)
+        : cus(cu_count), slots(head_dim <= 128 ? 2.0 * cu_count : cu_count),
+          size(head_dim / 128.0 * (head_dim <= 128 ? 1.0 : 1.15))
+    {
+    }
+    // A CU's time for a tile of keys and a row tile: as many as it runs at
+    // once share it.
+    double tile(uint32_t kernel) const { return (kernel == W8A16_KV_ROWS ? 0.3 : 1.15) * size; }
+    // A workgroup's time for one where it has the CU for itself.
+    double alone(uint32_t kernel) const { return (kernel == W8A16_KV_ROWS ? 0.3 : 1.4) * size; }
+    // The CU with the most workgroups of n.
+    double most(double n) const { return n <= cus ? 1.0 : (double)div_up((uint64_t)n, (uint64_t)cus); }
+    // Reading n tiles of keys from HBM.
+    double read(double n) const { return 0.85 * size * n / cus; }
+    // Partial rows written and read.
+    double partial(double rows, uint32_t dim) const { return 2.0 * rows * (dim + 4) * 4 / 4.0e6; }
+};
+
+// Shared tiles come from the caches, own ones from HBM.
+double one_pass(const Cost &c, const w8a16_kv_plan_t &p, uint64_t shared_tiles, uint64_t own_tiles, uint32_t dim)
+{
+    const double tile = c.tile(p.kernel), fetch = 0.85 * c.size / p.row_tiles;
+    const double all = (double)(shared_tiles + own_tiles);
+    const double mean = (shared_tiles * tile + own_tiles * (tile > fetch ? tile : fetch)) / all;
+    const double rows = p.chunks > 1 ? (double)p.grid * 16 * p.row_blocks : 0;
+    return 8.0 + (p.chunks > 1 ? 4.0 : 0.0) + c.most(p.grid) * (p.chunks > 1 ? p.chunk_tiles : all) * mean +
+           (p.kernel == W8A16_KV_TILE ? 2.0 + c.partial(rows, dim) : 0.0);
+}
+
+// The prefix's products run while the own keys are read.
+double two_passes(const Cost &c, const w8a16_kv_plan_t &p, const w8a16_kv_plan_t &o, uint64_t own_tiles,
+                  uint64_t rows, uint32_t kv_heads, uint32_t dim)
+{
+    const double own_tile = c.tile(o.kernel) * o.grid / o.chunks * own_tiles / c.cus;
+    const double read = c.read((double)o.grid / o.chunks / o.row_tiles * own_tiles);
+    const double chunk = c.alone(p.kernel) * p.chunk_tiles;
+    double busy = c.most(p.grid) * p.chunk_tiles * c.tile(p.kernel) + own_tile;
+    busy = busy > read ? busy : read;
+    busy = busy > chunk ? busy : chunk;
+    const double rounds = (double)div_up((uint64_t)p.grid + o.grid, (uint64_t)c.slots);
+    return 11.5 + (dim <= 128 ? 3.0 : 8.0) * (rounds - 1.0) + busy +
+           c.partial((double)rows * kv_heads * (p.chunks + o.chunks), dim);
 }
 
 }  // namespace
@@ -192,25 +244,65 @@ int make_kv_shared_plans(uint32_t seqs, uint32_t tokens, uint32_t max_new, uint3
                          w8a16_kv_plan_t *suffix)
 {
     std::memset(prefix, 0, sizeof *prefix);
-    // (the second pass starts with the tile that the shared keys end in)
+    w8a16_kv_plan_t whole;
+    int st = make_kv_plan(seqs, max_new, max_kv, q_heads, kv_heads, head_dim, 0, cu_count, &whole);
+    if (st != W8A16_OK)
+        return st;
+    *suffix = whole;
+    if (!shared || (seqs < 2 && !given))
+        return W8A16_OK;
+    // the own keys' pass: they start in the tile that the shared ones end in
     const uint32_t before = shared / (uint32_t)kKeysPerTile * (uint32_t)kKeysPerTile;
     const uint32_t own = max_kv > before ? max_kv - before : 1u;
-    if (given || (shared && seqs > 1)) {
-        int st = pass_plan(1, tokens, shared, q_heads, kv_heads, head_dim, cu_count, nullptr, prefix);
-        if (st == W8A16_OK)
-            st = pass_plan(seqs, max_new, own, q_heads, kv_heads, head_dim, cu_count, given, suffix);
-        // (one tile kernel is enough: own rows that want it are the prefix's too)
-        if (st == W8A16_OK && suffix->kernel == W8A16_KV_TILE && prefix->kernel == W8A16_KV_ROWS) {
-            w8a16_kv_plan_t tiles = *prefix;
-            tiles.kernel = W8A16_KV_TILE;
-            tiles.row_blocks = 8;
-            st = pass_plan(1, tokens, shared, q_heads, kv_heads, head_dim, cu_count, &tiles, prefix);
-        }
-        if (st == W8A16_OK || given)
+    const uint64_t own_tiles = div_up(own, kKeysPerTile), shared_tiles = div_up(shared, kKeysPerTile);
+    w8a16_kv_plan_t o;
+    if (given) {
+        o = *given;
+    } else {
+        st = make_kv_plan(seqs, max_new, own, q_heads, kv_heads, head_dim, 0, cu_count, &o);
+        if (st != W8A16_OK)
             return st;
-        std::memset(prefix, 0, sizeof *prefix);
+        const uint64_t least = div_up(own_tiles, kMaxPassChunks);
+        o = chunked(o.kernel, o.chunk_tiles < least ? least : o.chunk_tiles);
     }
-    return make_kv_plan(seqs, max_new, max_kv, q_heads, kv_heads, head_dim, 0, cu_count, suffix);
+    st = pass_plan(seqs, max_new, own, q_heads, kv_heads, head_dim, &o);
+    if (st != W8A16_OK) {
+        if (given)
+            return st;
+        return W8A16_OK;      // (too many workgroups: one pass)
+    }
+    // The shared keys' pass: either kernel (the tile kernel where the own
+    // keys' takes it: the launch holds no other pair), in chunks of twice as
+    // many tiles each time, or as many as give each CU one workgroup or two.
+    // One pass is kept unless two promise 5 % (what the estimates are off by
+    // where they are close).
+    const Cost c(cu_count ? cu_count : kDefaultCUs, head_dim);
+    const uint64_t rows = (uint64_t)tokens * (q_heads / kv_heads);
+    double best = given ? 1e30 : 0.95 * one_pass(c, whole, shared_tiles, own_tiles, head_dim);
+    auto consider = [&](uint32_t kernel, uint64_t per) {
+        w8a16_kv_plan_t p = chunked(kernel, per < shared_tiles ? per : shared_tiles);
+        if (div_up(shared_tiles, p.chunk_tiles) > kMaxPassChunks ||
+            pass_plan(1, tokens, shared, q_heads, kv_heads, head_dim, &p) != W8A16_OK)
+            return;
+        const double t = two_passes(c, p, o, own_tiles, rows, kv_heads, head_dim);
+        if (t < best) {
+            best = t;
+            *prefix = p;
+            *suffix = o;
+        }
+    };
+    for (uint32_t kernel = o.kernel == W8A16_KV_TILE ? W8A16_KV_TILE : W8A16_KV_ROWS; kernel <= W8A16_KV_TILE;
+         ++kernel) {
+        const uint64_t row_tiles = kv_heads * div_up(rows, kernel == W8A16_KV_ROWS ? 16 : 128);
+        for (uint64_t per = kMinTiles; per / 2 < shared_tiles; per *= 2)
+            consider(kernel, per);
+        for (uint64_t n = 1; n <= 2; ++n)
+            if (n * (uint64_t)c.cus > row_tiles)
+                consider(kernel, div_up(shared_tiles, n * (uint64_t)c.cus / row_tiles));
+    }
+    if (given && !prefix->grid)
+        return fail(W8A16_ERR_SHAPE, "w8a16_kv_attention: too many workgroups (2^32 threads) for one call");
+    return W8A16_OK;
 }
 
 }  // namespace w8a16

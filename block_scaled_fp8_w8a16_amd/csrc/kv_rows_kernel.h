@@ -630,7 +630,8 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
 
 // Adds the chunks' partial results of the tile kernel, or of the two passes
 // over a shared prefix: one wave per (row, KV head).  Its lanes are groups of
-// dim / 4, four channels each, that take the chunks in turn; the groups' sums are added in group order.
+// dim / 4, four channels each, that take the chunks in turn; the groups' sums
+// are added in group order.
 template <class E, class Args>
 __global__ __launch_bounds__(256) void w8a16_kv_join_kernel(Args a, uint32_t tile_rows,
                                                             uint32_t rows_used, uint32_t rows_all,

@@ -117,7 +117,7 @@ def compare(out, lse, want, dtype):
         bad.sum(), np.argwhere(bad)[0], got[bad][0], o[bad][0], to[bad][0])
     none = np.isinf(ls)
     assert np.array_equal(none, np.isinf(gl)) and (gl[none] < 0).all() and (got[none] == 0).all()
-    bad = ~(np.abs(gl - ls)[~none] <= tl[~none])
+    bad = ~(np.abs(gl[~none] - ls[~none]) <= tl[~none])
     assert not bad.any(), "%d log-sums off" % bad.sum()
 
 
