@@ -270,17 +270,6 @@ def gemm(a, w, scale, c=None, *, plan_: Optional[Plan] = None, stream=None):
 ACTIVATIONS = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 
 
-def _rows2(name, t, m, n, types):
-    """Row stride of an [m, n] operand with unit column stride."""
-    if t.dtype not in types or t.shape != (m, n) or not t.is_cuda:
-        raise ValueError("%s must be a GPU tensor [%d, %d] of %s" %
-                         (name, m, n, " or ".join(str(x) for x in types)))
-    rs, cs = t.stride()
-    if cs != 1 and n > 1:
-        raise ValueError("%s needs a unit column stride" % name)
-    return rs if m > 1 else max(rs, n)
-
-
 def gemm_epilogue(a, w, scale, c=None, *, bias=None, activation: Optional[str] = None, gate=None,
                   residual=None, out_dtype=None, stream=None):
     """C = residual + activation(A @ dequant(W)^T + bias) * gate, rounded once.
@@ -290,53 +279,13 @@ def gemm_epilogue(a, w, scale, c=None, *, bias=None, activation: Optional[str] =
     [m, n].  residual: bfloat16 or float32 [m, n]; it may be c.  c: bfloat16
     or float32 [m, n] (None: a new one of out_dtype, by default bfloat16).
     Unit column strides; what is None is left out.  Returns c."""
-    lib, torch, dtypes, check, raw = _attention._setup()
-    bf16, f32 = torch.bfloat16, torch.float32
-    if a.dim() != 2 or w.dim() != 2:
-        raise ValueError("a and w must be 2-D")
-    (m, k), n = a.shape, w.shape[0]
-    if w.shape[1] != k:
-        raise ValueError("w must be [n, k] with the k of a")
-    if w.dtype not in (torch.uint8, torch.float8_e4m3fn) or not w.is_contiguous():
-        raise ValueError("w must be contiguous float8_e4m3fn or uint8")
-    if scale.dtype != f32 or not scale.is_contiguous() or \
-            scale.numel() < (n + 127) // 128 * (k // 128 if k % 128 == 0 else 0):
-        raise ValueError("scale must be contiguous float32 [ceil(n/128), k/128]")
-    if activation not in ACTIVATIONS:
-        raise ValueError("activation must be None, 'relu', 'silu', 'gelu' or 'gelu_tanh'")
-    ars = _rows2("a", a, m, k, (bf16,))
-    if not (w.is_cuda and scale.is_cuda):
-        raise ValueError("all operands must be GPU tensors")
-    e = Epilogue(activation=ACTIVATIONS[activation])
-    if c is None:
-        if out_dtype is None:
-            out_dtype = bf16
-        elif out_dtype is not bf16 and out_dtype is not f32:
+    f32 = None
+    if out_dtype is not None:
+        import torch
+        if out_dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("out_dtype must be bfloat16 or float32")
-        with _attention._on(torch, stream):
-            c = a.new_empty((m, n), dtype=out_dtype)
-        crs = n
-    else:
-        if out_dtype is not None and out_dtype != c.dtype:
-            raise ValueError("out_dtype must be that of c")
-        crs = _rows2("c", c, m, n, (bf16, f32))
-    e.out_dtype = dtypes[c.dtype]
-    if bias is not None:
-        if bias.dtype not in (bf16, f32) or bias.shape != (n,) or not bias.is_contiguous() or \
-                not bias.is_cuda:
-            raise ValueError("bias must be a contiguous bfloat16 or float32 GPU tensor [n]")
-        e.bias, e.bias_dtype = bias.data_ptr(), dtypes[bias.dtype]
-    if gate is not None:
-        e.gate_row_stride = _rows2("gate", gate, m, n, (bf16,))
-        e.gate = gate.data_ptr()
-    if residual is not None:
-        e.residual_row_stride = _rows2("residual", residual, m, n, (bf16, f32))
-        e.residual, e.residual_dtype = residual.data_ptr(), dtypes[residual.dtype]
-    st = lib.w8a16_gemm_epilogue(a.data_ptr(), ars, w.data_ptr(), scale.data_ptr(), c.data_ptr(), crs, m, n,
-                                 k, e, raw(a.get_device()) if stream is None else stream.cuda_stream)
-    if st:
-        check(st)
-    return c
+        f32 = out_dtype == torch.float32
+    return _attention._run("gemm_epilogue", a, stream, a, w, scale, c, bias, activation, gate, residual, f32)
 
 
 def _desc_array(descs):

@@ -7,10 +7,11 @@ decoder layer between its Q/K/V and output projections.
     out = kv_attention(q, cache, block_table, kv_lens)
 
 Marshalling only, as in the rest of the package: shapes, types and devices
-are checked here, everything else by the C entry points (include/w8a16.h,
-which defines the operators and the cache's layout).  Calls run on the
-current (or given) torch stream, take the memory of their outputs there, and
-do not synchronise.
+are checked by the native part of the binding (csrc/binding.cpp), everything
+else by the C entry points (include/w8a16.h, which defines the operators and
+the cache's layout).  Calls run on their tensors' device, on the current (or
+given) torch stream, take the memory of their outputs there, and do not
+synchronise.
 """
 
 from __future__ import annotations
@@ -113,26 +114,59 @@ def declare(lib) -> None:
 
 
 _state = None
-_codes = _scale_bytes = ()     # torch types of a cache's codes and scale bytes
+_fast = None       # (native binding, raw stream of a device index, current device index, raise function)
 
 
 def _setup():
-    """(library, torch, dtype codes, raise function, raw stream of a device
-    index), resolved once."""
-    global _state, _codes, _scale_bytes
+    """(library, torch, raise function, raw stream of a device index),
+    resolved once, and the native binding's entry points."""
+    global _state, _fast
     if _state is None:
         import torch
 
         from . import _raise_if, library
+        lib = library()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise ImportError("_binding.so cannot be loaded (%s); run python -m "
+                              "block_scaled_fp8_w8a16_amd.build" % e) from e
         # what current_stream(device).cuda_stream returns, an order of
-        # magnitude faster (0.06 against 1.8 us of a call's 8)
+        # magnitude faster (0.06 against 1.8 us)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda index: torch.cuda.current_stream(index).cuda_stream)
-        _codes = (torch.uint8, torch.float8_e4m3fn)
-        _scale_bytes = (torch.uint8, torch.float8_e8m0fnu)
-        _state = (library(), torch,
-                  {torch.bfloat16: 1, torch.float16: 2, torch.float32: 3}, _raise_if, raw)
+        current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+        _binding.bind(*(ctypes.cast(getattr(lib, "w8a16_" + name), _vp).value
+                        for name in ("rope", "rope_axes", "kv_append", "kv_append_axes", "kv_attention",
+                                     "kv_attention_span", "gemm_epilogue")))
+        _fast = (_binding, raw, current, _raise_if)
+        _state = (lib, torch, _raise_if, raw)
     return _state
+
+
+def _run(name, x, stream, *args):
+    """Native entry point `name` on the given stream, or the current one of
+    x's device."""
+    if _fast is None:
+        _setup()
+    binding, raw, current, check = _fast
+    index = x.get_device()
+    if stream is None and (index < 0 or index == current()):
+        r = getattr(binding, name)(*args, raw(index) if index >= 0 else 0)
+    else:
+        # outputs are made on the stream that will write them (the current
+        # stream's memory might still be written by work that is to come there)
+        import torch
+        with torch.cuda.device(index) if stream is None else torch.cuda.stream(stream):
+            r = getattr(binding, name)(*args, raw(index) if stream is None else stream.cuda_stream)
+    if r.__class__ is int:
+        check(r)
+    return r
+
+
+def _on(torch, stream):
+    """Where a call makes its outputs."""
+    return nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 class KVCache(NamedTuple):
@@ -162,97 +196,13 @@ def kv_cache(pages: int, kv_heads: int, page_size: int, head_dim: int, device="c
                    zeros(pages, kv_heads, blocks), zeros(pages, kv_heads, blocks))
 
 
-def _page_stride(name, t, inside):
-    """Page stride of a cache tensor whose pages are contiguous inside."""
-    st, want = t.stride(), 1
-    for n, have in zip(reversed(t.shape[1:]), reversed(st[1:])):
-        if n > 1 and have != want:
-            raise ValueError("the inside of a %s page must be contiguous" % name)
-        want *= n
-    return max(st[0], inside) if t.shape[0] < 2 else st[0]
-
-
-def _cache_desc(cache) -> KVCacheDesc:
-    k, v, ks, vs = cache
-    pages, heads, page, dim = k.shape
-    blocks = page // KV_BLOCK
-    if v.shape != (pages, heads, blocks, dim, KV_BLOCK) or ks.shape != (pages, heads, blocks) or \
-            vs.shape != ks.shape:
-        raise ValueError("cache must be k [pages, heads, page, dim], v [pages, heads, page/16, dim, "
-                         "16] and scales [pages, heads, page/16]")
-    if k.dtype not in _codes or v.dtype not in _codes or ks.dtype not in _scale_bytes or \
-            vs.dtype not in _scale_bytes:
-        raise ValueError("cache codes must be uint8 or float8_e4m3fn, its scales uint8 or float8_e8m0fnu")
-    if not (k.is_cuda and v.is_cuda and ks.is_cuda and vs.is_cuda):
-        raise ValueError("cache must be GPU tensors")
-    codes, bytes_ = heads * page * dim, heads * blocks
-    return KVCacheDesc(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(),
-                       codes if k.is_contiguous() else _page_stride("k", k, codes),
-                       codes if v.is_contiguous() else _page_stride("v", v, codes),
-                       bytes_ if ks.is_contiguous() else _page_stride("k_scale", ks, bytes_),
-                       bytes_ if vs.is_contiguous() else _page_stride("v_scale", vs, bytes_),
-                       pages, page, heads, dim)
-
-
-def _seqs_desc(i32, block_table, kv_lens, cu_seqlens, tokens, max_new) -> KVSeqs:
-    if block_table.dtype != i32 or kv_lens.dtype != i32 or kv_lens.dim() != 1:
-        raise ValueError("block_table must be int32 [seqs, pages] and kv_lens int32 [seqs]")
-    seqs = kv_lens.shape[0]
-    rows, width = block_table.shape
-    if rows != seqs or not (block_table.is_cuda and kv_lens.is_cuda):
-        raise ValueError("block_table and kv_lens must be GPU tensors of the same sequences")
-    pitch = width
-    if not block_table.is_contiguous():
-        pitch = block_table.stride(0) if seqs > 1 else width
-        if width > 1 and block_table.stride(1) != 1:
-            raise ValueError("block_table rows must be contiguous")
-    if not kv_lens.is_contiguous():
-        raise ValueError("kv_lens must be contiguous")
-    cu = 0
-    if cu_seqlens is not None:
-        if cu_seqlens.dtype != i32 or cu_seqlens.shape != (seqs + 1,) or \
-                not cu_seqlens.is_contiguous() or not cu_seqlens.is_cuda:
-            raise ValueError("cu_seqlens must be a contiguous int32 GPU tensor [seqs + 1]")
-        cu = cu_seqlens.data_ptr()
-        if max_new is None:
-            max_new = tokens
-    elif max_new is None:
-        max_new = tokens // max(1, seqs)
-    return KVSeqs(block_table.data_ptr(), kv_lens.data_ptr(), cu, pitch, width, seqs, tokens, max_new)
-
-
-def _rows(name, t, tokens, heads, dim, dtype):
-    """Token and head strides of a [tokens, heads, dim] operand."""
-    if t.shape != (tokens, heads, dim) or t.dtype != dtype or not t.is_cuda:
-        raise ValueError("%s must be a %s GPU tensor [%d, %d, %d]" % (name, dtype, tokens, heads, dim))
-    st, sh, sd = t.stride()
-    if sd != 1 and dim > 1:
-        raise ValueError("%s needs a unit stride along head_dim" % name)
-    return st, sh
-
-
-def _on(torch, stream):
-    """Where a call makes its outputs: on the stream that will write them (the
-    current stream's memory might still be written by work that is to come
-    there)."""
-    return nullcontext() if stream is None else torch.cuda.stream(stream)
-
-
-def _like(torch, t, stream):
-    """A new contiguous tensor of t's shape and type."""
-    if stream is not None:
-        with _on(torch, stream):
-            return _like(torch, t, None)
-    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
-
-
 def rope_table(positions: int, rot_dim: int, *, base: float = 10000.0, scaling: Optional[str] = None,
                factor: float = 1.0, original: float = 0.0, low_turns: float = 1.0,
                high_turns: float = 4.0, magnitude: float = 1.0, out=None, device="cuda", stream=None):
     """float32 [positions, rot_dim / 2, 2]: (cos, sin) of every position and
     pair, times `magnitude`.  scaling: None, "linear", "base" or "bands"
     (w8a16_rope_scaling in include/w8a16.h)."""
-    lib, torch, _, check, raw = _setup()
+    lib, torch, check, raw = _setup()
     if scaling not in ROPE_SCALINGS:
         raise ValueError("scaling must be None, 'linear', 'base' or 'bands'")
     shape = (positions, rot_dim // 2, 2)
@@ -265,29 +215,6 @@ def rope_table(positions: int, rot_dim: int, *, base: float = 10000.0, scaling: 
     check(lib.w8a16_rope_table(cfg, out.data_ptr(), positions, rot_dim,
                                raw(out.get_device()) if stream is None else stream.cuda_stream))
     return out
-
-
-def _check_table(f32, table):
-    if table.dtype != f32 or table.dim() != 3 or table.shape[2] != 2 or \
-            not table.is_contiguous() or not table.is_cuda:
-        raise ValueError("table must be a contiguous float32 GPU tensor [positions, rot_dim/2, 2]")
-    positions, pairs, _ = table.shape
-    return table.data_ptr(), positions, 2 * pairs
-
-
-def _axes(i32, positions, tokens, sections, order, table_pairs) -> Axes:
-    """Positions of several axes; sections: pairs of each."""
-    if order not in ROPE_ORDERS:
-        raise ValueError("order must be 'split', 'turns' or 'own'")
-    count = len(sections)
-    if not 0 < count <= ROPE_MAX_AXES or min(sections) < 0:
-        raise ValueError("sections must be the pairs of 1 to %d axes" % ROPE_MAX_AXES)
-    if positions is None or positions.dtype != i32 or positions.shape != (count, tokens) or \
-            not positions.is_cuda or (tokens > 1 and positions.stride(1) != 1):
-        raise ValueError("positions must be an int32 GPU tensor [%d, %d] with a unit stride along tokens" %
-                         (count, tokens))
-    return Axes(positions.data_ptr(), positions.stride(0), count, ROPE_ORDERS[order],
-                (_u32 * ROPE_MAX_AXES)(*sections), table_pairs)
 
 
 def rope(x, table, positions, out=None, *, layout: str = "half", inverse: bool = False, sections=None,
@@ -304,38 +231,7 @@ def rope(x, table, positions, out=None, *, layout: str = "half", inverse: bool =
     i % axes's while that one has pairs left, else axis 0's) or "own" (as
     split, each axis starting again at the table's first column); the table has
     sum(sections) pairs, in "own" at least max(sections)."""
-    lib, torch, dtypes, check, raw = _setup()
-    dtype = x.dtype
-    if x.dim() != 3 or dtype not in dtypes:
-        raise ValueError("x must be bfloat16, float16 or float32 [tokens, heads, head_dim]")
-    tokens, heads, dim = x.shape
-    xt, xh = _rows("x", x, tokens, heads, dim, dtype)
-    if out is None:
-        out = _like(torch, x, stream)
-        yt, yh = heads * dim, dim
-    else:
-        yt, yh = _rows("out", out, tokens, heads, dim, dtype)
-    if layout not in ROPE_LAYOUTS:
-        raise ValueError("layout must be 'half' or 'interleaved'")
-    tp, tn, rot = _check_table(torch.float32, table)
-    if sections is not None:
-        st = lib.w8a16_rope_axes(x.data_ptr(), xt, xh, out.data_ptr(), yt, yh, dtypes[dtype], tokens, heads,
-                                 dim, tp, tn,
-                                 _axes(torch.int32, positions, tokens, sections, order, table.shape[1]),
-                                 ROPE_LAYOUTS[layout], inverse,
-                                 raw(x.get_device()) if stream is None else stream.cuda_stream)
-        if st:
-            check(st)
-        return out
-    if positions.shape != (tokens,) or positions.dtype != torch.int32 or \
-            not positions.is_contiguous() or not positions.is_cuda:
-        raise ValueError("positions must be a contiguous int32 GPU tensor [tokens]")
-    st = lib.w8a16_rope(x.data_ptr(), xt, xh, out.data_ptr(), yt, yh, dtypes[dtype], tokens, heads, dim,
-                        tp, tn, rot, positions.data_ptr(), ROPE_LAYOUTS[layout], inverse,
-                        raw(x.get_device()) if stream is None else stream.cuda_stream)
-    if st:
-        check(st)
-    return out
+    return _run("rope", x, stream, x, table, positions, out, layout, inverse, sections, order)
 
 
 def kv_append(cache, k, v, block_table, kv_lens, *, cu_seqlens=None, max_new: Optional[int] = None,
@@ -352,51 +248,8 @@ def kv_append(cache, k, v, block_table, kv_lens, *, cu_seqlens=None, max_new: Op
     bound launches less).  sections, positions (int32 [axes, tokens]) and
     order: rotate by positions of several axes, as rope does, in place of each
     token's place in its sequence.  Returns q_out (None without q)."""
-    lib, torch, dtypes, check, raw = _setup()
-    dtype = k.dtype
-    if k.dim() != 3 or dtype not in dtypes:
-        raise ValueError("k must be bfloat16, float16 or float32 [tokens, kv_heads, head_dim]")
-    tokens, heads, dim = k.shape
-    desc = _cache_desc(cache)
-    if heads != desc.kv_heads or dim != desc.head_dim:
-        raise ValueError("k must have the cache's heads and head_dim")
-    kt, kh = _rows("k", k, tokens, heads, dim, dtype)
-    vt, vh = _rows("v", v, tokens, heads, dim, dtype)
-    if layout not in ROPE_LAYOUTS:
-        raise ValueError("layout must be 'half' or 'interleaved'")
-    tp = tn = rot = qp = op = hq = qt = qh = ot = oh = 0
-    if table is not None:
-        tp, tn, rot = _check_table(torch.float32, table)
-    if q is not None:
-        hq = q.shape[1] if q.dim() == 3 else 0
-        qt, qh = _rows("q", q, tokens, hq, dim, dtype)
-        if q_out is None:
-            q_out = _like(torch, q, stream)
-            ot, oh = hq * dim, dim
-        else:
-            ot, oh = _rows("q_out", q_out, tokens, hq, dim, dtype)
-        qp, op = q.data_ptr(), q_out.data_ptr()
-    else:
-        q_out = None
-    seqs = _seqs_desc(torch.int32, block_table, kv_lens, cu_seqlens, tokens, max_new)
-    axes = None
-    if sections is not None:
-        if table is None:
-            raise ValueError("positions of several axes need a table")
-        axes = _axes(torch.int32, positions, tokens, sections, order, table.shape[1])
-        rot = 2 * sum(sections)
-    elif positions is not None:
-        raise ValueError("positions need sections")
-    args = KVAppendArgs(k.data_ptr(), v.data_ptr(), qp, op, kt, kh, vt, vh, qt, qh, ot, oh, tp, tn, rot,
-                        ROPE_LAYOUTS[layout], dtypes[dtype], hq)
-    queue = raw(k.get_device()) if stream is None else stream.cuda_stream
-    if axes is None:
-        st = lib.w8a16_kv_append(desc, seqs, args, queue)
-    else:
-        st = lib.w8a16_kv_append_axes(desc, seqs, args, axes, queue)
-    if st:
-        check(st)
-    return q_out
+    return _run("kv_append", k, stream, cache, k, v, block_table, kv_lens, cu_seqlens, max_new, table, layout,
+                q, q_out, positions, sections, order)
 
 
 def kv_attention(q, cache, block_table, kv_lens, out=None, *, cu_seqlens=None,
@@ -414,38 +267,9 @@ def kv_attention(q, cache, block_table, kv_lens, out=None, *, cu_seqlens=None,
     them): whole pages of them are read once for the batch where that pays;
     results are the same up to the order of additions.  Returns
     out, or (out, lse) with lse float32 [tokens, q_heads]."""
-    lib, torch, dtypes, check, raw = _setup()
-    desc = _cache_desc(cache)
-    dim, dtype = desc.head_dim, q.dtype
-    if q.dim() != 3 or dtype not in dtypes:
-        raise ValueError("q must be bfloat16 or float16 [tokens, q_heads, head_dim]")
-    tokens, heads, _ = q.shape
-    qt, qh = _rows("q", q, tokens, heads, dim, dtype)
-    if out is None:
-        out = _like(torch, q, stream)
-        ot, oh = heads * dim, dim
-    else:
-        ot, oh = _rows("out", out, tokens, heads, dim, dtype)
-    lse, lp = None, 0
-    if return_lse:
-        with _on(torch, stream):
-            lse = q.new_empty((tokens, heads), dtype=torch.float32)
-        lp = lse.data_ptr()
-    if window < 0 or sinks < 0 or shared < 0:
-        raise ValueError("window, sinks and shared must not be negative")
-    seqs = _seqs_desc(torch.int32, block_table, kv_lens, cu_seqlens, tokens, max_new)
-    args = KVAttentionArgs(q.data_ptr(), out.data_ptr(), lp, qt, qh, ot, oh,
-                           None if plan_ is None else ctypes.pointer(plan_),
-                           dim ** -0.5 if scale is None else scale, heads, dtypes[dtype], causal,
-                           window, max_kv or 0)
-    queue = raw(q.get_device()) if stream is None else stream.cuda_stream
-    if sinks or shared:
-        st = lib.w8a16_kv_attention_span(desc, seqs, args, KVSpan(min(sinks, 1 << 30), min(shared, 1 << 30)), queue)
-    else:
-        st = lib.w8a16_kv_attention(desc, seqs, args, queue)
-    if st:
-        check(st)
-    return (out, lse) if return_lse else out
+    return _run("kv_attention", q, stream, q, cache, block_table, kv_lens, out, cu_seqlens, max_new, max_kv,
+                scale, causal, window, sinks, shared, return_lse,
+                0 if plan_ is None else ctypes.addressof(plan_))
 
 
 def plan_kv_attention(seqs: int, max_new: int, max_kv: int, q_heads: int, kv_heads: int,

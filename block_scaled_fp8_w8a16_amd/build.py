@@ -1,7 +1,8 @@
-"""Build ``libw8a16.so`` (the HIP kernels and their C ABI) for gfx950.
+"""Build ``libw8a16.so`` (the HIP kernels and their C ABI) for gfx950, and
+``_binding.so`` (the native part of the Python binding).
 
-Run as ``python -m block_scaled_fp8_w8a16_amd.build``.  The library is built
-in-tree next to this file so it travels with the source tree.
+Run as ``python -m block_scaled_fp8_w8a16_amd.build``.  Both are built
+in-tree next to this file so they travel with the source tree.
 """
 
 from __future__ import annotations
@@ -16,6 +17,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libw8a16.so")
+BINDING = os.path.join(HERE, "_binding.so")
 
 SOURCES = ["plan.cpp", "api.hip", "stream_kernel.hip", "tile_m64.hip", "tile_m128.hip",
            "stream_epilogue.hip", "ring_epilogue.hip", "tile_epilogue.hip",
@@ -55,12 +57,29 @@ def _compile_cmd(src: str, obj: str) -> list:
             "-I", INCLUDE, "-I", CSRC, "-c", path, "-o", obj]
 
 
+def _binding_cmd(out: str) -> list:
+    """The binding's native part: C++ against torch and CPython, no HIP."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    lib = os.path.join(base, "lib")
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-shared",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I", INCLUDE,
+            "-isystem", os.path.join(base, "include"),
+            "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+            "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "binding.cpp"), "-o", out,
+            "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath," + lib]
+
+
 def build(verbose: bool = False) -> str:
     """Compile every source (in parallel, at most 8 at a time) and link."""
     builddir = os.path.join(HERE, "_build")
     os.makedirs(builddir, exist_ok=True)
     objs = [os.path.join(builddir, src + ".o") for src in SOURCES]
     cmds = [_compile_cmd(src, obj) for src, obj in zip(SOURCES, objs)]
+    binding = BINDING + ".tmp%d" % os.getpid()
+    cmds.append(_binding_cmd(binding))
     if verbose:
         for cmd in cmds:
             print(" ".join(cmd), flush=True)
@@ -74,6 +93,7 @@ def build(verbose: bool = False) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
     os.replace(tmp, LIB)
+    os.replace(binding, BINDING)
     return LIB
 
 
