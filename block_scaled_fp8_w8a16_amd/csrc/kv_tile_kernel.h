@@ -210,10 +210,19 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
                                              16, 0, 0);
         }
     };
+    // Scale bytes through the scalar cache too, out of the aligned words that
+    // hold them.  (As vector loads they were carried in registers from tile
+    // to tile, and the compiler waited for them, hence for every load in
+    // flight, at each turn.)
+    typedef const __attribute__((address_space(4))) uint32_t *scalar_words;
+    auto scalar_byte = [&](const uint8_t *p) {
+        const uintptr_t at = (uintptr_t)p;
+        return *(scalar_words)(at & ~(uintptr_t)3) >> (8u * (uint32_t)(at & 3u)) & 255u;
+    };
     auto scales = [&](const Where &p) {
         Scale s;
-        s.ks = pool.k_scale[p.page * pool.ks_page + p.slot];
-        s.vs = pool.v_scale[p.page * pool.vs_page + p.slot];
+        s.ks = scalar_byte(pool.k_scale + p.page * pool.ks_page + p.slot);
+        s.vs = scalar_byte(pool.v_scale + p.page * pool.vs_page + p.slot);
         return s;       // of page 0 where p.ok is 0
     };
 
@@ -484,7 +493,7 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
         // them there, hence for every load.
         auto turn = [&]() {
             put((buf + 2u) & 3u, was, was_ok);
-            wait_vm<2 * (2 * (DP / 64) + 2)>();
+            wait_vm<2 * 2 * (DP / 64)>();
             barrier_lds();
             ++tile;
             buf = (buf + 1u) & 3u;
