@@ -201,7 +201,7 @@ struct Cost {
     // once share it.
     double tile(uint32_t kernel) const { return (kernel == W8A16_KV_ROWS ? 0.3 : 1.15) * size; }
     // A workgroup's time for one where it has the CU for itself.
-    double alone(uint32_t kernel) const { return (kernel == W8A16_KV_ROWS ? 0.3 : 1.4) * size; }
+    double alone(uint32_t kernel) const { return (kernel == W8A16_KV_ROWS ? 0.3 : 1.25) * size; }
     // The CU with the most workgroups of n.
     double most(double n) const { return n <= cus ? 1.0 : (double)div_up((uint64_t)n, (uint64_t)cus); }
     // Reading n tiles of keys from HBM.

@@ -23,13 +23,17 @@
 //     fall out of step and one's exponentials run under another's matrix
 //     instructions; the second product follows each half's exponentials at
 //     once.
-// What bounds it: the issue of vector instructions (64 % of the time), and at
-// the end of every tile a wait for all loads in flight (see turn() below), so
-// that a tile costs at least its loads' latency: one workgroup alone on a CU
-// takes 1.5 us per tile, two between them 2.3.
+// What bounds it: where two workgroups fill every CU, the rate that the card
+// sustains its matrix instructions at beside the widening of codes (without
+// the widening 434 us in place of 532, a library's rate for plain products;
+// without the exponentials, maxima or sums 520 to 530).  One workgroup alone on
+// a CU takes 1.24 us per tile, two between them 2.2.
 // Measured, 2 x 2048 tokens of 32 query and 8 KV heads over 8192 keys of 128
-// channels: 495 to 530 us by run and card, 908 to 972 TFLOP/s (a plain FP16
-// matrix product of 8192^3 reaches 1151 here).  Tried on forms of this kernel
+// channels: 490 to 520 us by run and card, 925 to 982 TFLOP/s (a plain FP16
+// matrix product of 8192^3 reaches 1151 here).  Operands read from LDS ahead of
+// their use and scale bytes by DMA took 128 channels from 520 to 514 us, 64
+// from 372 to 340, 192 (2 x 1024 tokens over 4024) from 133 to 119, 256 from
+// 184 to 155, windows of 1024 keys from 86 to 82.  Tried on forms of this kernel
 // that took 488 to 508: two buffers and one loop for all tiles 530, no
 // priority 512, widening once per workgroup into LDS as 16-bit operands 584,
 // the next tile's scores under this one's exponentials 602, the raised
@@ -59,6 +63,8 @@ typedef float f32x16_t __attribute__((ext_vector_type(16)));
 
 constexpr uint32_t kRows = 128;      // rows per workgroup
 constexpr uint32_t kBuffers = 4;     // tiles in LDS: one in use, three on their way
+
+__device__ const uint8_t no_scale[4] = {0, 0, 0, 0};
 
 template <class Q> __device__ __forceinline__ f32x16_t mfma32(u32x4_t a, u32x4_t b, f32x16_t c);
 template <> __device__ __forceinline__ f32x16_t mfma32<QueryBf16>(u32x4_t a, u32x4_t b, f32x16_t c)
@@ -92,8 +98,9 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
     constexpr uint32_t BUF = 8 * BLK;       // of one buffer
     constexpr uint32_t SWZ = DP == 128 || DP == 256 ? 7 : 3;
     struct Scale { uint32_t ks, vs; };
+    struct ScaleRow { Scale s, unused[31]; };     // a wave's DMA writes a word per lane
     // kBuffers buffers of K and V codes, then the blocks' scale bytes
-    Scale (*const scl)[4] = reinterpret_cast<Scale (*)[4]>(lds + kBuffers * BUF);
+    ScaleRow (*const scl)[4] = reinterpret_cast<ScaleRow (*)[4]>(lds + kBuffers * BUF);
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t col = lane & 31u, h = lane >> 5;
@@ -209,23 +216,14 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
             __builtin_amdgcn_global_load_lds(vp + voff[j], (lds_void_t *)(lds + buf * BUF + (4 + wave) * BLK + 1024u * j),
                                              16, 0, 0);
         }
+        // The block's scale bytes, of a page that does not exist 0 (no
+        // scale).  By DMA like the codes: as vector loads the compiler waited
+        // for them, hence for every load in flight, a tile later, and as
+        // scalar loads every wait for LDS waited for them.
+        const uint8_t *const kb = p.ok ? pool.k_scale + p.page * pool.ks_page + p.slot : no_scale;
+        const uint8_t *const vb = p.ok ? pool.v_scale + p.page * pool.vs_page + p.slot : no_scale;
+        __builtin_amdgcn_global_load_lds(lane & 1u ? vb : kb, (lds_void_t *)&scl[buf][wave], 1, 0, 0);
     };
-    // Scale bytes through the scalar cache too, out of the aligned words that
-    // hold them.  (As vector loads they were carried in registers from tile
-    // to tile, and the compiler waited for them, hence for every load in
-    // flight, at each turn.)
-    typedef const __attribute__((address_space(4))) uint32_t *scalar_words;
-    auto scalar_byte = [&](const uint8_t *p) {
-        const uintptr_t at = (uintptr_t)p;
-        return *(scalar_words)(at & ~(uintptr_t)3) >> (8u * (uint32_t)(at & 3u)) & 255u;
-    };
-    auto scales = [&](const Where &p) {
-        Scale s;
-        s.ks = scalar_byte(pool.k_scale + p.page * pool.ks_page + p.slot);
-        s.vs = scalar_byte(pool.v_scale + p.page * pool.vs_page + p.slot);
-        return s;       // of page 0 where p.ok is 0
-    };
-
     f32x16_t o[VT];
 #pragma unroll
     for (int x = 0; x < VT; ++x)
@@ -240,16 +238,18 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
     const uint32_t kf = SWZ == 7 ? (krow & 3u) | ((krow >> 4) << 2) : ((krow >> 1) & 1u) | ((krow >> 4) << 1);
     const uint32_t kbase = krow * DP;
 
+    auto k_frag = [&](uint32_t buf, int x, int i) {
+        return *reinterpret_cast<const u32x4_t *>(lds + buf * BUF + x * 2 * BLK + kbase + 16u * ((2u * i + h) ^ kf));
+    };
     // Scores of 32 keys (half x of the tile), as the codes have them.
     auto products = [&](uint32_t buf, int x) {
         f32x16_t s;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             s[i] = 0.f;
-        const uint8_t *const kl = lds + buf * BUF + x * 2 * BLK + kbase;
 #pragma unroll
         for (int i = 0; i < QC; ++i) {
-            const u32x4_t raw = *reinterpret_cast<const u32x4_t *>(kl + 16u * ((2u * i + h) ^ kf));
+            const u32x4_t raw = k_frag(buf, x, i);
             s = mfma32<Q>(Q::widen(raw.x, raw.y), q[i][0], s);
             s = mfma32<Q>(Q::widen(raw.z, raw.w), q[i][1], s);
         }
@@ -313,14 +313,38 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
     auto whole = [&](uint32_t buf) {
         f32x16_t s[2];
         float c[2], e[2], mx[2];
+        // K of the whole tile is under way before its first product, V of a
+        // half before its exponentials or the other half's products.  (Left to
+        // the compiler each pair of reads was waited for.)
+        u32x4_t k[2][QC], v[VT];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int i = 0; i < QC; ++i)
+                k[x][i] = k_frag(buf, x, i);
+        const Scale sc[2] = {scl[buf][h].s, scl[buf][2 + h].s};
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const Scale sc = scl[buf][2 * x + h];
-            __builtin_amdgcn_s_setprio(1);
-            s[x] = products(buf, x);
-            __builtin_amdgcn_s_setprio(0);
-            c[x] = pow2_byte(sc.ks) * a.scale_log2;
-            e[x] = (float)sc.vs - 127.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                s[x][i] = 0.f;
+#pragma unroll
+            for (int i = 0; i < QC; ++i) {
+                s[x] = mfma32<Q>(Q::widen(k[x][i].x, k[x][i].y), q[i][0], s[x]);
+                s[x] = mfma32<Q>(Q::widen(k[x][i].z, k[x][i].w), q[i][1], s[x]);
+            }
+        }
+        __builtin_amdgcn_s_setprio(0);
+#pragma unroll
+        for (int d = 0; d < VT; ++d)
+            v[d] = v_frag(buf, 0, d);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            c[x] = pow2_byte(sc[x].ks) * a.scale_log2;
+            e[x] = (float)sc[x].vs - 127.0f;
             mx[x] = largest(s[x]) * c[x];
         }
         refer(mx, e);
@@ -341,7 +365,9 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
             pack(s[x], p);
 #pragma unroll
             for (int d = 0; d < VT; ++d) {
-                const u32x4_t raw = v_frag(buf, x, d);
+                const u32x4_t raw = v[d];
+                if (x == 0)
+                    v[d] = v_frag(buf, 1, d);
                 o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.x, raw.y, 1.0f), p[0], o[d]);
                 o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.z, raw.w, 1.0f), p[1], o[d]);
             }
@@ -356,7 +382,7 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
         uint32_t poison[2];      // a block without a V scale reads as NaN codes
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const Scale sc = scl[buf][2 * x + h];
+            const Scale sc = scl[buf][2 * x + h].s;
             c[x] = sc.ks - 1u >= 254u ? __builtin_nanf("") : pow2_byte(sc.ks) * a.scale_log2;
             e[x] = (float)sc.vs - 127.0f;
             poison[x] = sc.vs - 1u >= 254u ? 0x7f7f7f7fu : 0u;
@@ -450,57 +476,33 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
         const uint32_t past = list.tile0 - list.front;     // a tile of the range is this much less in the list
         whole0 = whole0 > past + begin ? whole0 - past : begin;
         whole1 = whole1 > past + end ? end : (whole1 > past ? whole1 - past : 0u);
-        // Scale bytes pass through registers and go to LDS a tile after their
-        // load, two tiles before their use, 255 for a block without a scale.
-        Scale sc, was;
-        uint32_t ok, was_ok;
-        auto put = [&](uint32_t in, const Scale &v, uint32_t good) {
-            if (lane == 0)
-                scl[in][wave] = Scale{good && v.ks ? v.ks : 255u, good && v.vs ? v.vs : 255u};
-        };
         // (all of the first tiles' loads before the first wait for one)
         Where at[kBuffers - 1];
-        Scale first[kBuffers - 1];
 #pragma unroll
         for (uint32_t k = 0; k + 1 < kBuffers; ++k)
             at[k] = locate(list.at(begin + k));
 #pragma unroll
-        for (uint32_t k = 0; k + 1 < kBuffers; ++k) {
-            first[k] = scales(at[k]);
-            stage(at[k], k);
-        }
-        Where next = locate(list.at(begin + kBuffers - 1));
-#pragma unroll
         for (uint32_t k = 0; k + 1 < kBuffers; ++k)
-            put(k, first[k], at[k].ok);
-        sc = first[kBuffers - 2];
-        ok = at[kBuffers - 2].ok;
+            stage(at[k], k);
+        Where next = locate(list.at(begin + kBuffers - 1));
         wait_vm<0>();
         __syncthreads();
         uint32_t tile = begin, buf = 0;
         auto ahead = [&]() {
-            was = sc;
-            was_ok = ok;
-            sc = scales(next);
-            ok = next.ok;
             stage(next, (buf + 3u) & 3u);
             next = locate(list.at(tile + kBuffers));
         };
         // The next tile has arrived when no more loads are open than the two
-        // tiles after it take: K and V pieces and two scale bytes each.  The
-        // buffers need no more than that; but the scale bytes carried to the
-        // next turn are widened at its start, and the compiler waits for
-        // them there, hence for every load.
+        // tiles after it take: K and V pieces and the scale bytes each.
         auto turn = [&]() {
-            put((buf + 2u) & 3u, was, was_ok);
-            wait_vm<2 * 2 * (DP / 64)>();
+            wait_vm<2 * (2 * (DP / 64) + 1)>();
             barrier_lds();
             ++tile;
             buf = (buf + 1u) & 3u;
         };
         auto scaled = [&](uint32_t in) {
-            const Scale s = scl[in][lane & 3u];
-            return !__ballot(s.ks == 255u || s.vs == 255u);
+            const Scale s = scl[in][lane & 3u].s;
+            return !__ballot(s.ks - 1u >= 254u || s.vs - 1u >= 254u);
         };
         auto general = [&](uint32_t stop) {
             while (tile < stop) {
@@ -597,7 +599,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void w8a16_kv_tile_kernel(A
 }
 
 // Dynamic LDS: codes and scale bytes.
-template <int DP> constexpr uint32_t tile_lds = kBuffers * (8 * 16 * DP + 4 * 8);
+template <int DP> constexpr uint32_t tile_lds = kBuffers * (8 * 16 * DP + 4 * 64 * 4);
 
 template <class Q, int DP, class Args>
 hipError_t launch_dim(const Args &a, hipStream_t stream)
