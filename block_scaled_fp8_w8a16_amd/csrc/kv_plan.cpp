@@ -280,6 +280,7 @@ int make_kv_shared_plans(uint32_t seqs, uint32_t tokens, uint32_t max_new, uint3
     const uint64_t rows = (uint64_t)tokens * (q_heads / kv_heads);
     double best = given ? 1e30 : 0.95 * one_pass(c, whole, shared_tiles, own_tiles, head_dim);
     auto consider = [&](uint32_t kernel, uint64_t per) {
+        per = per > kMinTiles ? per : kMinTiles;
         w8a16_kv_plan_t p = chunked(kernel, per < shared_tiles ? per : shared_tiles);
         if (div_up(shared_tiles, p.chunk_tiles) > kMaxPassChunks ||
             pass_plan(1, tokens, shared, q_heads, kv_heads, head_dim, &p) != W8A16_OK)

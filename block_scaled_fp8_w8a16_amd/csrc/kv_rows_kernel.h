@@ -632,6 +632,8 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
 // over a shared prefix: one wave per (row, KV head).  Its lanes are groups of
 // dim / 4, four channels each, that take the chunks in turn; the groups' sums
 // are added in group order.
+constexpr uint32_t kJoinAhead = 8;
+
 template <class E, class Args>
 __global__ __launch_bounds__(256) void w8a16_kv_join_kernel(Args a, uint32_t tile_rows,
                                                             uint32_t rows_used, uint32_t rows_all,
@@ -652,12 +654,15 @@ __global__ __launch_bounds__(256) void w8a16_kv_join_kernel(Args a, uint32_t til
     const uint32_t row = t.row0 + r;
     if (row >= t.rows)
         return;
-    tile_range(a, tile_rows, t);
-    const uint32_t tiles = TileList(a, t).tiles;
-    if (tiles <= a.chunk_tiles && !is_suffix<Args>)
-        return;      // one chunk: its workgroup has stored the row
-    uint32_t n = (tiles + a.chunk_tiles - 1) / a.chunk_tiles;
-    n = n < a.chunks ? n : a.chunks;
+    uint32_t n = 1;
+    if (!is_suffix<Args> || a.chunks > 1) {     // (else known before the sequence's length)
+        tile_range(a, tile_rows, t);
+        const uint32_t tiles = TileList(a, t).tiles;
+        if (tiles <= a.chunk_tiles && !is_suffix<Args>)
+            return;      // one chunk: its workgroup has stored the row
+        n = (tiles + a.chunk_tiles - 1) / a.chunk_tiles;
+        n = n < a.chunks ? n : a.chunks;
+    }
     const uint32_t own_chunks = n ? n : 1u;
     if constexpr (is_suffix<Args>)      // the prefix's after the row's own
         n = own_chunks + a.prefix_chunks;
@@ -679,43 +684,55 @@ __global__ __launch_bounds__(256) void w8a16_kv_join_kernel(Args a, uint32_t til
         return *reinterpret_cast<const f32x4_t *>(wo + (size_t)c * tile_rows * dim + d);
     };
 
+    // The lanes' pieces of the first chunks are under way before the
+    // statistics have come.
+    const uint32_t grp = lane / per, d = lane % per * 4u;
+    f32x4_t v[kJoinAhead];
+    auto fetch = [&](uint32_t base, uint32_t stop) {
+#pragma unroll
+        for (uint32_t u = 0; u < kJoinAhead; ++u) {
+            const uint32_t c = base + u * groups + grp;
+            v[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            if (c < stop && grp < groups)
+                v[u] = part_of(c, d);
+        }
+    };
+    fetch(0, n < 64u ? n : 64u);
     // the row's largest references over all chunks
     float m = kUnset, ex = kUnset;
+    f32x4_t st = {kUnset, 0.f, kUnset, 0.f};
     for (uint32_t c = lane; c < n; c += 64u) {
-        const f32x4_t st = stat_of(c);
-        m = fmaxf(m, st.x);
-        ex = fmaxf(ex, st.z);
+        const f32x4_t x = stat_of(c);
+        st = c < 64u ? x : st;
+        m = fmaxf(m, x.x);
+        ex = fmaxf(ex, x.z);
     }
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) {
         m = fmaxf(m, __shfl_xor(m, off, 64));
         ex = fmaxf(ex, __shfl_xor(ex, off, 64));
     }
-    const uint32_t grp = lane / per, d = lane % per * 4u;
     f32x4_t own = {0.f, 0.f, 0.f, 0.f};
     float l = 0.f;       // this lane's chunks c = lane, lane + 64, ...
     for (uint32_t c0 = 0; c0 < n; c0 += 64u) {
         float fac = 0.f;
         if (c0 + lane < n) {
-            const f32x4_t st = stat_of(c0 + lane);
+            if (c0)
+                st = stat_of(c0 + lane);
             l += exp2_fast(st.x - m) * st.y;
             fac = exp2_fast(st.z - ex);
         }
+        // all lanes: each lends its factor
         const uint32_t stop = n - c0 < 64u ? n - c0 : 64u;
-        for (uint32_t base = 0; base < stop; base += 4u * groups) {    // all lanes: each lends its factor
-            f32x4_t v[4];
-            float f[4];
+        for (uint32_t base = 0; base < stop; base += kJoinAhead * groups) {
+            if (c0 + base)
+                fetch(c0 + base, c0 + stop);
 #pragma unroll
-            for (uint32_t u = 0; u < 4; ++u) {
+            for (uint32_t u = 0; u < kJoinAhead; ++u) {
                 const uint32_t c = base + u * groups + grp;
-                v[u] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-                if (c < stop && grp < groups)
-                    v[u] = part_of(c0 + c, d);
-                f[u] = __shfl(fac, (int)(c & 63u), 64);
+                const float f = __shfl(fac, (int)(c & 63u), 64);
+                own += (c < stop ? f : 0.f) * v[u];
             }
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                own += f[u] * v[u];
         }
     }
 #pragma unroll
