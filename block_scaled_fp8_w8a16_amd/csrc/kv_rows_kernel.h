@@ -632,7 +632,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 && WAVES == 4 ? 2 : 1) void w
 // over a shared prefix: one wave per (row, KV head).  Its lanes are groups of
 // dim / 4, four channels each, that take the chunks in turn; the groups' sums
 // are added in group order.
-constexpr uint32_t kJoinAhead = 8;
+constexpr uint32_t kJoinAhead = 4;
 
 template <class E, class Args>
 __global__ __launch_bounds__(256) void w8a16_kv_join_kernel(Args a, uint32_t tile_rows,
