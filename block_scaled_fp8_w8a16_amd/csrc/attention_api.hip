@@ -599,7 +599,7 @@ int kv_attention(const char *entry, const w8a16_kv_cache_t *cache, const w8a16_k
     if (e != hipSuccess)
         return named(hip_fail(e, "kernel launch"), entry);
     if (log_enabled()) {
-        char line[512];
+        char line[768];
         int n = snprintf(line, sizeof line,
                          "w8a16: %s tokens=%u seqs=%u q_heads=%u kv_heads=%u head_dim=%u max_new=%u max_kv=%u "
                          "window=%u", entry, seqs->tokens, seqs->seqs, g->q_heads, cache->kv_heads,

@@ -120,6 +120,17 @@ void *stream_of(PyObject *o)
     return p;
 }
 
+// Other Python threads run while a call is enqueued (or its workspace grows).
+struct Unlocked {
+    PyThreadState *const state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <class F, class... A> int unlocked(F f, A... args)
+{
+    const Unlocked u;
+    return f(args...);
+}
+
 struct Rows {
     int64_t token, head;
 };
@@ -265,7 +276,7 @@ w8a16_kv_seqs_t seqs_of(PyObject *block_table, PyObject *kv_lens, PyObject *cu_s
     s.block_table = static_cast<const int32_t *>(bt.const_data_ptr());
     s.kv_lens = static_cast<const int32_t *>(lens.const_data_ptr());
     const int64_t pitch = n > 1 ? bt.stride(0) : width;
-    require(pitch >= 0, "block_table rows must follow each other");
+    require(pitch >= 0 && pitch <= 0xffffffffll, "block_table rows must be at most 2^32 - 1 places apart");
     s.block_table_stride = u32(pitch);
     s.block_table_width = u32(width);
     s.seqs = u32(n);
@@ -309,16 +320,17 @@ PyObject *rope(PyObject *const *o)
     int st;
     if (given(o[6])) {
         const w8a16_axes_t a = axes(o[2], tokens, o[6], o[7], table.size(1), dev);
-        st = f_rope_axes(x.const_data_ptr(), xr.token, xr.head, y.data_ptr(), yr.token, yr.head, code, u32(tokens),
-                         u32(heads), u32(dim), tp, u32(table.size(0)), &a, layout, truth(o[5]), stream_of(o[8]));
+        st = unlocked(f_rope_axes, x.const_data_ptr(), xr.token, xr.head, y.data_ptr(), yr.token, yr.head, code,
+                      u32(tokens), u32(heads), u32(dim), tp, u32(table.size(0)), &a, layout, truth(o[5]),
+                      stream_of(o[8]));
     } else {
         const Tensor &p = tensor(o[2], "positions");
         require(p.dim() == 1 && p.size(0) == tokens && p.scalar_type() == ScalarType::Int && p.is_contiguous() &&
                     dev.has(p),
                 "positions must be a contiguous int32 GPU tensor [tokens]");
-        st = f_rope(x.const_data_ptr(), xr.token, xr.head, y.data_ptr(), yr.token, yr.head, code, u32(tokens),
-                    u32(heads), u32(dim), tp, u32(table.size(0)), u32(2 * table.size(1)),
-                    static_cast<const int32_t *>(p.const_data_ptr()), layout, truth(o[5]), stream_of(o[8]));
+        st = unlocked(f_rope, x.const_data_ptr(), xr.token, xr.head, y.data_ptr(), yr.token, yr.head, code,
+                      u32(tokens), u32(heads), u32(dim), tp, u32(table.size(0)), u32(2 * table.size(1)),
+                      static_cast<const int32_t *>(p.const_data_ptr()), layout, truth(o[5]), stream_of(o[8]));
     }
     if (st)
         return status(st);
@@ -385,7 +397,8 @@ PyObject *kv_append(PyObject *const *o)
         a.q_heads = u32(hq);
     }
     void *stream = stream_of(o[14]);
-    const int st = by_axes ? f_kv_append_axes(&c, &s, &a, &ax, stream) : f_kv_append(&c, &s, &a, stream);
+    const int st = by_axes ? unlocked(f_kv_append_axes, &c, &s, &a, &ax, stream)
+                           : unlocked(f_kv_append, &c, &s, &a, stream);
     if (st)
         return status(st);
     if (!queries)
@@ -437,9 +450,9 @@ PyObject *kv_attention(PyObject *const *o)
     int st;
     if (sinks || shared) {
         const w8a16_kv_span_t span = {u32(sinks), u32(shared)};
-        st = f_kv_attention_span(&c, &s, &a, &span, stream);
+        st = unlocked(f_kv_attention_span, &c, &s, &a, &span, stream);
     } else {
-        st = f_kv_attention(&c, &s, &a, stream);
+        st = unlocked(f_kv_attention, &c, &s, &a, stream);
     }
     if (st)
         return status(st);
@@ -462,7 +475,7 @@ uint32_t rows2(const char *name, const Tensor &t, int64_t m, int64_t n, bool f32
     if (t.stride(1) != 1 && n > 1)
         throw Refused(std::string(name) + " needs a unit column stride");
     const int64_t rs = t.stride(0);
-    require(rs >= 0 || m < 2, "rows must follow each other");
+    require(m < 2 || (rs >= 0 && rs <= 0xffffffffll), "rows must be at most 2^32 - 1 elements apart");
     return u32(m > 1 ? rs : rs < n ? n : rs);
 }
 
@@ -513,9 +526,9 @@ PyObject *gemm_epilogue(PyObject *const *o)
         made = at::empty({m, n}, given(o[8]) && truth(o[8]) ? a.options().dtype(ScalarType::Float) : a.options());
     const Tensor &c = given(o[3]) ? THPVariable_Unpack(o[3]) : made;
     e.out_dtype = dtype_code(c.scalar_type());
-    const int st = f_gemm_epilogue(a.const_data_ptr(), ars, w.const_data_ptr(),
-                                   static_cast<const float *>(scale.const_data_ptr()), c.data_ptr(), crs, u32(m),
-                                   u32(n), u32(k), &e, stream_of(o[9]));
+    const int st = unlocked(f_gemm_epilogue, a.const_data_ptr(), ars, w.const_data_ptr(),
+                            static_cast<const float *>(scale.const_data_ptr()), c.data_ptr(), crs, u32(m), u32(n),
+                            u32(k), &e, stream_of(o[9]));
     if (st)
         return status(st);
     return given(o[3]) ? Py_NewRef(o[3]) : THPVariable_Wrap(made);

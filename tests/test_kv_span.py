@@ -298,6 +298,28 @@ def test_shared(w8, case, chunk):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("chunk", [1, 64])
+def test_shared_of_padded_slots_and_lost_tokens(w8, chunk):
+    """Slots without tokens, tokens in front of position 0 and tokens that no
+    sequence brings give zeros; a negative length is an empty slot."""
+    rng = np.random.default_rng(14)
+    new, totals, shared = [2, 2, 2, 2], [0, 1, 90, 300], 64
+    cache, table, q = make(rng, new, totals, 4, 2, 64, 16, "bf16", shared)
+    dev = cache.to(w8)
+    kw = dict(shared=shared, plan_=own_plan(w8, new, 2, chunk=chunk))
+    want = attention(q.astype(np.float64), cache, table, totals, new, 2, 64 ** -0.5, True, 0, 0)
+    compare(*call(w8, dev, table, q, "bf16", new, totals, **kw), want, "bf16")
+    cu, bt = i32([1, 3, 3, 5, 6]), cuda(table.astype(np.int32))
+    lens = [1, -3, 90, 300]
+    # (the first sequence counts a token whose page is not the others': its rows are not defined)
+    want = attention(q[3:6].astype(np.float64), cache, table[2:], lens[2:], [2, 1], 2, 64 ** -0.5, True, 0, 0)
+    out, lse = w8.kv_attention(cuda(q, DT["bf16"]), dev, bt, i32(lens), cu_seqlens=cu, max_new=2, return_lse=True,
+                               **kw)
+    assert (out[[0, 6, 7]] == 0).all() and lse[[0, 6, 7]].isneginf().all()
+    compare(out[3:6], lse[3:6], want, "bf16")
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("case", [([1] * 12, [1600 + 37 * i for i in range(12)], 1536, 8, 2, 128, 64, "bf16"),
                                   ([1] * 64, [2100 + 3 * i for i in range(64)], 2048, 4, 1, 64, 32, "fp16"),
                                   ([2] * 30, [1100 + 3 * i for i in range(30)], 1024, 16, 2, 256, 64, "bf16")],

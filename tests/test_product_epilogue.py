@@ -235,3 +235,37 @@ def test_refusals_of_tensors(w8):
             w8.gemm_epilogue(a, w, scale, **kw)
     with pytest.raises(w8.W8A16Error):      # rows of the gate on top of each other
         w8.gemm_epilogue(a, w, scale, gate=ok[:1].expand(2, 24))
+
+
+@pytest.mark.gpu
+def test_rows_too_far_apart_are_refused(w8):
+    _, w, scale, _ = operands(2, 24, 128, 1)
+    far = torch.empty((1 << 32) + 128, dtype=BF16, device="cuda").as_strided((2, 128), (1 << 32, 1))
+    with pytest.raises(ValueError, match="apart"):
+        w8.gemm_epilogue(far, w, scale)
+
+
+@pytest.mark.gpu
+def test_two_threads(w8):
+    """Threads on streams of their own get what one gets."""
+    import threading
+
+    a, w, scale, _ = operands(1, 1024, 8192, 6)      # cut along k: the streams' workspaces
+    rows = [a * (i + 1) for i in range(4)]
+    want = [w8.gemm_epilogue(x, w, scale, activation="silu") for x in rows]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    torch.cuda.synchronize()
+
+    def work(i):
+        for n in range(40):
+            got[i].append(w8.gemm_epilogue(rows[(n + i) % 4], w, scale, activation="silu", stream=streams[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert len(got[i]) == 40 and all(torch.equal(y, want[(n + i) % 4]) for n, y in enumerate(got[i]))
