@@ -291,18 +291,26 @@ template <class Args> constexpr bool is_prefix = std::is_same<Args, PrefixArgs>:
 template <class Args> constexpr bool is_suffix = std::is_same<Args, SuffixArgs>::value;
 
 // The tiles a row tile goes over, numbered from 0: those of its sinks, as far
-// as they lie before its range, then its range's.
+// as they lie before its range, then its range's.  apart: all of the sinks',
+// then those of its range behind the sinks (so one tile can be in both parts).
 struct TileList {
     uint32_t front, tile0, tiles;
-    template <class Args> __device__ __forceinline__ TileList(const Args &a, const RowTile &t)
+    template <class Args> __device__ __forceinline__ TileList(const Args &a, const RowTile &t, bool apart = false)
     {
-        tile0 = (uint32_t)t.lo / kKvTile;
+        uint32_t lo = (uint32_t)t.lo;
         front = 0;
         if constexpr (has_sinks<Args>) {
-            const uint32_t n = (a.sinks - 1u) / kKvTile + 1u;
-            front = n < tile0 ? n : tile0;
+            const uint32_t hi = (uint32_t)t.hi, sinks = a.sinks < hi ? a.sinks : hi;
+            const uint32_t n = apart ? (sinks + kKvTile - 1) / kKvTile : (a.sinks - 1u) / kKvTile + 1u;
+            if (apart)
+                lo = lo > sinks ? lo : sinks;
+            front = apart || n < lo / kKvTile ? n : lo / kKvTile;
+            if (apart && lo >= hi)
+                lo = n * kKvTile;      // (all of the range is sinks)
         }
-        tiles = ((uint32_t)t.hi + kKvTile - 1) / kKvTile - tile0 + front;
+        tile0 = lo / kKvTile;
+        const uint32_t end = ((uint32_t)t.hi + kKvTile - 1) / kKvTile;
+        tiles = (end > tile0 ? end - tile0 : 0u) + front;
     }
     __device__ __forceinline__ uint32_t at(uint32_t n) const { return n < front ? n : n - front + tile0; }
 };

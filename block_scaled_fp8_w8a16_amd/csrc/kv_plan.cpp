@@ -17,12 +17,14 @@ constexpr uint64_t kCutTiles = 10;     // that a cut has to spare, and one more
 uint64_t div_up(uint64_t a, uint64_t b) { return (a + b - 1) / b; }
 
 // The tiles a row tile can see: all of the cache, or the window's, those its
-// rows' positions add, and the sinks'; at least one.
-uint64_t tiles_of(uint32_t max_new, uint32_t max_kv, uint32_t window, uint32_t sinks)
+// rows' positions add, and the sinks'; at least one.  (Without sinks the
+// positions of all rows count, which is more than enough.)
+uint64_t tiles_of(uint32_t max_new, uint32_t max_kv, uint32_t window, uint32_t sinks, uint64_t tile_tokens)
 {
     uint64_t keys = max_kv;
-    if (window && (uint64_t)window + max_new < keys)
-        keys = (uint64_t)window + max_new;
+    const uint64_t span = window + (sinks && tile_tokens < max_new ? tile_tokens : (uint64_t)max_new);
+    if (window && span < keys)
+        keys = span;
     uint64_t tiles = div_up(keys, kKeysPerTile) + (window ? 1 : 0);
     if (window && sinks) {
         tiles += div_up(sinks, kKeysPerTile);
@@ -49,7 +51,7 @@ int kv_plan_finalize(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t 
                                         "W8A16_KV_TILE with row_blocks 8 and 4 waves, and "
                                         "chunk_tiles of at least 1");
     const uint64_t tile_rows = 16ull * p->row_blocks, rows = (uint64_t)max_new * (q_heads / kv_heads);
-    const uint64_t tiles = tiles_of(max_new, max_kv, window, sinks);
+    const uint64_t tiles = tiles_of(max_new, max_kv, window, sinks, tile_rows / (q_heads / kv_heads) + 2);
     const uint64_t row_tiles = div_up(rows, tile_rows), chunks = div_up(tiles, p->chunk_tiles);
     const uint64_t grid = (uint64_t)seqs * kv_heads * row_tiles * chunks;
     if (grid * 64ull * p->waves > kMaxThreads)
@@ -108,7 +110,7 @@ int make_kv_plan(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_he
     int st = kv_plan_finalize(seqs, max_new, max_kv, q_heads, kv_heads, head_dim, window, &p, sinks);
     if (st != W8A16_OK)
         return st;
-    const uint64_t tiles = tiles_of(max_new, max_kv, window, sinks);
+    const uint64_t tiles = tiles_of(max_new, max_kv, window, sinks, 16ull * p.row_blocks / (q_heads / kv_heads) + 2);
     // Cut the keys while that leaves no more workgroups than run at once: two
     // per CU, one of 8 waves or of heads above 128 channels.  Eight waves
     // where the row tiles alone do not give every CU a workgroup: half as

@@ -657,7 +657,7 @@ __global__ __launch_bounds__(256) void w8a16_kv_join_kernel(Args a, uint32_t til
     uint32_t n = 1;
     if (!is_suffix<Args> || a.chunks > 1) {     // (else known before the sequence's length)
         tile_range(a, tile_rows, t);
-        const uint32_t tiles = TileList(a, t).tiles;
+        const uint32_t tiles = TileList(a, t, true).tiles;
         if (tiles <= a.chunk_tiles && !is_suffix<Args>)
             return;      // one chunk: its workgroup has stored the row
         n = (tiles + a.chunk_tiles - 1) / a.chunk_tiles;

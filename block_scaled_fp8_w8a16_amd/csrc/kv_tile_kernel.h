@@ -126,7 +126,7 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
     if (t.row0 >= t.rows)
         return;
     tile_range(a, kRows, t);
-    const TileList list(a, t);
+    const TileList list(a, t, true);
     const uint32_t tiles = list.tiles;
     const uint32_t begin = chunk * a.chunk_tiles;
     if (begin >= tiles && chunk > 0 && !is_prefix<Args>)
@@ -134,8 +134,6 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
     const uint32_t end = chunk + 1 == a.chunks || begin + a.chunk_tiles > tiles
                              ? tiles : begin + a.chunk_tiles;
     const bool alone = !is_prefix<Args> && !is_suffix<Args> && (a.chunks == 1 || tiles <= a.chunk_tiles);
-    const int32_t sinks = sinks_of(a);
-    auto before_sinks = [&](int32_t key) { return has_sinks<Args> && key < sinks; };
 
     // this wave's rows, and the keys they see
     RowTile w = t;
@@ -147,6 +145,13 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
     const uint32_t row = w.row0 + col;
     int32_t rlo, rhi;
     row_range(a, t, row, rlo, rhi);
+    const bool none = rhi <= rlo;
+    if constexpr (has_sinks<Args>) {      // what is seen behind the sinks
+        const int32_t sinks = (int32_t)a.sinks;
+        rlo = rlo > sinks ? rlo : sinks;
+        w.lo = w.lo > sinks ? w.lo : sinks;
+        t.all_lo = t.all_lo > sinks ? t.all_lo : sinks;
+    }
     const uint32_t tok = a.by_group.div(row), hq = head * a.group + row - tok * a.group;
     u32x4_t q[QC][2];
     {
@@ -309,6 +314,18 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
             p[i >> 2][i & 3] = f16_pair(s[2 * i], s[2 * i + 1]);
     };
 
+    // What is seldom needed of the arguments is read where it is: loaded with
+    // the others it would stay in scalar registers, or be moved out of them
+    // and back, all through the loop (the outputs' strides, windows of 1000
+    // keys of 64 channels: 71.3 us, so 67.8).
+    typedef const __attribute__((address_space(4))) Args *args_ptr;
+    auto late_args = [&]() {
+        args_ptr late = (args_ptr)((const __attribute__((address_space(4))) uint8_t *)
+                                       __builtin_amdgcn_kernarg_segment_ptr() + AT);
+        asm volatile("" : "+s"(late));
+        return late;
+    };
+
     // A tile that every row of the workgroup sees, its blocks all with scales.
     auto whole = [&](uint32_t buf) {
         f32x16_t s[2];
@@ -375,7 +392,16 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
     };
 
     // Any tile: some rows may not see all of it, blocks may have no scale.
-    auto partly = [&](uint32_t tile, uint32_t buf) {
+    // first: one of the sinks', of which no other keys are seen.
+    auto partly = [&](uint32_t tile, uint32_t buf, bool first) {
+        int32_t lo = rlo, hi = rhi, wlo = w.lo, whi = w.hi;
+        if constexpr (has_sinks<Args>)
+            if (first) {
+                const int32_t sinks = (int32_t)late_args()->sinks;
+                lo = wlo = 0;
+                hi = hi < sinks ? hi : sinks;
+                whi = whi < sinks ? whi : sinks;
+            }
         const int32_t tk = (int32_t)(tile * kKvTile), key0 = tk + 16 * (int32_t)h;   // of half x: + 32 x
         f32x16_t s[2];
         float c[2], e[2], mx[2];
@@ -389,8 +415,7 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
             s[x] = products(buf, x);
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-                s[x][i] = (key0 + 32 * x + i >= rlo || before_sinks(key0 + 32 * x + i)) && key0 + 32 * x + i < rhi
-                              ? s[x][i] : kNegInf;
+                s[x][i] = key0 + 32 * x + i >= lo && key0 + 32 * x + i < hi ? s[x][i] : kNegInf;
             mx[x] = largest(s[x]) * c[x];
         }
         refer(mx, e);
@@ -412,7 +437,7 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int32_t key = key0 + 32 * x + 4 * i + j;
-                    keep |= (key >= w.lo || before_sinks(key)) && key < w.hi ? 0xffu << (8 * j) : 0u;
+                    keep |= key >= wlo && key < whi ? 0xffu << (8 * j) : 0u;
                 }
                 v[i] &= keep;
             }
@@ -423,24 +448,13 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
         for (int d = 0; d < VT; ++d)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                // 0 * NaN must not reach rows that do not see the key.  (With
-                // sinks, which add such a tile to most row tiles, pieces
-                // without a NaN are left as they are: a window of 1024 keys
-                // with 4 sinks 97.1 us, so 94.3.  Without them the rest of
-                // the kernel got worse registers: a prompt chunk 509, so 522.)
-                u32x4_t raw = v_frag(buf, x, d);
-                uint32_t odd = poison[x];
+                // 0 * NaN must not reach rows that do not see the key
+                u32x4_t raw = kept(x, d);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    odd |= nan_bytes(raw[i]);
-                if (!has_sinks<Args> || __ballot(odd != 0)) {
-                    raw = kept(x, d);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t nan = nan_bytes(raw[i]);
-                        any |= nan;
-                        raw[i] &= ~((nan >> 7) * 0xffu);
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t nan = nan_bytes(raw[i]);
+                    any |= nan;
+                    raw[i] &= ~((nan >> 7) * 0xffu);
                 }
                 o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.x, raw.y, 1.0f), p[x][0], o[d]);
                 o[d] = mfma32<QueryF16>(f16_from_fp8x8(raw.z, raw.w, 1.0f), p[x][1], o[d]);
@@ -467,8 +481,8 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
                     for (int i = 0; i < 8; ++i) {
                         const int32_t key = key0 + 32 * x + 2 * i;
                         seen[i >> 2][i & 3] =
-                            ((key >= rlo || before_sinks(key)) && key < rhi ? 0x3c00u : 0u) |
-                            ((key + 1 >= rlo || before_sinks(key + 1)) && key + 1 < rhi ? 0x3c000000u : 0u);
+                            (key >= lo && key < hi ? 0x3c00u : 0u) |
+                            (key + 1 >= lo && key + 1 < hi ? 0x3c000000u : 0u);
                     }
                     n = mfma32<QueryF16>(bad[0], seen[0], n);
                     n = mfma32<QueryF16>(bad[1], seen[1], n);
@@ -483,10 +497,11 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
     if (begin < end) {
         // Tiles every row of the workgroup sees run in a loop of their own; it
         // ends early at a block without a scale.
-        uint32_t whole0 = ((uint32_t)t.all_lo + kKvTile - 1) / kKvTile, whole1 = (uint32_t)t.all_hi / kKvTile;
-        const uint32_t past = list.tile0 - list.front;     // a tile of the range is this much less in the list
-        whole0 = whole0 > past + begin ? whole0 - past : begin;
-        whole1 = whole1 > past + end ? end : (whole1 > past ? whole1 - past : 0u);
+        const int32_t past = (int32_t)list.tile0 - (int32_t)list.front;   // a tile of the range is this much less in the list
+        const int32_t w0 = (t.all_lo + (int32_t)kKvTile - 1) / (int32_t)kKvTile - past;
+        const int32_t w1 = t.all_hi / (int32_t)kKvTile - past;
+        const uint32_t whole0 = w0 > (int32_t)begin ? (uint32_t)w0 : begin;
+        const uint32_t whole1 = w1 > (int32_t)end ? end : w1 > 0 ? (uint32_t)w1 : 0u;
         // (all of the first tiles' loads before the first wait for one)
         Where at[kBuffers - 1];
 #pragma unroll
@@ -499,9 +514,13 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
         wait_vm<0>();
         __syncthreads();
         uint32_t tile = begin, buf = 0;
-        auto ahead = [&]() {
+        // (behind the sinks' tiles: whether the tile at hand is)
+        auto place = [&](uint32_t n, auto behind) {
+            return decltype(behind)::value ? n + (uint32_t)past : list.at(n);
+        };
+        auto ahead = [&](auto behind) {
             stage(next, (buf + 3u) & 3u);
-            next = locate(list.at(tile + kBuffers));
+            next = locate(place(tile + kBuffers, behind));
         };
         // The next tile has arrived when no more loads are open than the two
         // tiles after it take: K and V pieces and the scale bytes each.
@@ -515,22 +534,24 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
             const Scale s = scl[in][lane & 3u].s;
             return !__ballot(s.ks - 1u >= 254u || s.vs - 1u >= 254u);
         };
-        auto general = [&](uint32_t stop) {
+        auto general = [&](uint32_t stop, auto behind) {
             while (tile < stop) {
-                ahead();
-                const int32_t tk = (int32_t)(list.at(tile) * kKvTile);
-                if (tk < w.hi && (tk + (int32_t)kKvTile > w.lo || before_sinks(tk)))   // some key of it is for this wave
-                    partly(list.at(tile), buf);
+                ahead(behind);
+                const uint32_t at_tile = place(tile, behind);
+                const int32_t tk = (int32_t)(at_tile * kKvTile);
+                const bool first = has_sinks<Args> && !decltype(behind)::value && tile < list.front;
+                if (tk < w.hi && (tk + (int32_t)kKvTile > w.lo || first))      // some key of it is for this wave
+                    partly(at_tile, buf, first);
                 turn();
             }
         };
-        general(whole0 < end ? whole0 : end);
+        general(whole0 < end ? whole0 : end, std::false_type{});
         while (tile < whole1 && scaled(buf)) {
-            ahead();
+            ahead(std::true_type{});
             whole(buf);
             turn();
         }
-        general(end);
+        general(end, std::true_type{});
         wait_vm<0>();
     }
 
@@ -538,15 +559,7 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
     l += __shfl_xor(l, 32, 64);
     if (row >= t.rows)
         return;
-    // What only the outputs need of the arguments is read
-    // here: loaded with the others it would stay in scalar registers, or be
-    // moved out of them and back, all through the loop (windows of 1000 keys,
-    // 64 channels: 71.3 us, so 67.8).
-    typedef const __attribute__((address_space(4))) Args *args_ptr;
-    args_ptr late = (args_ptr)((const __attribute__((address_space(4))) uint8_t *)
-                                   __builtin_amdgcn_kernarg_segment_ptr() + AT);
-    asm volatile("" : "+s"(late));
-    const bool none = rhi <= rlo;
+    const args_ptr late = late_args();
     if (alone) {
         const float inv = none ? 0.f : 1.0f / l;
         const float unit = m.out - m.sum;
