@@ -185,12 +185,18 @@ w8a16_kv_plan_t chunked(uint32_t kernel, uint64_t chunk_tiles)
 }
 
 // Times of the attention over caches with a shared part, in us, to choose
-// between one pass and two and between their chunks.  Fitted to 8 KV heads
-// of 128 channels, 2 to 128 sequences of 1 to 250 new tokens behind 512 to
-// 30016 shared ones; most of some 300 times agree within 10 %, e.g. 64
-// sequences of 32 heads behind 8192 with 8, 16 and 4 tiles to a chunk: 32.9,
-// 41.1 and 43.5 (here 35, 39, 42), one pass 89.9 (90); 128 of up to 2000 own
-// tokens with 32 and 16: 85.7 and 92.8 (88, 92).
+// between one pass and two and between their chunks.  Fitted to some 300
+// times of 8 KV heads of 128 channels, 2 to 128 sequences of 1 to 250 new
+// tokens behind 512 to 30016 shared ones; most agree within 10 %.  One pass
+// and two, and what is chosen, 32 query heads, one new token:
+//     2 sequences of  100 own tokens behind   512    8.8  10.1  one
+//     2 of  100 behind  8192   13.1  13.6  two;     64 channels   9.8  10.5  two
+//     6 of  333 behind  1984   12.0  11.8  two;     64 channels   9.7  10.2  two
+//    16 of  400 behind  1984   16.5  12.3  two;     64 channels  11.4  10.2  two
+//    64 of  700 behind   512   22.0  25.7  one;    behind 8192   89.5  38.3  two
+//   128 of 2000 behind   512   96    115   one;    behind 30016  606   158   two
+// and 24 of 4 new tokens and 101 own behind 1984 17.5 and 22.8 (one), behind
+// 8192 46.0 and 36.0 (two; 64 channels 26.8 and 28.6, two, the farthest off).
 struct Cost {
     double cus, slots, size;       // size: of a tile against 128 channels' (above them a CU holds one
                                    // workgroup, and its loads wait more)

@@ -1,6 +1,6 @@
 // Attention of many rows (prompts, prompt chunks) over the paged FP8 cache.
 //
-// The mathematics is that of the row kernel (kv_attention.hip): S^T = K Q^T,
+// The mathematics is that of the row kernel (kv_rows_kernel.h): S^T = K Q^T,
 // l += 2^(x - m), O^T += V^T p^T, p = 2^(x + e - M + 11) in FP16, V as its
 // codes.
 // A wave needs about 320 vector instructions (128 conversions of codes, 34
@@ -33,7 +33,11 @@
 // matrix product of 8192^3 reaches 1151 here).  Operands read from LDS ahead of
 // their use and scale bytes by DMA took 128 channels from 520 to 514 us, 64
 // from 372 to 340, 192 (2 x 1024 tokens over 4024) from 133 to 119, 256 from
-// 184 to 155, windows of 1024 keys from 86 to 82.  Tried on forms of this kernel
+// 184 to 155, windows of 1024 keys from 86 to 82.  Windows of 1024 keys with 4
+// sinks, 2 x 1501 tokens: 82 to 88, without the sinks 74 to 77 (a tile more,
+// seen in part).  While the loop of whole tiles asked for each tile whether
+// it was the sinks' or the window's that took 97: 14 moves of spilled scalar
+// registers a tile.  Tried on forms of this kernel
 // that took 488 to 508: two buffers and one loop for all tiles 530, no
 // priority 512, widening once per workgroup into LDS as 16-bit operands 584,
 // the next tile's scores under this one's exponentials 602, the raised

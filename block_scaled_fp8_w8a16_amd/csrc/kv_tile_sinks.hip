@@ -1,4 +1,4 @@
-// The tile kernels of windows with sinks.
+// The tile kernels of windows with sinks (figures in kv_tile_kernel.h).
 
 #include "kv_tile_kernel.h"
 

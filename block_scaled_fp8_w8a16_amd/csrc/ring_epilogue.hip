@@ -1,4 +1,4 @@
-// The ring kernels with an epilogue.
+// The ring kernels with an epilogue (as in stream_epilogue.hip).
 
 #include "ring_kernel.h"
 
