@@ -3,8 +3,8 @@
 // stores them; with splits the reduction does (split_reduce.hip), a thread
 // for four adjacent outputs.
 // 123 x 8190 x 8192 with a bias, GELU and an FP32 residual and output: 33.5 to
-// 35 us (30 for the product, 5.6 to 6 for the reduction of two splits, whose
-// partial sums are 8 MB each way); 16.5 GFLOP are 13.6 us at a library's
+// 35 us (30 for the product, 5.6 to 6 for the reduction of four splits, whose
+// partial sums are 17 MB each way); 16.5 GFLOP are 13.6 us at a library's
 // rate, its 77 MB 15.1.
 #include "tile_kernel.h"
 
