@@ -394,6 +394,45 @@ def test_captured_and_on_another_stream(w8, window, shared):
         compare(out, lse, want, "bf16")
 
 
+# Every width and type is a kernel of its own: rows or tiles of a window, with
+# and without sinks, and of the pairs of passes over a prefix.
+BUILDS = {
+    # new, totals, page, call
+    "window, rows": ([1, 3], [200, 333], 16, dict(window=100)),
+    "window, tiles": ([70, 40], [200, 333], 16, dict(window=100)),
+    "sinks, rows": ([1, 3], [200, 333], 16, dict(window=100, sinks=70)),
+    "sinks, tiles": ([70, 40], [200, 333], 16, dict(window=100, sinks=70)),
+    "rows, rows": ([1, 2, 1], [270, 300, 150], 32, dict(shared=256)),
+    "tiles, rows": ([1] * 96, [8194 + i % 40 for i in range(96)], 64, dict(shared=8192)),
+    "tiles, tiles": ([40, 50], [330, 310], 32, dict(shared=256)),
+}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", BUILDS)
+@pytest.mark.parametrize("dim", [48, 64, 128, 192, 256])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_every_build(w8, kind, dim, dtype):
+    new, totals, page, kw = BUILDS[kind]
+    kw = dict(kw)
+    shared, hq = kw.get("shared", 0), 16 if kind == "tiles, rows" else 4
+    rng = np.random.default_rng(dim + len(kind))
+    cache, table, q = make(rng, new, totals, hq, 2, dim, page, dtype, shared)
+    if kind == "tiles, rows":      # what the default plans choose; some of the sequences are compared
+        first, own = w8.plan_kv_shared(len(new), len(new), 1, table.shape[1] * page, shared, hq, 2, dim)
+        assert first.kernel == w8.KV_KERNEL_TILE and own.kernel == w8.KV_KERNEL_ROWS
+        some = [0, 39, 95]
+    else:
+        some = list(range(len(q)))
+        if shared:
+            kw["plan_"] = own_plan(w8, new, 2, chunk=1)
+    seqs = some if len(new) > 8 else range(len(new))
+    want = attention(q[some].astype(np.float64), cache, table[seqs], [totals[b] for b in seqs],
+                     [new[b] for b in seqs], hq // 2, dim ** -0.5, True, kw.get("window", 0), kw.get("sinks", 0))
+    out, lse = call(w8, cache.to(w8), table, q, dtype, new, totals, **kw)
+    compare(out[some], lse[some], want, dtype)
+
+
 @pytest.mark.gpu
 def test_strided_rows(w8):
     """Queries and outputs inside wider rows, unaligned."""
