@@ -434,6 +434,56 @@ def test_every_build(w8, kind, dim, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("max_kv", [1, 100, 300])
+@pytest.mark.parametrize("new", [[1, 2, 1], [40, 50, 33]])
+def test_longer_sequences_than_max_kv(w8, new, max_kv):
+    """max_kv shapes the launch only."""
+    rng = np.random.default_rng(max_kv + new[0])
+    totals = [600, 1000, 290]
+    cache, table, q = make(rng, new, totals, 4, 2, 64, 32, "bf16", 256)
+    dev = cache.to(w8)
+    for kw in (dict(shared=256), dict(shared=256, plan_=own_plan(w8, new, 2, chunk=1)), dict(window=200, sinks=70)):
+        want = attention(q.astype(np.float64), cache, table, totals, new, 2, 64 ** -0.5, True, kw.get("window", 0),
+                         kw.get("sinks", 0))
+        compare(*call(w8, dev, table, q, "bf16", new, totals, max_kv=max_kv, **kw), want, "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shared", [0, 512])
+def test_two_graphs_of_one_stream(w8, shared):
+    """They share the stream's workspace; replayed in turn, between eager
+    calls of another size, each gives what an eager call does."""
+    rng = np.random.default_rng(6)
+    calls = []
+    for n in (12, 7):
+        new, totals = [1] * n, [700 + 90 * i for i in range(n)]
+        cache, table, q = make(rng, new, totals, 8, 2, 128, 64, "bf16", shared)
+        calls.append((cuda(q, DT["bf16"]), cache.to(w8), cuda(table.astype(np.int32)), i32(totals)))
+    kw = [dict(max_new=1, shared=shared, plan_=own_plan(w8, [1], 4, chunk=c) if shared else
+               w8.KVPlan(kernel=1, row_blocks=1, waves=4, chunk_tiles=c)) for c in (4, 5)]
+    want = [w8.kv_attention(*c, **k) for c, k in zip(calls, kw)]
+    stream, graphs, outs = torch.cuda.Stream(), [], []
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        for c, k in zip(calls, kw):      # the workspace grows before the captures
+            w8.kv_attention(*c, **k)
+        for c, k in zip(calls, kw):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=stream):
+                outs.append(w8.kv_attention(*c, **k))
+            graphs.append(g)
+        for turn in range(6):
+            for o in outs:
+                o.zero_()
+            graphs[turn % 2].replay()
+            eager = w8.kv_attention(*calls[turn % 3 % 2], **kw[turn % 3 % 2])
+            graphs[1 - turn % 2].replay()
+            stream.synchronize()
+            assert all(torch.equal(o, w) for o, w in zip(outs, want))
+            assert torch.equal(eager, want[turn % 3 % 2])
+
+
+@pytest.mark.gpu
 def test_strided_rows(w8):
     """Queries and outputs inside wider rows, unaligned."""
     rng = np.random.default_rng(8)
