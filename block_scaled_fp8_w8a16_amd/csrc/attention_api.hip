@@ -74,11 +74,11 @@ void fill_rope(RopeRows &r, const void *x, void *y, const int64_t strides[4], co
     r.by_items = FastDiv(r.items);
 }
 
-// Several heads per thread where that still leaves every CU 512 threads
+// Several heads per thread where that still leaves every CU `threads` of them
 // (figures in rope_kernel.hip).
-uint32_t rope_heads_per_thread(uint64_t items)
+uint32_t rope_heads_per_thread(uint64_t items, uint32_t threads = 512)
 {
-    return items >= 512ull * kDefaultCUs * kRopeHeads ? kRopeHeads : 1;
+    return items >= (uint64_t)threads * kDefaultCUs * kRopeHeads ? kRopeHeads : 1;
 }
 
 // Whether rows of dim elements that a call writes, `token` and `head` apart,
@@ -319,7 +319,7 @@ int rope(const char *entry, const void *x, const int64_t strides[4], void *y, ui
     RopeAxesArgs a;
     std::memset(static_cast<void *>(&a), 0, sizeof a);
     fill_rope(a.r, x, y, strides, table, table_positions, rot, head_dim, layout, heads, dtype);
-    a.heads_per_thread = rope_heads_per_thread((uint64_t)heads * a.r.items * tokens);
+    a.heads_per_thread = rope_heads_per_thread((uint64_t)heads * a.r.items * tokens, axes ? 256 : 512);
     const uint64_t row = (uint64_t)((heads + a.heads_per_thread - 1) / a.heads_per_thread) * a.r.items;
     const uint64_t total = row * tokens;
     if (total >= (1ull << 31))

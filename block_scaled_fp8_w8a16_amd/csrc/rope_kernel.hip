@@ -14,9 +14,12 @@
 // the last-level cache, where a large copy moves 4.9.
 // Several axes: a thread loads its token's positions (up to four) and takes
 // the pairs of one axis as one piece of the table where every thread's pairs
-// lie within an axis, else each by itself.  4097 tokens of 16 heads of 80 FP16
-// channels on two axes, backwards: 7.4 us, 3.0 TB/s of 22 MB (6.9 on the GPU;
-// launch, then positions, table and row one after the other).
+// lie within an axis, else each by itself.  Four heads a thread share that
+// too, from 256 threads per CU on (us, one head and four: 2048 tokens of 16
+// heads of 80 channels 5.0 and 5.0, 4097 8.4 and 7.9; 512 tokens of 32 heads
+// of 128 3.5 and 4.2, 1024 6.0 and 6.2, by turns 7.4 and 7.0).  4097 tokens of
+// 16 heads of 80 FP16 channels on two axes, backwards: 7.2 us, 3.1 TB/s of 22
+// MB (launch, then positions, table and row one after the other).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
