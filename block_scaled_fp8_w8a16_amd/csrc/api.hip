@@ -25,12 +25,23 @@ namespace w8a16 {
 
 namespace {
 
-std::mutex g_ws_mutex;
-std::map<std::pair<int, hipStream_t>, Workspace> g_ws;
+struct StreamWorkspace {
+    Workspace w;
+    std::mutex held;
+};
+
+std::mutex g_ws_mutex;      // of the map and the list, not of what they hold
+std::map<std::pair<int, hipStream_t>, StreamWorkspace> g_ws;
 // Buffers replaced by larger ones.  They are never freed: a HIP graph
 // captured with an earlier, smaller plan on that stream keeps their
 // addresses and may still be replayed.
 std::vector<void *> g_retired;
+
+void retire(void *p)
+{
+    std::lock_guard<std::mutex> lock(g_ws_mutex);
+    g_retired.push_back(p);
+}
 
 std::mutex g_cu_mutex;
 std::map<int, uint32_t> g_cu_count;
@@ -193,10 +204,15 @@ int device_cu_count(int dev, uint32_t *out)
 // graphs captured earlier, use them), so it needs no synchronisation.  It
 // cannot happen while the stream is being captured into a graph: that
 // returns W8A16_ERR_WORKSPACE and enqueues nothing.
-int get_workspace(int dev, hipStream_t stream, const w8a16_plan_t &plan, Workspace *out)
+int get_workspace(int dev, hipStream_t stream, const w8a16_plan_t &plan, Workspace *out, WorkspaceHold *hold)
 {
-    std::lock_guard<std::mutex> lock(g_ws_mutex);
-    Workspace &w = g_ws[std::make_pair(dev, stream)];
+    StreamWorkspace *at;
+    {
+        std::lock_guard<std::mutex> lock(g_ws_mutex);
+        at = &g_ws[std::make_pair(dev, stream)];
+    }
+    *hold = WorkspaceHold(at->held);
+    Workspace &w = at->w;
     const bool grow_ws = plan.workspace_bytes > w.ws_bytes;
     const bool grow_ctr = plan.counter_count > w.counter_count;
     if (grow_ws || grow_ctr) {
@@ -222,7 +238,7 @@ int get_workspace(int dev, hipStream_t stream, const w8a16_plan_t &plan, Workspa
         if (e != hipSuccess)
             return hip_fail(e, "hipMalloc(workspace)");
         if (w.ws)
-            g_retired.push_back(w.ws);
+            retire(w.ws);
         w.ws = nws;
         w.ws_bytes = plan.workspace_bytes;
     }
@@ -238,7 +254,7 @@ int get_workspace(int dev, hipStream_t stream, const w8a16_plan_t &plan, Workspa
             return hip_fail(e, "hipMemsetAsync(counters)");
         }
         if (w.counters)
-            g_retired.push_back(w.counters);
+            retire(w.counters);
         w.counters = nc;
         w.counter_count = plan.counter_count;
     }
@@ -273,9 +289,9 @@ std::map<int, uint8_t *> g_scratch;   // device address of `scratch`, per device
 // fill kernel on `stream` (a kernel rather than a memset node, so that a
 // graph capturing this first call records a plain kernel).  The counters
 // start at zero and every kernel that uses them leaves them at zero.
-int device_scratch(int dev, hipStream_t stream, uint8_t **out)
+int device_scratch(int dev, hipStream_t stream, uint8_t **out, WorkspaceHold *hold)
 {
-    std::lock_guard<std::mutex> lock(g_scratch_mutex);
+    *hold = WorkspaceHold(g_scratch_mutex);
     auto it = g_scratch.find(dev);
     if (it != g_scratch.end()) {
         *out = it->second;
@@ -355,7 +371,8 @@ int check_epilogue(const char *entry, const w8a16_epilogue_t *x, const void *c, 
 }
 
 // Enqueue the plan's kernels.  `fixed`: the split-K workspace to use (the
-// no-alloc entry's scratch); null takes the (device, stream) workspace.
+// no-alloc entry's scratch, held by it); null takes the (device, stream)
+// workspace.
 // `epilogue`: null for a plain GEMM; else `plan` is a default plan.
 int run(const char *entry, const char *why, const void *a, uint32_t a_row_stride,
         const void *w_fp8, const float *block_scale, void *c, uint32_t c_row_stride,
@@ -367,11 +384,12 @@ int run(const char *entry, const char *why, const void *a, uint32_t a_row_stride
     if (e != hipSuccess)
         return hip_fail(e, "hipGetDevice");
     Workspace wsp;
+    WorkspaceHold hold;
     if (plan.splits > 1) {
         if (fixed) {
             wsp = *fixed;
         } else {
-            int st = get_workspace(dev, stream, plan, &wsp);
+            int st = get_workspace(dev, stream, plan, &wsp, &hold);
             if (st != W8A16_OK)
                 return st;
         }
@@ -543,7 +561,8 @@ int w8a16_gemm_noalloc(const void *a, uint32_t a_row_stride, const void *w_fp8,
         return fail(W8A16_ERR_WORKSPACE, buf);
     }
     uint8_t *ptr = nullptr;
-    st = device_scratch(dev, hs, &ptr);
+    WorkspaceHold hold;
+    st = device_scratch(dev, hs, &ptr, &hold);
     if (st != W8A16_OK)
         return st;
     Workspace wsp;

@@ -548,6 +548,7 @@ int kv_attention(const char *entry, const w8a16_kv_cache_t *cache, const w8a16_k
     if ((kv_launch_groups(a, p.waves) + (shared ? first.grid : 0u)) * 64ull * p.waves > kMaxThreads)
         return refuse(W8A16_ERR_SHAPE, "%s: %u tokens of %u sequences are too many for one call", entry,
                       seqs->tokens, seqs->seqs);
+    WorkspaceHold hold;
     if (p.workspace_bytes) {
         w8a16_plan_t need;
         std::memset(&need, 0, sizeof need);
@@ -555,7 +556,7 @@ int kv_attention(const char *entry, const w8a16_kv_cache_t *cache, const w8a16_k
         if (p.kernel == W8A16_KV_ROWS && !shared)
             need.counter_count = p.grid / p.chunks * kKvCounterStride;
         Workspace ws;
-        st = get_workspace(dev, stream, need, &ws);
+        st = get_workspace(dev, stream, need, &ws, &hold);
         if (st != W8A16_OK)
             return named(st, entry);
         a.ws = ws.ws;

@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "w8a16.h"
 
 namespace w8a16 {
@@ -18,6 +20,11 @@ struct Workspace {
     uint32_t counter_count = 0;
 };
 
+// One call's use of a workspace.  The launches of a call hand each other
+// partial results through it, and another thread's on the same stream must not
+// come between them: held until the last of them is enqueued.
+using WorkspaceHold = std::unique_lock<std::mutex>;
+
 // Record a HIP failure of `what`; returns W8A16_ERR_HIP.
 int hip_fail(hipError_t e, const char *what);
 // W8A16_OK, or W8A16_ERR_ENV for a bad diagnostic setting.
@@ -29,6 +36,6 @@ void log_line(const char *line);
 int launched(hipStream_t stream);
 int device_cu_count(int dev, uint32_t *out);
 // Workspace with at least the plan's workspace_bytes and counter_count.
-int get_workspace(int dev, hipStream_t stream, const w8a16_plan_t &plan, Workspace *out);
+int get_workspace(int dev, hipStream_t stream, const w8a16_plan_t &plan, Workspace *out, WorkspaceHold *hold);
 
 }  // namespace w8a16

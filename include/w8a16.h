@@ -34,6 +34,10 @@
  * was captured on: two replays of graphs captured on one stream must not
  * overlap in time.
  *
+ * Threads: calls may come from several threads, on one stream too; the
+ * launches of a call that use a workspace are enqueued with none of another
+ * call's that uses it between them.
+ *
  * Alignment and aliasing: A, W, S and C must be 16-byte aligned (torch
  * allocations are).  C must not overlap A, W or S.  c_row_stride may be any
  * value >= n.

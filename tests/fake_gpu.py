@@ -1,0 +1,99 @@
+"""The library's host code without a GPU: run as ``python tests/fake_gpu.py
+STAND_IN.so CHECK``, it loads the stand-in for the HIP runtime
+(tests/host/fake_hip.cpp), then the library, and runs one of the checks below
+(their tests: test_fake_gpu.py).  Kernels do not run; launches are recorded."""
+
+import ctypes
+import os
+import sys
+import threading
+
+sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+P = 1 << 20      # an address: never read
+_keep = []
+
+
+def launches(fake):
+    """(thread, stream, workgroups, threads of each) of every launch so far."""
+    out, buf = [], (ctypes.c_uint64 * 4)()
+    for i in range(fake.fake_launches()):
+        fake.fake_launch(ctypes.c_uint64(i), buf)
+        out.append(tuple(buf))
+    fake.fake_forget()
+    return out
+
+
+def attention(w8, seqs, new, pages, q_heads, kv_heads, dim, page=64, plan=None, span=None, stream=0, **kw):
+    """Status of an attention call of `seqs` sequences of `new` tokens."""
+    A = w8.attention
+    page_bytes = kv_heads * page * dim
+    cache = A.KVCacheDesc(P, P, P, P, page_bytes, page_bytes, kv_heads * page // 16, kv_heads * page // 16, 1 << 20,
+                          page, kv_heads, dim)
+    s = A.KVSeqs(P, P, None, pages, pages, seqs, seqs * new, new)
+    a = A.KVAttentionArgs(P, P, None, q_heads * dim, dim, q_heads * dim, dim,
+                          ctypes.pointer(plan) if plan else None, 0.1, q_heads, 1, 1, kw.get("window", 0), 0)
+    lib = w8.library()
+    if span:
+        return lib.w8a16_kv_attention_span(cache, s, a, A.KVSpan(*span), stream)
+    return lib.w8a16_kv_attention(cache, s, a, stream)
+
+
+def calls_are_whole(w8, fake):
+    """Launches that hand partial results to each other through a stream's
+    workspace follow each other, whatever other threads do on that stream."""
+    lib, m, n, k = w8.library(), 40, 2304, 8192
+    tile = dict(kernel=2, row_blocks=8, waves=4, chunk_tiles=2)
+    e = w8.Epilogue(out_dtype=1)
+    plan = w8.plan(m, n, k)
+    assert plan.kernel == w8.KERNEL_TILE and plan.splits > 1
+
+    def with_plan(**kw):
+        p = w8.KVPlan(**kw)
+        return attention(w8, 2, 40, 8, 8, 2, 64, plan=p)
+    ways = {
+        "shared prefix": lambda: attention(w8, 6, 1, 36, 32, 8, 128, span=(0, 1984),
+                                           plan=w8.KVPlan(kernel=1, row_blocks=1, waves=4, chunk_tiles=4)),
+        "tile kernel in chunks": lambda: with_plan(**tile),
+        "sinks in chunks": lambda: attention(w8, 2, 40, 8, 8, 2, 64, plan=w8.KVPlan(**tile), span=(4, 0), window=100),
+        "product": lambda: lib.w8a16_gemm(P, k, P, P, P, n, m, n, k, 0),
+        "product by a plan": lambda: lib.w8a16_gemm_planned(P, k, P, P, P, n, m, n, k, plan, 0),
+        "product without allocation": lambda: lib.w8a16_gemm_noalloc(P, k, P, P, P, n, m, n, k, 0),
+        "product with an epilogue": lambda: lib.w8a16_gemm_epilogue(P, k, P, P, P, n, m, n, k, e, 0),
+    }
+    for name, call in ways.items():
+        fake.fake_thread(ctypes.c_uint64(0))
+        assert call() == 0, (name, w8.last_error())
+        launches(fake)      # (the first call may clear what it has allocated)
+        call()
+        one = len(launches(fake))
+        assert one >= 2, name
+        fake.fake_pause_us(ctypes.c_uint64(2000))
+        status = []
+
+        def work(i):
+            fake.fake_thread(ctypes.c_uint64(i))
+            for _ in range(4):
+                status.append(call())
+        threads = [threading.Thread(target=work, args=(i,)) for i in (1, 2, 3)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        fake.fake_pause_us(ctypes.c_uint64(0))
+        got = launches(fake)
+        assert status == [0] * 12 and len(got) == 12 * one, name
+        for i in range(0, len(got), one):
+            assert len({g[0] for g in got[i:i + one]}) == 1, "%s: launches of threads %s" % (name, [g[0] for g in got])
+
+
+def main():
+    # (bound with symbols before the library's own dependencies)
+    fake = ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_GLOBAL)
+    import block_scaled_fp8_w8a16_amd as w8
+    globals()[sys.argv[2]](w8, fake)
+    print("done")
+
+
+if __name__ == "__main__":
+    main()
