@@ -179,22 +179,30 @@ __device__ __forceinline__ uint32_t sequences(const PrefixArgs &) { return 1; }
 
 // The row of the block table that leads to the keys: for a shared prefix
 // that of a sequence which holds all of it, else (every row then sees less
-// of it) of the longest.
+// of it) of the longest.  A slot that brings no tokens leads nowhere: its
+// length and row may be anything.
 __device__ __forceinline__ uint32_t table_row(const AttnArgs &, uint32_t b) { return b; }
 
 __device__ __forceinline__ uint32_t table_row(const PrefixArgs &a, uint32_t)
 {
+    const KvSeqs &s = a.seqs;
     const uint32_t lane = threadIdx.x & 63u;
     int32_t most = -1;
     uint32_t longest = 0;
-    for (uint32_t b0 = 0; b0 < a.seqs.seqs; b0 += 64u) {
-        const int32_t len = b0 + lane < a.seqs.seqs ? a.seqs.kv_lens[b0 + lane] : -1;
+    for (uint32_t b0 = 0; b0 < s.seqs; b0 += 64u) {
+        const uint32_t b = b0 + lane, in = b < s.seqs ? b : s.seqs - 1u;
+        int32_t len = s.kv_lens[in];
+        if (s.cu) {
+            const uint32_t first = (uint32_t)s.cu[in], end = (uint32_t)s.cu[in + 1];
+            len = first < end && end <= s.tokens ? len : -1;
+        }
+        len = b < s.seqs ? len : -1;
         const uint64_t whole = __ballot(len >= (int32_t)a.shared);
         if (whole)
             return __builtin_amdgcn_readfirstlane(b0 + (uint32_t)__builtin_ctzll(whole));
         if (len > most) {
             most = len;
-            longest = b0 + lane;
+            longest = b;
         }
     }
 #pragma unroll
