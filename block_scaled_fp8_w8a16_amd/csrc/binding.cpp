@@ -201,7 +201,8 @@ uint32_t axes_rot(const w8a16_axes_t &a)
     return u32((int64_t)(2 * sum));
 }
 
-// Page stride of a cache tensor whose pages are contiguous inside.
+// Page stride of a cache tensor whose pages are contiguous inside (of a single
+// page its size, whatever the tensor says).
 uint64_t page_stride(const char *name, const Tensor &t)
 {
     int64_t want = 1;
@@ -210,8 +211,7 @@ uint64_t page_stride(const char *name, const Tensor &t)
             throw Refused(std::string("the inside of a ") + name + " page must be contiguous");
         want *= t.size(i);
     }
-    const int64_t st = t.stride(0);
-    return (uint64_t)(t.size(0) < 2 && st < want ? want : st);
+    return (uint64_t)(t.size(0) < 2 ? want : t.stride(0));
 }
 
 w8a16_kv_cache_t cache_of(PyObject *o, const Device &d)

@@ -1,5 +1,5 @@
 """Attention and its cache where callers' shapes end: slots without tokens
-beside a shared prefix."""
+beside a shared prefix, caches of one page."""
 
 import numpy as np
 import pytest
@@ -57,3 +57,20 @@ def test_slots_without_tokens_do_not_lead_to_the_prefix(w8, slot, longest, new):
         want = run(table, totals, cu, plan)
         got = run(*stale[slot], plan)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("pitch", [0, 3, 8])
+def test_caches_of_one_page(w8, pitch):
+    """The pitch of a single page says nothing."""
+    heads, page, dim, tokens = 2, 32, 64, 20
+    plain = w8.kv_cache(1, heads, page, dim)
+    odd = w8.KVCache(*(t.clone().as_strided(t.shape, (t.stride(0) + pitch,) + t.stride()[1:]) for t in plain))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k, v, q = (torch.randn(tokens, heads, dim, generator=g, device="cuda").bfloat16() for _ in range(3))
+    bt, lens = torch.zeros(1, 1, dtype=torch.int32, device="cuda"), i32([tokens])
+    out = []
+    for cache in (plain, odd):
+        w8.kv_append(cache, k, v, bt, lens)
+        out.append(w8.kv_attention(q, cache, bt, lens))
+    assert torch.equal(*out) and all(torch.equal(a, b) for a, b in zip(plain, odd))
