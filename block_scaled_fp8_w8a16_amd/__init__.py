@@ -60,7 +60,8 @@ EXPORTS = ("w8a16_check_args", "w8a16_plan", "w8a16_plan_finalize", "w8a16_gemm"
            "w8a16_gemm_w8a8_planned", "w8a16_gemm_w4a4", "w8a16_plan_w4a4",
            "w8a16_gemm_w4a4_planned", "w8a16_rope_table", "w8a16_rope", "w8a16_rope_axes",
            "w8a16_kv_append", "w8a16_kv_append_axes", "w8a16_kv_attention",
-           "w8a16_kv_attention_span", "w8a16_plan_kv_shared", "w8a16_plan_kv_attention", "w8a16_status_string",
+           "w8a16_kv_attention_span", "w8a16_plan_kv_shared", "w8a16_plan_kv_sinks", "w8a16_plan_kv_attention",
+           "w8a16_status_string",
            "w8a16_last_error")
 
 MAX_BATCH = 8

@@ -107,9 +107,10 @@ def declare(lib) -> None:
                                             _vp]
     lib.w8a16_plan_kv_shared.argtypes = [_u32] * 9 + [ptr(KVPlan)] * 2
     lib.w8a16_plan_kv_attention.argtypes = [_u32] * 8 + [ptr(KVPlan)]
+    lib.w8a16_plan_kv_sinks.argtypes = [_u32] * 9 + [ptr(KVPlan)]
     for name in ("w8a16_rope_table", "w8a16_rope", "w8a16_rope_axes", "w8a16_kv_append",
                  "w8a16_kv_append_axes", "w8a16_kv_attention", "w8a16_kv_attention_span",
-                 "w8a16_plan_kv_shared", "w8a16_plan_kv_attention"):
+                 "w8a16_plan_kv_shared", "w8a16_plan_kv_sinks", "w8a16_plan_kv_attention"):
         getattr(lib, name).restype = ctypes.c_int
 
 
@@ -273,12 +274,12 @@ def kv_attention(q, cache, block_table, kv_lens, out=None, *, cu_seqlens=None,
 
 
 def plan_kv_attention(seqs: int, max_new: int, max_kv: int, q_heads: int, kv_heads: int,
-                      head_dim: int, window: int = 0, cu_count: int = 0) -> KVPlan:
+                      head_dim: int, window: int = 0, cu_count: int = 0, sinks: int = 0) -> KVPlan:
     """Default plan of kv_attention (no GPU call)."""
     from . import _raise_if, library
     p = KVPlan()
-    _raise_if(library().w8a16_plan_kv_attention(seqs, max_new, max_kv, q_heads, kv_heads, head_dim,
-                                                window, cu_count, ctypes.byref(p)))
+    _raise_if(library().w8a16_plan_kv_sinks(seqs, max_new, max_kv, q_heads, kv_heads, head_dim, window, sinks,
+                                            cu_count, ctypes.byref(p)))
     return p
 
 

@@ -518,8 +518,7 @@ int kv_attention(const char *entry, const w8a16_kv_cache_t *cache, const w8a16_k
     st = device_cu_count(dev, &cus);
     if (st != W8A16_OK)
         return named(st, entry);
-    const uint32_t window = g->window < 0x7fffffffu ? g->window : 0;
-    const uint32_t sinks = !window ? 0 : span.sinks < (1u << 30) ? span.sinks : 1u << 30;
+    const uint32_t window = kv_window(g->window), sinks = kv_sinks(window, span.sinks);
     // whole pages that all sequences hold (a window is not worth two passes)
     uint32_t shared = span.shared < max_kv ? span.shared : max_kv;
     shared = window ? 0 : shared / cache->page_size * cache->page_size;

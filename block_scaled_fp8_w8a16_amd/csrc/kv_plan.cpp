@@ -339,6 +339,14 @@ extern "C" int w8a16_plan_kv_attention(uint32_t seqs, uint32_t max_new, uint32_t
                                        uint32_t q_heads, uint32_t kv_heads, uint32_t head_dim,
                                        uint32_t window, uint32_t cu_count, w8a16_kv_plan_t *out)
 {
-    return w8a16::make_kv_plan(seqs, max_new, max_kv, q_heads, kv_heads, head_dim, window, cu_count,
-                               out);
+    return w8a16_plan_kv_sinks(seqs, max_new, max_kv, q_heads, kv_heads, head_dim, window, 0, cu_count, out);
+}
+
+extern "C" int w8a16_plan_kv_sinks(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_heads,
+                                   uint32_t kv_heads, uint32_t head_dim, uint32_t window, uint32_t sinks,
+                                   uint32_t cu_count, w8a16_kv_plan_t *out)
+{
+    window = w8a16::kv_window(window);
+    return w8a16::make_kv_plan(seqs, max_new, max_kv, q_heads, kv_heads, head_dim, window, cu_count, out,
+                               w8a16::kv_sinks(window, sinks));
 }

@@ -173,6 +173,13 @@ constexpr uint64_t kMaxThreads = (1ull << 32) - 1;
 // LDS; arrival counters sit 64 bytes apart.
 constexpr uint32_t kKvMaxChunks = 128;
 constexpr uint32_t kKvCounterStride = 16;
+// A call's window (0: all keys, which such as reach past any sequence are as
+// well) and, beside one, its sinks.
+inline uint32_t kv_window(uint32_t window) { return window < 0x7fffffffu ? window : 0; }
+inline uint32_t kv_sinks(uint32_t window, uint32_t sinks)
+{
+    return !window ? 0 : sinks < (1u << 30) ? sinks : 1u << 30;
+}
 int kv_plan_finalize(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_heads,
                      uint32_t kv_heads, uint32_t head_dim, uint32_t window, w8a16_kv_plan_t *p,
                      uint32_t sinks = 0);

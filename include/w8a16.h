@@ -554,7 +554,8 @@ typedef struct w8a16_kv_plan {
     uint32_t chunk_tiles;     /* 64-key tiles per chunk */
     uint32_t chunks;          /* chunks the longest sequence is cut into (derived) */
     uint32_t grid;            /* workgroups launched (derived) */
-    uint64_t workspace_bytes; /* partial results (derived; 0 if chunks == 1) */
+    uint64_t workspace_bytes; /* partial results (derived; 0 if chunks == 1, but for the two
+                                 passes over a shared part, which always leave some) */
 } w8a16_kv_plan_t;
 
 /* For query row i of sequence b at position p = kv_lens[b] - n_b + i and
@@ -621,6 +622,12 @@ int w8a16_plan_kv_shared(uint32_t seqs, uint32_t tokens, uint32_t max_new, uint3
 int w8a16_plan_kv_attention(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_heads,
                             uint32_t kv_heads, uint32_t head_dim, uint32_t window,
                             uint32_t cu_count, w8a16_kv_plan_t *out);
+
+/* The same of a window with sinks, whose tiles a plan's chunks have to cover as
+ * well.  Pure: no GPU call. */
+int w8a16_plan_kv_sinks(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t q_heads,
+                        uint32_t kv_heads, uint32_t head_dim, uint32_t window, uint32_t sinks,
+                        uint32_t cu_count, w8a16_kv_plan_t *out);
 
 /* ---- Product with an epilogue ---------------------------------------------
  *   c[i][j] = residual[i][j] + act(s + bias[j]) * gate[i][j]

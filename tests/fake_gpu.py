@@ -87,6 +87,32 @@ def calls_are_whole(w8, fake):
             assert len({g[0] for g in got[i:i + one]}) == 1, "%s: launches of threads %s" % (name, [g[0] for g in got])
 
 
+def plans_are_the_calls(w8, fake):
+    """The public default plan of a window with sinks is the one that a call
+    launches by itself, and a call takes it."""
+    import random
+    rng = random.Random(3)
+
+    def shapes():
+        yield 1, 1, 313, 64, 8, 8, 128, 16, 100000          # (20032 keys, all of them sinks)
+        for _ in range(1500):
+            kv = rng.choice([1, 2, 8])
+            yield (rng.randint(1, 40), rng.choice([1, 3, 40, 300]), int(2 ** rng.uniform(0, 9)),
+                   rng.choice([16, 64, 256]), kv * rng.choice([1, 4, 5]), kv, 16 * rng.randint(1, 16),
+                   rng.choice([0, int(2 ** rng.uniform(0, 14)), 1 << 31]), int(2 ** rng.uniform(0, 17)))
+    for seqs, new, pages, page, hq, hkv, dim, window, sinks in shapes():
+        shape = (seqs, new, pages, page, hq, hkv, dim, window, sinks)
+        p = w8.plan_kv_attention(seqs, new, pages * page, hq, hkv, dim, window, sinks=sinks)
+        seen = []
+        for plan in (None, p):
+            st = attention(w8, seqs, new, pages, hq, hkv, dim, page, plan, (sinks, 0), window=window)
+            assert st == 0, (shape, w8.last_error())
+            seen.append([g[2:] for g in launches(fake)])
+        assert seen[0] == seen[1], shape
+        assert seen[0][0] == (p.grid, 64 * p.waves), shape
+        assert len(seen[0]) == (2 if p.kernel == w8.KV_KERNEL_TILE and p.chunks > 1 else 1), shape
+
+
 def main():
     # (bound with symbols before the library's own dependencies)
     fake = ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_GLOBAL)

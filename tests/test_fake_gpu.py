@@ -26,3 +26,7 @@ def run(stand_in, check):
 
 def test_calls_are_whole(stand_in):
     run(stand_in, "calls_are_whole")
+
+
+def test_plans_are_the_calls(stand_in):
+    run(stand_in, "plans_are_the_calls")
