@@ -34,6 +34,16 @@ uint64_t tiles_of(uint32_t max_new, uint32_t max_kv, uint32_t window, uint32_t s
     return tiles < 1 ? 1 : tiles;
 }
 
+const char *const kTooMany = "w8a16_kv_attention: too many workgroups (2^32 threads) for one call";
+
+// Whether the launch that joins a plan's partial rows fits, a wave per row
+// that exists (of at most `rows` of a sequence) and KV head.
+bool join_fits(const w8a16_kv_plan_t &p, uint64_t rows)
+{
+    const uint64_t tile = 16ull * p.row_blocks, all = (uint64_t)(p.grid / p.chunks) * (rows < tile ? rows : tile);
+    return div_up(all, 4) * 256 <= kMaxThreads;
+}
+
 }  // namespace
 
 // Fills the derived fields of a plan whose kernel, row_blocks and
@@ -55,7 +65,7 @@ int kv_plan_finalize(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t 
     const uint64_t row_tiles = div_up(rows, tile_rows), chunks = div_up(tiles, p->chunk_tiles);
     const uint64_t grid = (uint64_t)seqs * kv_heads * row_tiles * chunks;
     if (grid * 64ull * p->waves > kMaxThreads)
-        return fail(W8A16_ERR_SHAPE, "w8a16_kv_attention: too many workgroups (2^32 threads) for one call");
+        return fail(W8A16_ERR_SHAPE, kTooMany);
     p->row_tiles = (uint32_t)row_tiles;
     p->chunks = (uint32_t)chunks;
     p->grid = (uint32_t)grid;
@@ -65,6 +75,8 @@ int kv_plan_finalize(uint32_t seqs, uint32_t max_new, uint32_t max_kv, uint32_t 
                  (unsigned long long)chunks, kKvMaxChunks);
         return fail(W8A16_ERR_BAD_PLAN, buf);
     }
+    if (p->kernel == W8A16_KV_TILE && chunks > 1 && !join_fits(*p, rows))
+        return fail(W8A16_ERR_SHAPE, kTooMany);
     p->workspace_bytes = chunks > 1 ? grid * tile_rows * (head_dim + 4) * 4 : 0;
     return W8A16_OK;
 }
@@ -159,9 +171,9 @@ namespace {
 constexpr uint64_t kMaxPassChunks = kKvMaxChunks / 2;
 
 // A pass's plan over `keys` keys, with room for its partial rows: the given
-// kernel and chunks.
+// kernel and chunks.  joined: the join goes by its rows (the own keys' pass).
 int pass_plan(uint32_t seqs, uint32_t max_new, uint32_t keys, uint32_t q_heads, uint32_t kv_heads,
-              uint32_t head_dim, w8a16_kv_plan_t *p)
+              uint32_t head_dim, bool joined, w8a16_kv_plan_t *p)
 {
     const int st = kv_plan_finalize(seqs, max_new, keys, q_heads, kv_heads, head_dim, 0, p);
     if (st != W8A16_OK)
@@ -169,6 +181,8 @@ int pass_plan(uint32_t seqs, uint32_t max_new, uint32_t keys, uint32_t q_heads, 
     if (p->chunks > kMaxPassChunks || p->waves != 4)
         return fail(W8A16_ERR_BAD_PLAN, "w8a16_kv_attention: behind a shared part a plan has 4 waves and at "
                                         "most 64 chunks");
+    if (joined && !join_fits(*p, (uint64_t)max_new * (q_heads / kv_heads)))
+        return fail(W8A16_ERR_SHAPE, kTooMany);
     p->workspace_bytes = (uint64_t)p->grid * 16 * p->row_blocks * (head_dim + 4) * 4;
     return W8A16_OK;
 }
@@ -273,7 +287,7 @@ int make_kv_shared_plans(uint32_t seqs, uint32_t tokens, uint32_t max_new, uint3
         const uint64_t least = div_up(own_tiles, kMaxPassChunks);
         o = chunked(o.kernel, o.chunk_tiles < least ? least : o.chunk_tiles);
     }
-    st = pass_plan(seqs, max_new, own, q_heads, kv_heads, head_dim, &o);
+    st = pass_plan(seqs, max_new, own, q_heads, kv_heads, head_dim, true, &o);
     if (st != W8A16_OK) {
         if (given)
             return st;
@@ -291,7 +305,11 @@ int make_kv_shared_plans(uint32_t seqs, uint32_t tokens, uint32_t max_new, uint3
         per = per > kMinTiles ? per : kMinTiles;
         w8a16_kv_plan_t p = chunked(kernel, per < shared_tiles ? per : shared_tiles);
         if (div_up(shared_tiles, p.chunk_tiles) > kMaxPassChunks ||
-            pass_plan(1, tokens, shared, q_heads, kv_heads, head_dim, &p) != W8A16_OK)
+            pass_plan(1, tokens, shared, q_heads, kv_heads, head_dim, false, &p) != W8A16_OK)
+            return;
+        // (one launch, with the workgroups that fill tokens of no sequence:
+        // kv_launch_groups)
+        if (((uint64_t)p.grid + o.grid + 513 + tokens / 256) * 256 > kMaxThreads)
             return;
         const double t = two_passes(c, p, o, own_tiles, rows, kv_heads, head_dim);
         if (t < best) {
@@ -310,7 +328,7 @@ int make_kv_shared_plans(uint32_t seqs, uint32_t tokens, uint32_t max_new, uint3
                 consider(kernel, div_up(shared_tiles, n * (uint64_t)c.cus / row_tiles));
     }
     if (given && !prefix->grid)
-        return fail(W8A16_ERR_SHAPE, "w8a16_kv_attention: too many workgroups (2^32 threads) for one call");
+        return fail(W8A16_ERR_SHAPE, kTooMany);
     return W8A16_OK;
 }
 

@@ -113,6 +113,31 @@ def plans_are_the_calls(w8, fake):
         assert len(seen[0]) == (2 if p.kernel == w8.KV_KERNEL_TILE and p.chunks > 1 else 1), shape
 
 
+def all_launches_or_none(w8, fake):
+    """A call one of whose launches would pass 2^32 threads (both passes over a
+    shared prefix, or the join: a wave per row and KV head) takes another way
+    or is refused before the first."""
+    tile = dict(kernel=2, row_blocks=8, waves=4)
+    rows = dict(kernel=1, row_blocks=1, waves=4)
+    refused = 0
+    for seqs, new, pages, hq, dim, plan, span, window in [
+            (1 << 20, 1, 560, 64, 64, None, (0, 30016), 0), (1 << 18, 40, 560, 64, 64, None, (0, 30016), 0),
+            ((1 << 21) - 1, 1, 560, 8, 64, None, (0, 30016), 0),
+            (1 << 20, 1, 560, 64, 64, dict(rows, chunk_tiles=100), (0, 30016), 0),
+            (1 << 17, 20, 560, 64, 128, dict(tile, chunk_tiles=100), (0, 30016), 0),
+            (1 << 18, 16, 40, 64, 128, dict(tile, chunk_tiles=20), (0, 0), 0),
+            (1 << 18, 16, 40, 64, 128, dict(tile, chunk_tiles=5), (9, 0), 1500)]:
+        launches(fake)
+        st = attention(w8, seqs, new, pages, hq, 8, dim, 64, w8.KVPlan(**plan) if plan else None, span, window=window)
+        n = len(launches(fake))
+        case = (seqs, new, plan, span, st, n, w8.last_error())
+        if plan is None:
+            assert st == 0, case
+        assert st == 0 or (st == w8.ERR_SHAPE and n == 0 and "too many" in w8.last_error()), case
+        refused += st != 0
+    assert refused
+
+
 def main():
     # (bound with symbols before the library's own dependencies)
     fake = ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_GLOBAL)

@@ -30,3 +30,7 @@ def test_calls_are_whole(stand_in):
 
 def test_plans_are_the_calls(stand_in):
     run(stand_in, "plans_are_the_calls")
+
+
+def test_all_launches_or_none(stand_in):
+    run(stand_in, "all_launches_or_none")
