@@ -10,6 +10,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <exception>
 #include <map>
 #include <mutex>
 #include <set>
@@ -96,6 +97,19 @@ const Levers &levers()
 }
 
 }  // namespace
+
+int caught(const char *entry) noexcept
+{
+    char buf[288];
+    try {
+        throw;
+    } catch (const std::exception &e) {
+        snprintf(buf, sizeof buf, "%s: %s", entry, e.what());
+    } catch (...) {
+        snprintf(buf, sizeof buf, "%s: unknown C++ exception", entry);
+    }
+    return fail(W8A16_ERR_HIP, buf);
+}
 
 bool log_enabled() { return levers().log; }
 
@@ -441,7 +455,7 @@ extern "C" {
 int w8a16_gemm(const void *a, uint32_t a_row_stride, const void *w_fp8,
                const float *block_scale, void *c, uint32_t c_row_stride, uint32_t m,
                uint32_t n, uint32_t k, void *stream)
-{
+try {
     using namespace w8a16;
     int st = check_levers("w8a16_gemm");
     if (st != W8A16_OK)
@@ -463,12 +477,14 @@ int w8a16_gemm(const void *a, uint32_t a_row_stride, const void *w_fp8,
         return st;
     return run("w8a16_gemm", plan_reason(), a, a_row_stride, w_fp8, block_scale, c,
                c_row_stride, m, n, k, plan, static_cast<hipStream_t>(stream));
+} catch (...) {
+    return w8a16::caught("w8a16_gemm");
 }
 
 int w8a16_gemm_epilogue(const void *a, uint32_t a_row_stride, const void *w_fp8,
                         const float *block_scale, void *c, uint32_t c_row_stride, uint32_t m,
                         uint32_t n, uint32_t k, const w8a16_epilogue_t *epilogue, void *stream)
-{
+try {
     using namespace w8a16;
     const char *entry = "w8a16_gemm_epilogue";
     int st = check_levers(entry);
@@ -496,13 +512,15 @@ int w8a16_gemm_epilogue(const void *a, uint32_t a_row_stride, const void *w_fp8,
     st = run(entry, plan_reason(), a, a_row_stride, w_fp8, block_scale, c, c_row_stride, m, n, k, plan,
              static_cast<hipStream_t>(stream), nullptr, &e);
     return st == W8A16_OK ? st : fail_with_name(st, entry);
+} catch (...) {
+    return w8a16::caught("w8a16_gemm_epilogue");
 }
 
 int w8a16_gemm_planned(const void *a, uint32_t a_row_stride, const void *w_fp8,
                        const float *block_scale, void *c, uint32_t c_row_stride,
                        uint32_t m, uint32_t n, uint32_t k, const w8a16_plan_t *plan,
                        void *stream)
-{
+try {
     using namespace w8a16;
     int st = check_levers("w8a16_gemm_planned");
     if (st != W8A16_OK)
@@ -521,12 +539,14 @@ int w8a16_gemm_planned(const void *a, uint32_t a_row_stride, const void *w_fp8,
                                         "activations (w8a16_gemm_w8a8_planned)");
     return run("w8a16_gemm_planned", nullptr, a, a_row_stride, w_fp8, block_scale, c,
                c_row_stride, m, n, k, p, static_cast<hipStream_t>(stream));
+} catch (...) {
+    return w8a16::caught("w8a16_gemm_planned");
 }
 
 int w8a16_gemm_noalloc(const void *a, uint32_t a_row_stride, const void *w_fp8,
                        const float *block_scale, void *c, uint32_t c_row_stride, uint32_t m,
                        uint32_t n, uint32_t k, void *stream)
-{
+try {
     using namespace w8a16;
     int st = check_levers("w8a16_gemm_noalloc");
     if (st != W8A16_OK)
@@ -572,11 +592,13 @@ int w8a16_gemm_noalloc(const void *a, uint32_t a_row_stride, const void *w_fp8,
     wsp.counter_count = (uint32_t)kScratchCounterWords;
     return run("w8a16_gemm_noalloc", plan_reason(), a, a_row_stride, w_fp8, block_scale, c,
                c_row_stride, m, n, k, plan, hs, &wsp);
+} catch (...) {
+    return w8a16::caught("w8a16_gemm_noalloc");
 }
 
 int w8a16_act_quant_fp8(const void *a, uint32_t a_row_stride, void *q, uint32_t q_row_stride,
                         float *scales, uint32_t m, uint32_t k, void *stream)
-{
+try {
     using namespace w8a16;
     int st = check_levers("w8a16_act_quant_fp8");
     if (st != W8A16_OK)
@@ -618,13 +640,15 @@ int w8a16_act_quant_fp8(const void *a, uint32_t a_row_stride, void *q, uint32_t 
         log_line(buf);
     }
     return launched(static_cast<hipStream_t>(stream));
+} catch (...) {
+    return w8a16::caught("w8a16_act_quant_fp8");
 }
 
 int w8a16_gemm_w8a8_planned(const void *qa, uint32_t qa_row_stride, const float *a_scales,
                             const void *w_fp8, const float *block_scale, void *c,
                             uint32_t c_row_stride, uint32_t m, uint32_t n, uint32_t k,
                             const w8a16_plan_t *plan, void *stream)
-{
+try {
     using namespace w8a16;
     int st = check_levers("w8a16_gemm_w8a8");
     if (st != W8A16_OK)
@@ -684,6 +708,8 @@ int w8a16_gemm_w8a8_planned(const void *qa, uint32_t qa_row_stride, const float 
     log_plan(plan ? "w8a16_gemm_w8a8_planned" : "w8a16_gemm_w8a8", m, n, k, p,
              plan ? nullptr : plan_reason());
     return launched(static_cast<hipStream_t>(stream));
+} catch (...) {
+    return w8a16::caught("w8a16_gemm_w8a8_planned");
 }
 
 int w8a16_gemm_w8a8(const void *qa, uint32_t qa_row_stride, const float *a_scales,
@@ -698,7 +724,7 @@ int w8a16_gemm_w4a4_planned(const void *a, uint32_t a_row_stride, const uint8_t 
                             const void *w_fp4, const uint8_t *w_scale, void *c,
                             uint32_t c_row_stride, uint32_t m, uint32_t n, uint32_t k,
                             const w8a16_plan_t *plan, void *stream)
-{
+try {
     using namespace w8a16;
     int st = check_levers("w8a16_gemm_w4a4");
     if (st != W8A16_OK)
@@ -754,6 +780,8 @@ int w8a16_gemm_w4a4_planned(const void *a, uint32_t a_row_stride, const uint8_t 
     log_plan(plan ? "w8a16_gemm_w4a4_planned" : "w8a16_gemm_w4a4", m, n, k, p,
              plan ? nullptr : plan_reason());
     return launched(hs);
+} catch (...) {
+    return w8a16::caught("w8a16_gemm_w4a4_planned");
 }
 
 int w8a16_gemm_w4a4(const void *a, uint32_t a_row_stride, const uint8_t *a_scale,
@@ -765,7 +793,7 @@ int w8a16_gemm_w4a4(const void *a, uint32_t a_row_stride, const uint8_t *a_scale
 }
 
 int w8a16_gemm_batched(const w8a16_gemm_desc_t *descs, uint32_t count, void *stream)
-{
+try {
     using namespace w8a16;
     if (check_levers("w8a16_gemm_batched") != W8A16_OK)
         return W8A16_ERR_ENV;
@@ -832,6 +860,8 @@ int w8a16_gemm_batched(const w8a16_gemm_desc_t *descs, uint32_t count, void *str
         log_plan(entry, descs[0].m, descs[0].n, descs[0].k, plan, plan_reason());
     }
     return launched(static_cast<hipStream_t>(stream));
+} catch (...) {
+    return w8a16::caught("w8a16_gemm_batched");
 }
 
 }  // extern "C"

@@ -5,7 +5,6 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
-#include <exception>
 
 #include "attention.h"
 #include "host.h"
@@ -621,22 +620,6 @@ int kv_attention(const char *entry, const w8a16_kv_cache_t *cache, const w8a16_k
         log_line(line);
     }
     return named(launched(stream), entry);
-}
-
-// No C++ exception (an allocation in the maps and strings behind the
-// helpers) leaves a C entry.
-template <class F> int guarded(const char *entry, F f)
-{
-    try {
-        return f();
-    } catch (const std::exception &e) {
-        try {
-            return refuse(W8A16_ERR_HIP, "%s: %s", entry, e.what());
-        } catch (...) {
-        }
-    } catch (...) {
-    }
-    return W8A16_ERR_HIP;
 }
 
 }  // namespace

@@ -38,4 +38,16 @@ int device_cu_count(int dev, uint32_t *out);
 // Workspace with at least the plan's workspace_bytes and counter_count.
 int get_workspace(int dev, hipStream_t stream, const w8a16_plan_t &plan, Workspace *out, WorkspaceHold *hold);
 
+// Status of the exception being handled: none (of an allocation in the maps and
+// strings behind the helpers, of a mutex) leaves a C entry.
+int caught(const char *entry) noexcept;
+template <class F> int guarded(const char *entry, F f) noexcept
+{
+    try {
+        return f();
+    } catch (...) {
+        return caught(entry);
+    }
+}
+
 }  // namespace w8a16

@@ -20,12 +20,11 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
-#include <string>
 
 namespace w8a16 {
 
 namespace {
-thread_local std::string g_last_error;
+thread_local char g_last_error[400];      // (a message must not need memory: there may be none)
 thread_local char g_plan_reason[256];
 
 void set_reason(const char *fmt, ...) __attribute__((format(printf, 1, 2)));
@@ -40,9 +39,9 @@ void set_reason(const char *fmt, ...)
 
 const char *plan_reason() { return g_plan_reason; }
 
-void set_last_error(const char *fmt_msg) { g_last_error = fmt_msg ? fmt_msg : ""; }
+void set_last_error(const char *msg) { snprintf(g_last_error, sizeof g_last_error, "%s", msg ? msg : ""); }
 
-const char *last_error() { return g_last_error.c_str(); }
+const char *last_error() { return g_last_error; }
 
 int fail(int status, const char *msg)
 {
@@ -861,7 +860,7 @@ int fail_with_name(int status, const char *name)
 {
     char buf[320];
     const char *msg = last_error();
-    snprintf(buf, sizeof buf, "%s: %s", name,
+    snprintf(buf, sizeof buf, "%.64s: %.250s", name,
              strncmp(msg, "w8a16_gemm: ", 12) == 0 ? msg + 12 : msg);
     return fail(status, buf);
 }
@@ -872,7 +871,7 @@ int fail_at(int status, uint32_t index)
 {
     char buf[320];
     const char *msg = last_error();
-    snprintf(buf, sizeof buf, "w8a16_gemm_batched: descriptor %u: %s", index,
+    snprintf(buf, sizeof buf, "w8a16_gemm_batched: descriptor %u: %.250s", index,
              strncmp(msg, "w8a16_gemm: ", 12) == 0 ? msg + 12 : msg);
     return fail(status, buf);
 }

@@ -138,6 +138,43 @@ def all_launches_or_none(w8, fake):
     assert refused
 
 
+def no_exception_leaves(w8, fake):
+    """Where the host has no memory left a call returns a status, with or
+    without a message of its own, and the next one is right again."""
+    lib, m, n, k = w8.library(), 40, 2304, 8192
+    e, plan = w8.Epilogue(out_dtype=1), w8.plan(m, n, k)
+    descs = (w8.GemmDesc * 1)(w8.GemmDesc(P, P, P, P, 256, 256, 4, 256, 256))
+    ways = {        # on a stream of its own, whose workspace is to be noted
+        "gemm": lambda s: lib.w8a16_gemm(P, k, P, P, P, n, m, n, k, s),
+        "planned": lambda s: lib.w8a16_gemm_planned(P, k, P, P, P, n, m, n, k, plan, s),
+        "epilogue": lambda s: lib.w8a16_gemm_epilogue(P, k, P, P, P, n, m, n, k, e, s),
+        "noalloc": lambda s: lib.w8a16_gemm_noalloc(P, k, P, P, P, n, m, n, k, s),
+        "batched": lambda s: lib.w8a16_gemm_batched(descs, 1, s),
+        "quantiser": lambda s: lib.w8a16_act_quant_fp8(P, 256, P, 256, P, 4, 256, s),
+        "w8a8": lambda s: lib.w8a16_gemm_w8a8(P, 256, P, P, P, P, 256, 4, 256, 256, s),
+        "w4a4": lambda s: lib.w8a16_gemm_w4a4(P, 256, P, P, P, P, 256, 4, 256, 256, s),
+        "attention": lambda s: attention(w8, 6, 1, 36, 32, 8, 128, span=(0, 1984), stream=s, plan=w8.KVPlan(
+            kernel=1, row_blocks=1, waves=4, chunk_tiles=4)),
+    }
+    stopped = 0
+    for i, (name, call) in enumerate(ways.items()):
+        fake.fake_no_memory(1)
+        st = call(i + 1)
+        fake.fake_no_memory(0)
+        assert st in (0, w8.ERR_HIP), (name, st)
+        stopped += st != 0
+        if st:
+            assert "bad_alloc" in w8.last_error(), (name, w8.last_error())
+        assert call(i + 1) == 0, name
+    assert stopped >= 4
+    # refusals: their messages
+    fake.fake_no_memory(1)
+    st = [lib.w8a16_gemm(P, 64, P, P, P, n, m, n, k, 0), lib.w8a16_plan(0, 1, 128, 0, plan),
+          lib.w8a16_gemm_epilogue(P, k, P, P, P, n, m, n, k, None, 0)]
+    fake.fake_no_memory(0)
+    assert st == [w8.ERR_PITCH_TOO_SHORT, w8.ERR_M_ZERO, w8.ERR_NULL_PTR] and "null epilogue" in w8.last_error()
+
+
 def main():
     # (bound with symbols before the library's own dependencies)
     fake = ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_GLOBAL)

@@ -3,6 +3,7 @@
 // global symbols, so that the library binds to it.  Memory is malloc's,
 // launches run nothing and are recorded.
 //
+// fake_no_memory: C++ allocations of the calling thread fail while it is set.
 // fake_pause_us: sleep after each launch, so that other threads get between
 // one call's launches where nothing keeps them out.
 #include <chrono>
@@ -10,6 +11,7 @@
 #include <cstdint>
 #include <cstdlib>
 #include <mutex>
+#include <new>
 #include <thread>
 #include <vector>
 
@@ -34,12 +36,24 @@ uint64_t g_pause_us = 0;
 thread_local std::vector<Config> g_configs;
 thread_local int g_error = 0;
 thread_local uint64_t g_thread = 0;
+thread_local bool g_no_memory = false;
 uint8_t g_symbol[32];
 
 }  // namespace
 
+void *operator new(size_t n)
+{
+    void *p = g_no_memory ? nullptr : std::malloc(n ? n : 1);
+    if (!p)
+        throw std::bad_alloc();
+    return p;
+}
+void operator delete(void *p) noexcept { std::free(p); }
+void operator delete(void *p, size_t) noexcept { std::free(p); }
+
 extern "C" {
 
+void fake_no_memory(int on) { g_no_memory = on != 0; }
 void fake_pause_us(uint64_t us) { g_pause_us = us; }
 void fake_thread(uint64_t id) { g_thread = id; }
 uint64_t fake_launches() { return g_launches.size(); }

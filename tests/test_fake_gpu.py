@@ -34,3 +34,7 @@ def test_plans_are_the_calls(stand_in):
 
 def test_all_launches_or_none(stand_in):
     run(stand_in, "all_launches_or_none")
+
+
+def test_no_exception_leaves(stand_in):
+    run(stand_in, "no_exception_leaves")
