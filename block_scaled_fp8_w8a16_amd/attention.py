@@ -127,11 +127,14 @@ def _setup():
 
         from . import _raise_if, library
         lib = library()
+        again = "; run python -m block_scaled_fp8_w8a16_amd.build"
         try:
             from . import _binding
         except ImportError as e:
-            raise ImportError("_binding.so cannot be loaded (%s); run python -m "
-                              "block_scaled_fp8_w8a16_amd.build" % e) from e
+            raise ImportError("_binding.so cannot be loaded (%s)%s" % (e, again)) from e
+        if _binding.torch_version != str(torch.__version__):
+            raise ImportError("_binding.so is built for torch %s, this is %s%s" %
+                              (_binding.torch_version, torch.__version__, again))
         # what current_stream(device).cuda_stream returns, an order of
         # magnitude faster (0.06 against 1.8 us)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \

@@ -65,7 +65,8 @@ def _binding_cmd(out: str) -> list:
     base = os.path.dirname(torch.__file__)
     lib = os.path.join(base, "lib")
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-shared",
-            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I", INCLUDE,
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+            '-DW8A16_TORCH_VERSION="%s"' % torch.__version__, "-I", INCLUDE,
             "-isystem", os.path.join(base, "include"),
             "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
             "-I", sysconfig.get_paths()["include"], os.path.join(CSRC, "binding.cpp"), "-o", out,

@@ -585,4 +585,21 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding() { return PyModule_Create(&module); }
+// W8A16_TORCH_VERSION: of the torch it is compiled against, whose tensors it
+// reads by their layout.  What is checked here works in any CPython 3.
+PyMODINIT_FUNC PyInit__binding()
+{
+    const std::string python = std::to_string(PY_MAJOR_VERSION) + "." + std::to_string(PY_MINOR_VERSION);
+    const std::string here = Py_GetVersion();
+    if (here.compare(0, python.size() + 1, python + ".") != 0) {
+        PyErr_Format(PyExc_ImportError, "built for Python %s, this is %.8s", python.c_str(), here.c_str());
+        return nullptr;
+    }
+    PyObject *m = PyModule_Create(&module);
+    if (m && (PyModule_AddStringConstant(m, "torch_version", W8A16_TORCH_VERSION) < 0 ||
+              PyModule_AddStringConstant(m, "python_version", python.c_str()) < 0)) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
