@@ -268,9 +268,6 @@ def gemm(a, w, scale, c=None, *, plan_: Optional[Plan] = None, stream=None):
     return c
 
 
-ACTIVATIONS = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
-
-
 def gemm_epilogue(a, w, scale, c=None, *, bias=None, activation: Optional[str] = None, gate=None,
                   residual=None, out_dtype=None, stream=None):
     """C = residual + activation(A @ dequant(W)^T + bias) * gate, rounded once.

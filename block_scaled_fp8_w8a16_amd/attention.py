@@ -20,8 +20,6 @@ import ctypes
 from contextlib import nullcontext
 from typing import NamedTuple, Optional
 
-ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
-ROPE_ORDERS = {"split": 0, "turns": 1, "own": 2}
 ROPE_MAX_AXES = 4
 ROPE_SCALINGS = {None: 0, "linear": 1, "base": 2, "bands": 3}
 KV_BLOCK = 16
