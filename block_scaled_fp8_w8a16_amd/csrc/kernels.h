@@ -98,7 +98,8 @@ inline hipError_t allow_lds(const void *kern, uint32_t bytes, uint32_t limit,
 }
 
 hipError_t launch_stream(const GemmArgs &g, const w8a16_plan_t &p, hipStream_t stream);
-// The same with an epilogue, of the variants that w8a16_plan() chooses.
+// The same with an epilogue, of the variants that w8a16_plan() can choose for
+// some number of CUs.
 hipError_t launch_stream(const EpilogueArgs &g, const w8a16_plan_t &p, hipStream_t stream);
 hipError_t launch_ring(const EpilogueArgs &g, const w8a16_plan_t &p, hipStream_t stream);
 hipError_t launch_tile(const EpilogueArgs &g, const w8a16_plan_t &p, hipStream_t stream);

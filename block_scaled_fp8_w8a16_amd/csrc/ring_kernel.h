@@ -328,7 +328,11 @@ hipError_t launch_ring_n(const Args &g, const w8a16_plan_t &p, hipStream_t strea
     switch (p.depth) {
     case 2: return launch_ring_w<MB, NBW, SK, 2, A8>(g, p, stream);
     case 3: return launch_ring_w<MB, NBW, SK, 3, A8>(g, p, stream);
-    case 4: return launch_ring_w<MB, NBW, SK, 4, A8>(g, p, stream);
+    case 4:         // (nor stages of 8 steps: never a default plan's, all that an epilogue is built for)
+        if constexpr (std::is_same<Args, GemmArgs>::value)
+            return launch_ring_w<MB, NBW, SK, 4, A8>(g, p, stream);
+        else
+            return hipErrorInvalidValue;
     default: return hipErrorInvalidValue;
     }
 }
@@ -336,7 +340,6 @@ hipError_t launch_ring_n(const Args &g, const w8a16_plan_t &p, hipStream_t strea
 template <int MB, int NBW, bool A8, class Args>
 hipError_t launch_ring_s(const Args &g, const w8a16_plan_t &p, hipStream_t stream)
 {
-    // (default plans, all that an epilogue is built for, take 4 steps)
     if (p.stage_steps == 4)
         return launch_ring_n<MB, NBW, 4, A8>(g, p, stream);
     if constexpr (std::is_same<Args, GemmArgs>::value)

@@ -491,7 +491,11 @@ hipError_t launch_stream_any(const Args &g, const w8a16_plan_t &p, hipStream_t s
     case 201: return launch_stream_mn<2, 1>(g, p, stream);
     case 202: return launch_stream_mn<2, 2>(g, p, stream);
     case 204: return launch_stream_mn<2, 4>(g, p, stream);
-    case 208: return launch_stream_mn<2, 8>(g, p, stream);
+    case 208:       // (never a default plan's, all that an epilogue is built for)
+        if constexpr (!std::is_same<Args, EpilogueArgs>::value)
+            return launch_stream_mn<2, 8>(g, p, stream);
+        else
+            return hipErrorInvalidValue;
     case 401: return launch_stream_mn<4, 1>(g, p, stream);
     case 402: return launch_stream_mn<4, 2>(g, p, stream);
     default: return hipErrorInvalidValue;
