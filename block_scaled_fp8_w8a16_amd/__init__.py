@@ -260,8 +260,8 @@ def gemm(a, w, scale, c=None, *, plan_: Optional[Plan] = None, stream=None):
             raise ValueError("all operands must be GPU tensors")
     if stream is None:
         stream = torch.cuda.current_stream(a.device)
-    a_rs = a.stride(0) if m > 1 else max(a.stride(0), k)
-    c_rs = c.stride(0) if m > 1 else max(c.stride(0), n)
+    a_rs = a.stride(0) if m > 1 else k
+    c_rs = c.stride(0) if m > 1 else n
     st = gemm_raw(a.data_ptr(), a_rs, w.data_ptr(), scale.data_ptr(), c.data_ptr(),
                   c_rs, m, n, k, stream.cuda_stream, plan_)
     _raise_if(st)

@@ -465,7 +465,8 @@ PyObject *kv_attention(PyObject *const *o)
     return pair;
 }
 
-// Row stride of an [m, n] operand with unit column stride.
+// Row stride of an [m, n] operand with unit column stride (of a single row its
+// length, whatever the tensor says).
 uint32_t rows2(const char *name, const Tensor &t, int64_t m, int64_t n, bool f32, const Device &dev)
 {
     const bool type = t.scalar_type() == ScalarType::BFloat16 || (f32 && t.scalar_type() == ScalarType::Float);
@@ -476,7 +477,7 @@ uint32_t rows2(const char *name, const Tensor &t, int64_t m, int64_t n, bool f32
         throw Refused(std::string(name) + " needs a unit column stride");
     const int64_t rs = t.stride(0);
     require(m < 2 || (rs >= 0 && rs <= 0xffffffffll), "rows must be at most 2^32 - 1 elements apart");
-    return u32(m > 1 ? rs : rs < n ? n : rs);
+    return u32(m > 1 ? rs : n);
 }
 
 // gemm_epilogue(a, w, scale, c, bias, activation, gate, residual, out is float32 (None: not said), stream)
