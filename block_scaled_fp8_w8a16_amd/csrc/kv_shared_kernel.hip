@@ -20,11 +20,11 @@
 // the tile kernel's rate; in between both, and reading the own keys.
 // Measured, 32 query and 8 KV heads of 128 channels, one new token: 6
 // sequences of up to 333 own tokens behind 1984 shared ones 11.8 us (8.0 and
-// 3.8 for the join; as two launches and a join 20.5), 64 of up to 700 behind
-// 8192 31.3 (26 and 6.5; 41.0), reading 67 MB of HBM where 60 are the least;
-// without sharing 89.5.  24 sequences of 4 new tokens, 64 query heads, 101 own
-// tokens behind 30016: 124 to 128 (130; the products alone 78 at a library's
-// rate).  In the middle case a prefix workgroup takes 6 us to its first
+// 3.8 for the join; as two launches and a join 20.5), in one pass over
+// everything 12.0; 64 of up to 512 behind 8192 31.5 (26 and 6.5; 41.0),
+// reading 67 MB of HBM where 60 are the least, in one pass 85.5.  24 sequences
+// of 4 new tokens, 64 query heads, 101 own tokens behind 30016: 123 to 128
+// (130; the products alone 78 at a library's rate), in one pass 284.  In the middle case a prefix workgroup takes 6 us to its first
 // products, 15 for 8 tiles beside the own keys' workgroups and 2 for its
 // partial rows.  Tried there: the first tiles' loads before the rows' ranges
 // 31.2, partial rows through LDS, by whole rows, 31.4; in the last, eight

@@ -284,7 +284,12 @@ __device__ __forceinline__ void kv_tile(const Args &a, uint32_t group_id, uint8_
         }
     };
     // A block far from the row's others: its weights by themselves to l, its
-    // operands' sum to nothing.
+    // operands' sum to nothing.  (Some lanes of a wave may take this branch.
+    // In one form of the masked tiles below the compiler moved the 16
+    // accumulators of a channel tile to other registers right behind it, before
+    // it had put the other lanes back in EXEC, and those lost them: the wrong
+    // copies stand in that build's assembly, in no kernel's here, and not
+    // without -amdgpu-mfma-vgpr-form.)
     auto far = [&](const f32x16_t &s, float c, float &shift) {
         shift = kNegInf;
 #pragma unroll

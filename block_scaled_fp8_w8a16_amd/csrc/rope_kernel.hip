@@ -15,11 +15,14 @@
 // Several axes: a thread loads its token's positions (up to four) and takes
 // the pairs of one axis as one piece of the table where every thread's pairs
 // lie within an axis, else each by itself.  Four heads a thread share that
-// too, from 256 threads per CU on (us, one head and four: 2048 tokens of 16
-// heads of 80 channels 5.0 and 5.0, 4097 8.4 and 7.9; 512 tokens of 32 heads
-// of 128 3.5 and 4.2, 1024 6.0 and 6.2, by turns 7.4 and 7.0).  4097 tokens of
-// 16 heads of 80 FP16 channels on two axes, backwards: 7.2 us, 3.1 TB/s of 22
-// MB (launch, then positions, table and row one after the other).
+// too, from 256 threads per CU on (us a call, one head and four: 4097 tokens of
+// 16 heads of 80 FP16 channels, pairs of two axes in an item 7.8 and 7.2,
+// backwards 7.4 and 7.2; 32 heads of 128, by turns, 1024 tokens 6.2 and 5.8,
+// 4096 15.8 and 12.9, 16384 53.3 and 48.2; of one axis 1024 tokens 5.2 and 5.2
+// to 5.4, 2048 7.95 and 8.4, 4096 13.1 and 12.0, 8192 23.8 and 24.7, 16384 44.1
+// and 44.5, so that what the one gains at a size it loses at the next).  The
+// 4097 backwards are 3.1 TB/s of 22 MB (launch, then positions, table and row
+// one after the other).
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -36,7 +36,8 @@
  *
  * Threads: calls may come from several threads, on one stream too; the
  * launches of a call that use a workspace are enqueued with none of another
- * call's that uses it between them.
+ * call's that uses it between them.  hipStreamPerThread is a stream of each
+ * thread's but has one workspace: calls on it that use one must not overlap.
  *
  * Alignment and aliasing: A, W, S and C must be 16-byte aligned (torch
  * allocations are).  C must not overlap A, W or S.  c_row_stride may be any
