@@ -132,3 +132,30 @@ def test_gelu_of_special_values(w8, act):
     x = y[fin].abs().clamp(max=20)
     tol = want[fin].abs() * U * (40 + (2 * x * x if act == "gelu" else 18 * (0.8 * x + 0.036 * x ** 3))) + 2.0 ** -50 * x
     assert ((got - want)[fin].abs() <= tol + 2.0 ** -122).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(40, 2304, 8192), (130, 4099, 4096), (65, 4152, 8192)], ids=str)
+def test_captured_sums_of_tile_splits(w8, shape):
+    """Two launches through the stream's workspace, replayed with eager calls
+    of the same stream in between."""
+    m, n, k = shape
+    assert w8.plan(m, n, k).kernel == w8.KERNEL_TILE and w8.plan(m, n, k).splits > 1
+    a, w, scale, s = big_operands(m, n, k, 3)
+    x, bias = torch.randn(m, n, device="cuda").to(BF16), torch.randn(n, device="cuda")
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):       # workspaces grow before the capture
+        w8.gemm_epilogue(a, w, scale, bias=bias, residual=x)
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            y = w8.gemm_epilogue(a, w, scale, bias=bias, residual=x)
+        for _ in range(4):
+            x.copy_(torch.randn(m, n, device="cuda"))
+            y.zero_()
+            graph.replay()
+            eager = w8.gemm_epilogue(a, w, scale, bias=bias, residual=x)
+            stream.synchronize()
+            assert torch.equal(y, eager)
+            check(y, s, bias, None, None, x)
